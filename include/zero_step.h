@@ -98,6 +98,7 @@ typedef enum {
  * block left with copies in flight into its shared memory, so treat the CUDA
  * context as suspect (finish or reset it) rather than continue training. */
 #define ZERO_DEV_DRAIN_FAILED 8
+#define ZERO_DEV_BAD_TOKEN 16      /* a token id or target at or past the table's rows */
 
 /* Flags for zero_step / zero_rs_avg. */
 #define ZERO_FLAG_CHECK_FINITE 1   /* set ZERO_DEV_NONFINITE when g is non-finite */
@@ -588,6 +589,131 @@ zero_status zero_ckpt_job_wait(zero_ckpt_job* job);
 zero_status zero_ckpt_load(const zero_plan_t* plan, const char* dir, uint16_t* const* dev_params,
                            int32_t n_params, float* dev_master, float* dev_m, float* dev_v,
                            int64_t* step_out, zero_adamw_hparams* hp_out, void* stream);
+
+/* ----------------------------------------------------------------------
+ * Language-model operators around the step: what fills the gradient buffers at
+ * both ends of a tied embedding table (a GPT-2-small- or Llama-3.2-1B-shaped
+ * set's largest tensor), and the norm between them.  They need no plan:
+ * `table`, `weight` and their gradients point into a replica and a gradient
+ * buffer at the tensor's offset (plan->tensor_offsets).
+ *
+ * Beyond the conventions at the top of this file:
+ *   - T tokens (0 <= T), V table rows (1 <= V), D columns (a multiple of 8).
+ *     Matrices are row-major, their columns contiguous; `x_ld` is the stride
+ *     between the rows of x in elements, a multiple of 8 and at least D.  Tables
+ *     and gradients of tables are contiguous.  T, V below 2^31 - 1024,
+ *     D <= 65536 (ZERO_NORM_MAX_WIDTH for the norm), else ZERO_ERR_SIZE.
+ *   - Token ids are 4- or 8-byte signed integers (token_bytes).  A negative id
+ *     is "no token": its row of the lookup is zero, it has no loss and no
+ *     gradient.  An id at or past V counts as no token too and sets
+ *     ZERO_DEV_BAD_TOKEN in dev_status (optional).
+ *   - Sums, softmax statistics and norms are fp32; each bf16 output is rounded
+ *     once (to nearest even) from fp32.  Every sum has an order that depends on
+ *     the arguments (and, for zero_embed_grad, the ids) alone: a call repeated
+ *     gives the same bits.
+ *   - T = 0 is allowed: outputs with one row per token are not touched, and
+ *     the gradients of tables and weights become zero (or keep what they hold,
+ *     with accumulate).
+ *   - scratch: scratch_bytes of device memory, at least what the matching
+ *     *_scratch_bytes call returns (-1 for sizes it does not take), 16-byte
+ *     aligned, not shared by calls that may overlap in time.  Its contents
+ *     need no preparation.
+ * ---------------------------------------------------------------------- */
+
+#define ZERO_NORM_BLOCK 128        /* elements of a row that share a scale of the checkpoint */
+#define ZERO_NORM_MAX_WIDTH 16384
+
+/*
+ * Embedding lookup with scaling: out[t, :] = bf16(scale * table[tokens[t], :]),
+ * or zeros where tokens[t] is no token.
+ */
+zero_status zero_embed(const uint16_t* table, int64_t V, int32_t D, const void* tokens,
+                       int32_t token_bytes, int64_t T, float scale, uint16_t* out, int64_t out_ld,
+                       int32_t* dev_status, void* stream);
+
+int64_t zero_embed_grad_scratch_bytes(int64_t T, int64_t V, int32_t D);
+
+/*
+ * Its gradient: grad[v, :] = bf16(scale * sum of dy[t, :] over the t with
+ * tokens[t] == v), every row of the table being written; with accumulate = 1,
+ * bf16(grad[v, :] + that) for the rows that are met, the others untouched (a
+ * tied table's gradient, after zero_xent_grad).  The tokens are sorted first,
+ * and each row's terms are added in ascending t.
+ */
+zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const void* tokens,
+                            int32_t token_bytes, int64_t T, float scale, int64_t V, int32_t D,
+                            uint16_t* grad, int32_t accumulate, void* scratch,
+                            int64_t scratch_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and an 8-bit checkpoint.
+ *   s = x + residual (fp32; residual may be NULL), rstd[t] = 1/sqrt(mean(s^2) + eps)
+ *   y = bf16(s * rstd * weight);  sum = bf16(s) (may be NULL)
+ *   per row and block b of ZERO_NORM_BLOCK columns, with amax = max |s|:
+ *   scales[t, b] = amax / 127, codes[t, i] = rint(s * (127 / amax));
+ *   both zero where amax < 1e-30; codes 0 and scale NaN where amax is Inf or NaN.
+ * codes: T*D int8; scales: T * ceil(D / ZERO_NORM_BLOCK) floats; both NULL keeps no
+ * checkpoint.  rstd: T floats.
+ */
+zero_status zero_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual,
+                      int64_t residual_ld, const uint16_t* weight, int64_t T, int32_t D, float eps,
+                      uint16_t* y, int64_t y_ld, uint16_t* sum, int64_t sum_ld, int8_t* codes,
+                      float* scales, float* rstd, void* stream);
+
+/*
+ * The normalised activation again, from the checkpoint, for the backward pass
+ * of what consumed it: y = bf16(codes * scales * rstd * weight).
+ */
+zero_status zero_norm_replay(const int8_t* codes, const float* scales, const float* rstd,
+                             const uint16_t* weight, int64_t T, int32_t D, uint16_t* y,
+                             int64_t y_ld, void* stream);
+
+int64_t zero_norm_grad_scratch_bytes(int64_t T, int32_t D);
+
+/*
+ * The norm's gradient from the checkpoint: with xhat = codes * scales * rstd,
+ *   dx = bf16(rstd * (dy*weight - xhat * mean(dy*weight*xhat)) + dsum),
+ *   dweight = bf16(sum over t of dy * xhat).
+ * dsum: the gradient that reaches `sum` by itself (may be NULL).  dx is the
+ * gradient of x and of the residual alike.
+ */
+zero_status zero_norm_grad(const uint16_t* dy, int64_t dy_ld, const uint16_t* dsum,
+                           int64_t dsum_ld, const int8_t* codes, const float* scales,
+                           const float* rstd, const uint16_t* weight, int64_t T, int32_t D,
+                           uint16_t* dx, int64_t dx_ld, uint16_t* dweight, void* scratch,
+                           int64_t scratch_bytes, void* stream);
+
+int64_t zero_xent_scratch_bytes(int64_t T, int64_t V, int32_t D);
+
+/*
+ * Softmax cross entropy over the vocabulary, the logits h table^T never being
+ * stored: lse[t] = log(sum over v of exp(logit[t, v])) for every row, and
+ * loss[t] = lse[t] - logit[t, targets[t]], 0 where the target is no token.
+ * flags: 0 or ZERO_FLAG_DEBUG_EXPIRE_WAITS (as in zero_step: every bounded
+ * device wait gives up at once, for tests; needs dev_status).  A wait that runs
+ * out sets ZERO_DEV_TIMEOUT and leaves the outputs unspecified.
+ */
+zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t* table, int64_t V, int32_t D,
+                      const void* targets, int32_t target_bytes, int64_t T, float* loss,
+                      float* lse, void* scratch, int64_t scratch_bytes, int32_t flags,
+                      int32_t* dev_status, void* stream);
+
+/* piece: as for zero_xent_grad. */
+int64_t zero_xent_grad_scratch_bytes(int64_t T, int64_t V, int32_t D, int64_t piece);
+
+/*
+ * Its gradients, from lse (zero_xent's) and the upstream gradient dloss[t] of
+ * each token's loss: with P = bf16((exp(logit - lse) - [v == target]) * dloss),
+ * zero in the rows of no token whatever h and dloss hold there,
+ *   dh = bf16(P table),  dtable = bf16(P^T h)   (every row written).
+ * The vocabulary is taken `piece` rows at a time (a multiple of 256; 0: chosen
+ * so that P takes at most 512 MiB); a larger piece needs more scratch.
+ */
+zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uint16_t* table, int64_t V,
+                           int32_t D, const void* targets, int32_t target_bytes, int64_t T,
+                           const float* lse, const float* dloss, uint16_t* dh, int64_t dh_ld,
+                           uint16_t* dtable, int64_t piece, void* scratch, int64_t scratch_bytes,
+                           int32_t flags, int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -18,3 +18,18 @@ from .binding import (  # noqa: F401
     ZERO_DEV_DRAIN_FAILED, ZERO_COMP_FP16, ZERO_COMP_INT8, ZERO_COMP_SIGN, ZERO_DEV_NONFINITE, ZERO_FLAG_CHECK_FINITE, ZERO_VARIANT_FUSED,
     ZERO_VARIANT_STAGED, ZERO_VARIANT_FUSED_TMA, ZERO_DEV_TIMEOUT, ZERO_FLAG_DEBUG_EXPIRE_WAITS,
 )
+from .binding import ZERO_DEV_BAD_TOKEN, ZERO_NORM_BLOCK, ZERO_NORM_MAX_WIDTH  # noqa: F401
+
+# the operators of lm.py, which needs torch at import; the steps above do not
+_LM = ("zero_embed", "zero_embed_grad", "zero_embed_grad_scratch_bytes", "zero_norm",
+       "zero_norm_grad", "zero_norm_grad_scratch_bytes", "zero_norm_replay", "zero_xent",
+       "zero_xent_grad", "zero_xent_grad_scratch_bytes", "zero_xent_scratch_bytes")
+
+
+def __getattr__(name):
+    if name in _LM:
+        from . import lm
+        for k in _LM:
+            globals()[k] = getattr(lm, k)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -35,6 +35,9 @@ ZERO_VARIANT_STAGED = 1
 ZERO_VARIANT_FUSED_TMA = 2
 ZERO_DEV_TIMEOUT = 2
 ZERO_DEV_DRAIN_FAILED = 8
+ZERO_DEV_BAD_TOKEN = 16
+ZERO_NORM_BLOCK = 128
+ZERO_NORM_MAX_WIDTH = 16384
 ZERO_FLAG_DEBUG_EXPIRE_WAITS = 1 << 30
 ZERO_COMP_FP16 = 1
 ZERO_COMP_INT8 = 2
@@ -51,7 +54,10 @@ EXPORTED = ("zero_abi_version", "zero_status_string", "zero_plan_create", "zero_
             "zero_ckpt_read_host", "zero_ckpt_save_async", "zero_ckpt_job_wait",
             "zero_ckpt_load", "zero_step_compressed", "zero_check_replicas", "zero_step_onebit",
             "zero3_rs_unit", "zero3_update", "zero_get_device_status",
-            "zero3_gather_units")
+            "zero3_gather_units", "zero_embed", "zero_embed_grad",
+            "zero_embed_grad_scratch_bytes", "zero_norm", "zero_norm_replay", "zero_norm_grad",
+            "zero_norm_grad_scratch_bytes", "zero_xent", "zero_xent_scratch_bytes",
+            "zero_xent_grad", "zero_xent_grad_scratch_bytes")
 
 
 class ZeroError(RuntimeError):
@@ -159,6 +165,27 @@ def lib():
         L.zero_get_device_status.restype = ctypes.c_int
         L.zero3_gather_units.argtypes = [P(zero_plan_t), vp, P(zero_gather_unit), i32, vp]
         L.zero3_gather_units.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        L.zero_embed.argtypes = [vp, i64, i32, vp, i32, i64, f32, vp, i64, vp, vp]
+        L.zero_embed_grad_scratch_bytes.argtypes = [i64, i64, i32]
+        L.zero_embed_grad.argtypes = [vp, i64, vp, i32, i64, f32, i64, i32, vp, i32, vp, i64, vp,
+                                      vp]
+        L.zero_norm.argtypes = [vp, i64, vp, i64, vp, i64, i32, f32, vp, i64, vp, i64, vp, vp, vp,
+                                vp]
+        L.zero_norm_replay.argtypes = [vp, vp, vp, vp, i64, i32, vp, i64, vp]
+        L.zero_norm_grad_scratch_bytes.argtypes = [i64, i32]
+        L.zero_norm_grad.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, i32, vp, i64, vp, vp,
+                                     i64, vp]
+        L.zero_xent_scratch_bytes.argtypes = [i64, i64, i32]
+        L.zero_xent.argtypes = [vp, i64, vp, i64, i32, vp, i32, i64, vp, vp, vp, i64, i32, vp, vp]
+        L.zero_xent_grad_scratch_bytes.argtypes = [i64, i64, i32, i64]
+        L.zero_xent_grad.argtypes = [vp, i64, vp, i64, i32, vp, i32, i64, vp, vp, vp, i64, vp, i64,
+                                     vp, i64, i32, vp, vp]
+        for name in ("zero_embed", "zero_embed_grad", "zero_norm", "zero_norm_replay",
+                     "zero_norm_grad", "zero_xent", "zero_xent_grad"):
+            getattr(L, name).restype = ctypes.c_int
+        for name in ("zero_embed_grad", "zero_norm_grad", "zero_xent", "zero_xent_grad"):
+            getattr(L, name + "_scratch_bytes").restype = i64
         _lib = L
     return _lib
 

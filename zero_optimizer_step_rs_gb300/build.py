@@ -1,8 +1,8 @@
 """Build the in-tree C-ABI library libzero_step.so for sm_103a.
 
-Two translation units (the CUDA kernels + entry points, and the host-only
-plan code) are compiled in parallel by nvcc and linked into one shared
-library with the CUDA runtime linked statically, so the library needs no
+The translation units (the step's CUDA kernels and entry points, the
+language-model operators' three, and the host-only plan and checkpoint code)
+are compiled in parallel by nvcc and linked into one shared library with the CUDA runtime linked statically, so the library needs no
 libcudart at load time and can be loaded (and its host-only entry points
 called) on a machine without a GPU.
 """
@@ -22,7 +22,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 SOURCES = [os.path.join(CSRC, "zero_step.cu"), os.path.join(CSRC, "plan.cpp"),
-           os.path.join(CSRC, "ckpt.cpp")]
+           os.path.join(CSRC, "ckpt.cpp"), os.path.join(CSRC, "lm_embed.cu"),
+           os.path.join(CSRC, "lm_norm.cu"), os.path.join(CSRC, "lm_xent.cu")]
 HEADERS = [os.path.join(INCLUDE, "zero_step.h")] + sorted(
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh"))
 

@@ -1,0 +1,529 @@
+// lm_norm.cu - root-mean-square norm of (activation + residual) that keeps its
+// input as an 8-bit checkpoint, the normalised activation rebuilt from the
+// checkpoint, and the gradient computed from it (declared in
+// include/zero_step.h).
+//
+//   s = x + r                      (fp32; the new residual stream is bf16(s))
+//   rstd = 1 / sqrt(mean(s^2) + eps),   y = bf16(s * rstd * w)
+//   checkpoint, per 128 elements of a row: amax = max |s|, scale = amax / 127,
+//   code = rint(s * (127 / amax)) in [-127, 127]
+// and, with xhat = code * scale * rstd and u = dy * w:
+//   replay: y' = bf16(xhat * w)
+//   dx = bf16(rstd * (u - xhat * mean(u * xhat)) + dsum),  dw = sum_t dy * xhat
+//
+// Backward needs neither s nor y in 16 bits: the checkpoint is 1 byte an
+// element and 4 bytes per 128, and every value that the backward pass takes
+// from it is made in registers.  All of it is bound by HBM traffic: forward
+// 2+2 bytes an element read and 2+2+1 written, replay 1 and 2, gradient 2+2+1
+// and 2.
+#include "lm_common.cuh"
+
+namespace {
+
+using namespace lm;
+
+constexpr int kBlock = ZERO_NORM_BLOCK;          // elements that share a scale
+constexpr int kLanesPerBlock = kBlock / 8;       // 16 lanes of 8 elements
+constexpr float kTiny = 1e-30f;                  // 127 / amax stays finite from here up
+
+struct NormArgs {
+    const uint16_t* x;
+    const uint16_t* res;             // may be null
+    const uint16_t* w;
+    uint16_t* y;
+    uint16_t* sum;                   // may be null
+    int8_t* codes;                   // may be null (with scales): no checkpoint
+    float* scales;
+    float* rstd;
+    int64_t T, x_ld, res_ld, y_ld, sum_ld;
+    int32_t D;
+    float eps;
+};
+
+// The sum of one value over the TPR threads of a row: a warp by shuffles, more
+// through shared memory.  `slot` alternates from row to row, so that one
+// barrier a row is enough.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, float (*slots)[32], int slot)
+{
+    x = warp_sum(x);
+    if constexpr (TPR > 32) {
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) slots[slot][warp] = x;
+        __syncthreads();
+        x = 0.0f;
+#pragma unroll
+        for (int k = 0; k < TPR / 32; ++k) x += slots[slot][k];
+    }
+    return x;
+}
+
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
+{
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 |
+           (uint32_t)(d & 255) << 24;
+}
+
+__device__ __forceinline__ void unpack_codes(const uint2& q, float (&f)[8])
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        f[k] = (float)(int8_t)(q.x >> (8 * k));
+        f[4 + k] = (float)(int8_t)(q.y >> (8 * k));
+    }
+}
+
+// TPR threads take a row, each NV vectors of 8 elements; blocks of at least
+// 128 threads, so a block holds several rows where a row is one warp's.
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_norm(const __grid_constant__ NormArgs a)
+{
+    constexpr int THREADS = TPR > 128 ? TPR : 128;
+    pdl_enter();
+    __shared__ float slots[2][32];
+    const int64_t t = (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
+    if (t >= a.T) return;                                  // whole warps; whole blocks if TPR > 32
+    const int lane = threadIdx.x % TPR;
+    const int nv = a.D >> 3;
+    const uint16_t* x = a.x + t * a.x_ld;
+    const uint16_t* r = a.res ? a.res + t * a.res_ld : nullptr;
+
+    float f[NV][8];
+    {
+        uint4 v[NV], u[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = lane + k * TPR;
+            v[k] = u[k] = make_uint4(0, 0, 0, 0);
+            if (c < nv) {
+                v[k] = ld16_stream(x + c * 8);
+                if (r) u[k] = ld16_stream(r + c * 8);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            float g[8];
+            bf_unpack8(v[k], f[k]);
+            bf_unpack8(u[k], g);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[k][q] += g[q];
+        }
+    }
+    float ss = 0.0f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int q = 0; q < 8; ++q) ss = fmaf(f[k][q], f[k][q], ss);
+    ss = row_sum<TPR>(ss, slots, 0);
+    const float rstd = 1.0f / sqrtf(ss / (float)a.D + a.eps);
+    if (lane == 0) a.rstd[t] = rstd;
+
+    const int blocks = (a.D + kBlock - 1) / kBlock;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = lane + k * TPR;
+        if (a.codes) {
+            // 16 consecutive lanes hold a block; as integers, so that Inf and NaN win
+            uint32_t m = 0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(f[k][q]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = kLanesPerBlock / 2; o > 0; o >>= 1)
+                m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            const float amax = __uint_as_float(m);
+            float scale = 0.0f, inv = 0.0f;
+            if (m >= 0x7F800000u) {
+                scale = __uint_as_float(0x7FC00000u);      // the block stands for NaN
+            } else if (amax >= kTiny) {
+                scale = __fdiv_rn(amax, 127.0f);
+                inv = __fdiv_rn(127.0f, amax);
+            }
+            if (c < nv) {
+                int q8[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) q8[q] = __float2int_rn(__fmul_rn(f[k][q], inv));
+                __stcs(reinterpret_cast<uint2*>(a.codes + t * a.D + c * 8),
+                       make_uint2(pack4(q8[0], q8[1], q8[2], q8[3]),
+                                  pack4(q8[4], q8[5], q8[6], q8[7])));
+                if (c % kLanesPerBlock == 0) a.scales[t * blocks + c / kLanesPerBlock] = scale;
+            }
+        }
+        if (c < nv) {
+            if (a.sum) st16_stream(a.sum + t * a.sum_ld + c * 8, bf_pack8(f[k]));
+            float w[8];
+            bf_unpack8(ld16(a.w + c * 8), w);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] *= f[k][q] * rstd;
+            st16_stream(a.y + t * a.y_ld + c * 8, bf_pack8(w));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- replay --
+
+struct ReplayArgs {
+    const int8_t* codes;
+    const float* scales;
+    const float* rstd;
+    const uint16_t* w;
+    uint16_t* y;
+    int64_t T, y_ld;
+    int32_t D;
+};
+
+constexpr int kReplayThreads = 256;
+constexpr int kReplayVecs = 4;
+
+// A warp takes a row, 4 vectors of each lane in flight.
+__global__ void __launch_bounds__(kReplayThreads) k_replay(const __grid_constant__ ReplayArgs a)
+{
+    pdl_enter();
+    const int64_t t = ((int64_t)blockIdx.x * kReplayThreads + threadIdx.x) >> 5;
+    if (t >= a.T) return;
+    const int lane = threadIdx.x & 31, nv = a.D >> 3;
+    const float rstd = a.rstd[t];
+    const float* scales = a.scales + t * ((a.D + kBlock - 1) / kBlock);
+    const int8_t* codes = a.codes + t * a.D;
+    uint16_t* y = a.y + t * a.y_ld;
+    for (int base = lane; base < nv; base += 32 * kReplayVecs) {
+        uint2 q[kReplayVecs];
+        float s[kReplayVecs];
+#pragma unroll
+        for (int k = 0; k < kReplayVecs; ++k) {
+            const int c = base + k * 32;
+            if (c < nv) {
+                q[k] = __ldcs(reinterpret_cast<const uint2*>(codes + c * 8));
+                s[k] = scales[c / kLanesPerBlock];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kReplayVecs; ++k) {
+            const int c = base + k * 32;
+            if (c >= nv) break;
+            float f[8], w[8];
+            unpack_codes(q[k], f);
+            bf_unpack8(ld16(a.w + c * 8), w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = f[j] * s[k] * rstd * w[j];
+            st16_stream(y + c * 8, bf_pack8(f));
+        }
+    }
+}
+
+// -------------------------------------------------------------- gradient --
+
+struct NormGradArgs {
+    const uint16_t* dy;
+    const uint16_t* dsum;            // may be null
+    const int8_t* codes;
+    const float* scales;
+    const float* rstd;
+    const uint16_t* w;
+    uint16_t* dx;
+    uint16_t* dw;
+    float* parts;                    // [blocks][D]
+    int64_t T, dy_ld, dsum_ld, dx_ld;
+    int32_t D, blocks;
+};
+
+// As k_norm, but a row's threads walk over many rows and keep the sums of dw
+// in registers; a block's row groups are added in order at its end.
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_norm_grad(const __grid_constant__ NormGradArgs a)
+{
+    constexpr int THREADS = TPR > 128 ? TPR : 128;
+    constexpr int GROUPS = THREADS / TPR;
+    pdl_enter();
+    __shared__ float slots[2][32];
+    const int group = threadIdx.x / TPR, lane = threadIdx.x % TPR;
+    const int nv = a.D >> 3;
+    const int nb = (a.D + kBlock - 1) / kBlock;
+    float dw[NV][8] = {};
+    int slot = 0;
+    // every group of a block makes the same number of rounds (barriers)
+    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
+        const int64_t t = t0 + group;
+        const bool in = t < a.T;
+        uint4 vd[NV], vs[NV];
+        uint2 vq[NV];
+        float sc[NV];
+        const float rstd = in ? a.rstd[t] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = lane + k * TPR;
+            vd[k] = vs[k] = make_uint4(0, 0, 0, 0);
+            vq[k] = make_uint2(0, 0);
+            sc[k] = 0.0f;
+            if (in && c < nv) {
+                vd[k] = ld16_stream(a.dy + t * a.dy_ld + c * 8);
+                vq[k] = __ldcs(reinterpret_cast<const uint2*>(a.codes + t * a.D + c * 8));
+                sc[k] = a.scales[t * nb + c / kLanesPerBlock];
+                if (a.dsum) vs[k] = ld16_stream(a.dsum + t * a.dsum_ld + c * 8);
+            }
+        }
+        float inner = 0.0f;
+        float xh[NV][8], u[NV][8];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = lane + k * TPR;
+            float w[8] = {};
+            if (c < nv) bf_unpack8(ld16(a.w + c * 8), w);
+            unpack_codes(vq[k], xh[k]);
+            bf_unpack8(vd[k], u[k]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                xh[k][q] *= sc[k] * rstd;
+                dw[k][q] = fmaf(u[k][q], xh[k][q], dw[k][q]);
+                u[k][q] *= w[q];
+                inner = fmaf(u[k][q], xh[k][q], inner);
+            }
+        }
+        inner = row_sum<TPR>(inner, slots, slot) / (float)a.D;
+        slot ^= 1;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = lane + k * TPR;
+            if (in && c < nv) {
+                float s[8];
+                bf_unpack8(vs[k], s);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) s[q] += rstd * (u[k][q] - xh[k][q] * inner);
+                st16_stream(a.dx + t * a.dx_ld + c * 8, bf_pack8(s));
+            }
+        }
+    }
+    float* part = a.parts + (int64_t)blockIdx.x * a.D;
+    if constexpr (GROUPS == 1) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = lane + k * TPR;
+            if (c < nv)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) part[c * 8 + q] = dw[k][q];
+        }
+    } else {
+        __shared__ float all[GROUPS][TPR * NV * 8];
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) all[group][(lane + k * TPR) * 8 + q] = dw[k][q];
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.D; i += THREADS) {
+            float s = all[0][i];
+#pragma unroll
+            for (int g = 1; g < GROUPS; ++g) s += all[g][i];
+            part[i] = s;
+        }
+    }
+}
+
+// dw = the blocks' parts, added in an order that depends on their number only:
+// 32 columns a block, 128 shares of the rows, then the shares in order.
+constexpr int kJoinThreads = 1024;
+constexpr int kJoinCols = 32;
+constexpr int kJoinShares = kJoinThreads / (kJoinCols / 4);
+
+__global__ void __launch_bounds__(kJoinThreads) k_norm_join(const __grid_constant__ NormGradArgs a)
+{
+    pdl_enter();
+    __shared__ float4 share[kJoinShares][kJoinCols / 4];
+    const int cv = threadIdx.x % (kJoinCols / 4), sh = threadIdx.x / (kJoinCols / 4);
+    const int col = blockIdx.x * kJoinCols + cv * 4;
+    float4 s = make_float4(0, 0, 0, 0);
+    if (col < a.D)
+        for (int r = sh; r < a.blocks; r += kJoinShares) {
+            const float4 x =
+                __ldcs(reinterpret_cast<const float4*>(a.parts + (int64_t)r * a.D + col));
+            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
+        }
+    share[sh][cv] = s;
+    __syncthreads();
+#pragma unroll
+    for (int o = kJoinShares / 2; o > 0; o >>= 1) {
+        if (sh < o) {
+            float4 p = share[sh][cv];
+            const float4 q = share[sh + o][cv];
+            p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
+            share[sh][cv] = p;
+        }
+        __syncthreads();
+    }
+    if (sh == 0 && col < a.D) {
+        const float4 p = share[0][cv];
+        *reinterpret_cast<uint2*>(a.dw + col) = make_uint2(bf_pack(p.x, p.y), bf_pack(p.z, p.w));
+    }
+}
+
+int grad_blocks(int64_t T)
+{
+    return (int)std::min<int64_t>(T, 1216);          // at most 8 for each of 152 SMs
+}
+
+}  // namespace
+
+// The widths each form takes: a row of up to 512 columns is one warp's, wider
+// ones are shared by 128 to 512 threads with two or four vectors each.
+#define NORM_FORMS(F)                  \
+    if (D <= 256) return F(32, 1);     \
+    if (D <= 512) return F(32, 2);     \
+    if (D <= 1024) return F(128, 1);   \
+    if (D <= 2048) return F(128, 2);   \
+    if (D <= 4096) return F(256, 2);   \
+    if (D <= 8192) return F(512, 2);   \
+    return F(512, 4)
+
+extern "C" zero_status zero_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual,
+                                 int64_t residual_ld, const uint16_t* weight, int64_t T, int32_t D,
+                                 float eps, uint16_t* y, int64_t y_ld, uint16_t* sum,
+                                 int64_t sum_ld, int8_t* codes, float* scales, float* rstd,
+                                 void* stream)
+{
+    LM_CHECK(check_sizes(T, 1, D, ZERO_NORM_MAX_WIDTH));
+    LM_CHECK(check_ld(x_ld, D));
+    LM_CHECK(check_ld(y_ld, D));
+    if (residual) LM_CHECK(check_ld(residual_ld, D));
+    if (sum) LM_CHECK(check_ld(sum_ld, D));
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return ZERO_ERR_INVALID_ARG;
+    if (T == 0) return ZERO_OK;
+    LM_CHECK(check_ptr(x));
+    if (residual) LM_CHECK(check_ptr(residual));
+    LM_CHECK(check_ptr(weight));
+    LM_CHECK(check_ptr(y));
+    if (sum) LM_CHECK(check_ptr(sum));
+    LM_CHECK(check_ptr(rstd));
+    if (codes || scales) {
+        LM_CHECK(check_ptr(codes));
+        LM_CHECK(check_ptr(scales));
+    }
+    const int64_t nb = (D + kBlock - 1) / kBlock;
+    Spans sp;
+    sp.rows(x, T, x_ld, D, 2, false);
+    if (residual) sp.rows(residual, T, residual_ld, D, 2, false);
+    sp.add(weight, 2 * D, false);
+    sp.rows(y, T, y_ld, D, 2, true);
+    if (sum) sp.rows(sum, T, sum_ld, D, 2, true);
+    if (codes) sp.add(codes, T * D, true);
+    if (codes) sp.add(scales, 4 * T * nb, true);
+    sp.add(rstd, 4 * T, true);
+    LM_CHECK(sp.check());
+
+    NormArgs a{};
+    a.x = x;
+    a.res = residual;
+    a.w = weight;
+    a.y = y;
+    a.sum = sum;
+    a.codes = codes;
+    a.scales = scales;
+    a.rstd = rstd;
+    a.T = T;
+    a.x_ld = x_ld;
+    a.res_ld = residual_ld;
+    a.y_ld = y_ld;
+    a.sum_ld = sum_ld;
+    a.D = D;
+    a.eps = eps;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+#define NORM_GO(tpr, nv)                                                                       \
+    status_of(launch(k_norm<tpr, nv>,                                                          \
+                     dim3((unsigned)((T + (tpr > 128 ? 1 : 128 / tpr) - 1) /                   \
+                                     (tpr > 128 ? 1 : 128 / tpr))),                            \
+                     tpr > 128 ? tpr : 128, 0, 1, st, a))
+    NORM_FORMS(NORM_GO);
+#undef NORM_GO
+}
+
+extern "C" zero_status zero_norm_replay(const int8_t* codes, const float* scales,
+                                        const float* rstd, const uint16_t* weight, int64_t T,
+                                        int32_t D, uint16_t* y, int64_t y_ld, void* stream)
+{
+    LM_CHECK(check_sizes(T, 1, D, ZERO_NORM_MAX_WIDTH));
+    LM_CHECK(check_ld(y_ld, D));
+    if (T == 0) return ZERO_OK;
+    LM_CHECK(check_ptr(codes));
+    LM_CHECK(check_ptr(scales));
+    LM_CHECK(check_ptr(rstd));
+    LM_CHECK(check_ptr(weight));
+    LM_CHECK(check_ptr(y));
+    Spans sp;
+    sp.add(codes, T * D, false);
+    sp.add(scales, 4 * T * ((D + kBlock - 1) / kBlock), false);
+    sp.add(rstd, 4 * T, false);
+    sp.add(weight, 2 * D, false);
+    sp.rows(y, T, y_ld, D, 2, true);
+    LM_CHECK(sp.check());
+    const ReplayArgs a{codes, scales, rstd, weight, y, T, y_ld, D};
+    const int per = kReplayThreads / 32;
+    return status_of(launch(k_replay, dim3((unsigned)((T + per - 1) / per)), kReplayThreads, 0, 1,
+                            static_cast<cudaStream_t>(stream), a));
+}
+
+extern "C" int64_t zero_norm_grad_scratch_bytes(int64_t T, int32_t D)
+{
+    if (check_sizes(T, 1, D, ZERO_NORM_MAX_WIDTH) != ZERO_OK) return -1;
+    return up(4 * (int64_t)grad_blocks(T) * D, 256);
+}
+
+extern "C" zero_status zero_norm_grad(const uint16_t* dy, int64_t dy_ld, const uint16_t* dsum,
+                                      int64_t dsum_ld, const int8_t* codes, const float* scales,
+                                      const float* rstd, const uint16_t* weight, int64_t T,
+                                      int32_t D, uint16_t* dx, int64_t dx_ld, uint16_t* dweight,
+                                      void* scratch, int64_t scratch_bytes, void* stream)
+{
+    LM_CHECK(check_sizes(T, 1, D, ZERO_NORM_MAX_WIDTH));
+    LM_CHECK(check_ld(dy_ld, D));
+    LM_CHECK(check_ld(dx_ld, D));
+    if (dsum) LM_CHECK(check_ld(dsum_ld, D));
+    LM_CHECK(check_ptr(dweight));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return status_of(cudaMemsetAsync(dweight, 0, (size_t)(2 * D), st));
+    LM_CHECK(check_ptr(dy));
+    if (dsum) LM_CHECK(check_ptr(dsum));
+    LM_CHECK(check_ptr(codes));
+    LM_CHECK(check_ptr(scales));
+    LM_CHECK(check_ptr(rstd));
+    LM_CHECK(check_ptr(weight));
+    LM_CHECK(check_ptr(dx));
+    LM_CHECK(check_ptr(scratch));
+    const int64_t need = zero_norm_grad_scratch_bytes(T, D);
+    if (scratch_bytes < need) return ZERO_ERR_SIZE;
+    Spans sp;
+    sp.rows(dy, T, dy_ld, D, 2, false);
+    if (dsum) sp.rows(dsum, T, dsum_ld, D, 2, false);
+    sp.add(codes, T * D, false);
+    sp.add(scales, 4 * T * ((D + kBlock - 1) / kBlock), false);
+    sp.add(rstd, 4 * T, false);
+    sp.add(weight, 2 * D, false);
+    sp.rows(dx, T, dx_ld, D, 2, true);
+    sp.add(dweight, 2 * D, true);
+    sp.add(scratch, need, true);
+    LM_CHECK(sp.check());
+
+    NormGradArgs a{};
+    a.dy = dy;
+    a.dsum = dsum;
+    a.codes = codes;
+    a.scales = scales;
+    a.rstd = rstd;
+    a.w = weight;
+    a.dx = dx;
+    a.dw = dweight;
+    a.parts = static_cast<float*>(scratch);
+    a.T = T;
+    a.dy_ld = dy_ld;
+    a.dsum_ld = dsum_ld;
+    a.dx_ld = dx_ld;
+    a.D = D;
+    auto run = [&](void (*kernel)(NormGradArgs), int tpr) {
+        const int threads = tpr > 128 ? tpr : 128, groups = threads / tpr;
+        a.blocks = (int)std::min<int64_t>((T + groups - 1) / groups, grad_blocks(T));
+        cudaError_t e = launch(kernel, dim3((unsigned)a.blocks), threads, 0, 1, st, a);
+        if (e == cudaSuccess)
+            e = launch(k_norm_join, dim3((unsigned)((D + kJoinCols - 1) / kJoinCols)),
+                       kJoinThreads, 0, 1, st, a);
+        return status_of(e);
+    };
+#define GRAD_GO(tpr, nv) run(k_norm_grad<tpr, nv>, tpr)
+    NORM_FORMS(GRAD_GO);
+#undef GRAD_GO
+}

@@ -1,0 +1,981 @@
+// lm_xent.cu - softmax cross entropy of activations against a (tied)
+// embedding table, in pieces of the vocabulary and without kept logits, and
+// its gradients (declared in include/zero_step.h).
+//
+//   l = h E^T (bf16 products, fp32 sums), lse_t = log sum_v exp(l_tv),
+//   loss_t = lse_t - l_{t, y_t}                       (0 for an ignored token)
+//   P_tv = (exp(l_tv - lse_t) - [v = y_t]) * dloss_t  (0 in an ignored row)
+//   dh = P E,  dE = P^T h
+//
+// Forward is one matrix product whose epilogue keeps, per row and tile of 256
+// vocabulary rows, a running maximum and the sum of exponentials relative to
+// it; a small second kernel joins the tiles.  Backward keeps nothing but lse: for
+// a piece of the vocabulary at a time it makes the logits again, turns them
+// into P in bf16 (the one rounding before the sums; P is an operand of the
+// tensor cores), and multiplies P with both operands.  The gradient of the
+// table's piece is final and written once; dh is summed over the pieces in
+// fp32 and rounded once at the end.
+//
+// Floor: 2*T*D*V operations forward, 6*T*D*V backward (the logits are needed
+// again), on the tensor cores; with few tokens the table's 2*V*D bytes.
+//
+// The product kernel (k_mma): a pair of CTAs (cta_group::2) owns a 256 x 256
+// tile of fp32 sums in tensor memory, 128 rows in each CTA, two tiles deep, so
+// that one tile's epilogue runs under the next tile's products.  Warp 0 of each
+// CTA brings its half of both operands into shared memory with TMA (64 wide
+// along the summed dimension, 128-byte swizzle, 6 or 7 stages), one thread of
+// the first CTA issues the products, warps 4-7 run the epilogue.  An operand
+// may be contiguous along the summed dimension or along the other one; both
+// are read as they lie in memory, nothing is transposed.
+//
+// Every wait is bounded.  When one runs out the CTA sets ZERO_DEV_TIMEOUT, all
+// of its roles leave their loops, copies and products in flight are waited
+// for (again bounded, ZERO_DEV_DRAIN_FAILED if that runs out), the tensor
+// memory is freed and the kernel returns.
+#include <cuda.h>
+
+#include "lm_common.cuh"
+
+namespace {
+
+using namespace lm;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int BM = 256, BN = 256, BK = 64;         // a CTA pair's tile and one stage's depth
+constexpr int kThreads = 256;
+constexpr int kStageBytes = 2 * 128 * BK * 2;      // per CTA: 128 rows of each operand
+constexpr int kPieceAlign = 256;
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kDrainLimit = 1u << 24;
+constexpr int kWarpStage = 4096;                   // an epilogue warp's output buffer (two of them)
+
+enum Kind { kLse, kDlogits, kDtable, kDh };
+
+template <Kind K>
+struct Form;
+template <>
+struct Form<kLse> {
+    static constexpr bool a_k = true, b_k = true, out = false;
+    static constexpr int stages = 7;
+};
+template <>
+struct Form<kDlogits> {
+    static constexpr bool a_k = true, b_k = true, out = true;
+    static constexpr int stages = 6;
+};
+template <>
+struct Form<kDtable> {
+    static constexpr bool a_k = false, b_k = false, out = true;
+    static constexpr int stages = 6;
+};
+template <>
+struct Form<kDh> {
+    static constexpr bool a_k = true, b_k = false, out = true;
+    static constexpr int stages = 6;
+};
+
+template <Kind K>
+constexpr int smem_bytes()
+{
+    return 1024 + Form<K>::stages * kStageBytes + (Form<K>::out ? 4 * 2 * kWarpStage : 0) + 256;
+}
+
+struct MmaArgs {
+    CUtensorMap a, b, out;
+    int32_t m_tiles, n_tiles;          // tiles of 256 x 256
+    int32_t k_blocks, splits;          // blocks of 64 along the summed dimension; its splits
+    int32_t m_fast;                    // which tile coordinate runs fastest
+    int64_t rows, cols;                // of the result (cols: of the piece)
+    int64_t out_split_rows;            // rows between the splits' results (kDh)
+    int32_t add;                       // kDh: add to what is there
+    int32_t token_bytes;
+    const void* targets;
+    int64_t V, v0;                     // the vocabulary, and where the piece starts
+    const float* lse;
+    const float* dloss;
+    float2* part;                      // kLse: [n_tiles][part_ld] (maximum, sum)
+    int64_t part_ld;
+    float* at_target;                  // kLse: the target's logit
+    int32_t* status;
+    uint32_t wait_limit;
+};
+
+// ------------------------------------------------------------ PTX pieces --
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+// the same address in the pair's first CTA
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Wait for a phase; gives up after `limit` tries, or once another role of the
+// CTA has given up.  False: the caller leaves its loop.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t limit,
+                                          volatile int* dead)
+{
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if ((i & 63) == 63 && *dead) return false;
+    }
+    *dead = 1;
+    return false;
+}
+// One box into this CTA's shared memory; the bytes count on the leader's barrier.
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                         uint32_t leader_bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(map), "r"(leader_bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_add(const CUtensorMap* map, int x, int y, uint32_t src)
+{
+    asm volatile(
+        "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+            map),
+        "r"(x), "r"(y), "r"(src)
+        : "memory");
+}
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.ne.u32 p, %4, 0; "
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+// Arrive at the barrier at this offset in both CTAs once the products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float (&x)[32])
+{
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, "
+        "%19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Shared-memory operand descriptors, 128-byte swizzle.  Contiguous along the
+// summed dimension: rows of 128 bytes, 1024 bytes between groups of 8 rows.
+// Contiguous along the other one: two chunks of 64 x 64, 8192 bytes apart,
+// 1024 bytes between groups of 8 along the summed dimension.
+template <bool K_MAJOR>
+__device__ __forceinline__ uint64_t operand(uint32_t addr)
+{
+    const uint64_t lead = K_MAJOR ? 1 : 8192 >> 4;
+    return (uint64_t)((addr >> 4) & 0x3FFF) | lead << 16 | (uint64_t)(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+template <bool K_MAJOR>
+__host__ __device__ constexpr uint64_t operand_step()               // 16 further along the summed dimension
+{
+    return (K_MAJOR ? 32 : 2048) >> 4;
+}
+// fp32 sums, bf16 operands, 256 x 256
+template <Kind K>
+__host__ __device__ constexpr uint32_t instruction()
+{
+    return 1u << 4 | 1u << 7 | 1u << 10 | (Form<K>::a_k ? 0u : 1u << 15) |
+           (Form<K>::b_k ? 0u : 1u << 16) | (uint32_t)(BN >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
+}
+
+// One operand's 128 rows of a stage.
+template <bool K_MAJOR>
+__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int k,
+                                             uint32_t bar)
+{
+    if constexpr (K_MAJOR) {
+        tma_load(dst, map, k, row, bar);
+    } else {
+        tma_load(dst, map, row, k, bar);
+        tma_load(dst + 8192, map, row + 64, k, bar);
+    }
+}
+
+struct Unit {
+    int m, n, k0, k1, split;
+};
+
+__device__ __forceinline__ Unit unit_at(const MmaArgs& a, int u)
+{
+    Unit t;
+    const int tiles = a.m_tiles * a.n_tiles;
+    t.split = u / tiles;
+    const int q = u - t.split * tiles;
+    const int fast = a.m_fast ? a.m_tiles : a.n_tiles;
+    const int hi = q / fast, lo = q - hi * fast;
+    t.m = a.m_fast ? lo : hi;
+    t.n = a.m_fast ? hi : lo;
+    t.k0 = (int)((int64_t)a.k_blocks * t.split / a.splits);
+    t.k1 = (int)((int64_t)a.k_blocks * (t.split + 1) / a.splits);
+    return t;
+}
+
+// ---------------------------------------------------------- the epilogues --
+
+// A row's target, or -1 where it takes part in nothing.
+__device__ __forceinline__ int64_t target_of(const MmaArgs& a, int64_t row)
+{
+    if (row >= a.rows) return -1;
+    const int64_t y = token_at(a.targets, a.token_bytes, row);
+    return y < a.V ? y : -1;
+}
+
+// The row's running maximum (in units of log 2) and sum over the tile's columns.
+__device__ __forceinline__ void epilogue_lse(const MmaArgs& a, const Unit& t, uint32_t tmem,
+                                             int64_t row)
+{
+    const int64_t c0 = (int64_t)t.n * BN;
+    const int live = (int)min((int64_t)BN, a.V - c0);
+    const int64_t y = target_of(a, row) - c0;                // of the tile, if in it
+    float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < BN; c += 32) {
+        if (c >= live) break;
+        float x[32];
+        tmem_load32(tmem + c, x);
+        if (c + 32 > live) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i >= live) x[i] = -INFINITY;
+        }
+        const int at = (int)(y - c);
+        if (y >= c && y < c + 32) {
+            float v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i == at) v = x[i];
+            a.at_target[row] = v;
+        }
+        float m = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) m = fmaxf(m, x[i]);
+        m = fmaxf(top, m * kLog2e);
+        const float ref = m == -INFINITY ? 0.0f : m;         // nothing but -Inf so far
+        sum *= exp2_fast(top - ref);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i & 3] += exp2_fast(fmaf(x[i], kLog2e, -ref));
+        sum += (s[0] + s[1]) + (s[2] + s[3]);
+        top = m;
+    }
+    if (row < a.rows) a.part[(int64_t)t.n * a.part_ld + row] = make_float2(top, sum);
+}
+
+// 16 bytes at (row, chunk) of a 32-row buffer of 128-byte rows, 128-byte swizzle.
+__device__ __forceinline__ void stage16(uint32_t buf, int row, int chunk, uint32_t x, uint32_t y,
+                                        uint32_t z, uint32_t w)
+{
+    const uint32_t p = buf + row * 128 + ((chunk ^ (row & 7)) << 4);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(x), "r"(y), "r"(z),
+                 "r"(w)
+                 : "memory");
+}
+
+// A buffer is free once at most one later store still reads its own.
+__device__ __forceinline__ void stage_free(int lane)
+{
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+}
+__device__ __forceinline__ void stage_full()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+}
+
+// The tile's 128 rows of this CTA in bf16 (P, or the table's gradient): 64
+// columns at a time through the warp's two buffers.
+template <Kind K>
+__device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, uint32_t tmem,
+                                              int64_t row0, int lane, uint32_t buf, int& flip)
+{
+    const int64_t c0 = (int64_t)t.n * BN;
+    if (row0 >= a.rows) return;
+    const int64_t row = row0 + lane;
+    int64_t y = -1;
+    float lse2 = 0.0f, g = 0.0f;
+    bool live = true;
+    if constexpr (K == kDlogits) {
+        y = target_of(a, row);
+        live = y >= 0;
+        lse2 = live ? a.lse[row] * kLog2e : 0.0f;
+        g = live ? a.dloss[row] : 0.0f;
+        y -= a.v0 + c0;
+    }
+#pragma unroll 1
+    for (int c = 0; c < BN; c += 64) {
+        if (c0 + c >= a.cols) break;
+        const uint32_t to = buf + flip * kWarpStage;
+        flip ^= 1;
+        stage_free(lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float x[32];
+            tmem_load32(tmem + c + 32 * h, x);
+            if constexpr (K == kDlogits) {
+                const int at = (int)(y - (c + 32 * h));
+                const bool here = live && y >= c + 32 * h && y < c + 32 * h + 32;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    x[i] = live ? exp2_fast(fmaf(x[i], kLog2e, -lse2)) : 0.0f;
+                }
+                if (here) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i == at) x[i] -= 1.0f;
+                }
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] *= g;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                stage16(to, lane, 4 * h + j, bf_pack(x[8 * j], x[8 * j + 1]),
+                        bf_pack(x[8 * j + 2], x[8 * j + 3]), bf_pack(x[8 * j + 4], x[8 * j + 5]),
+                        bf_pack(x[8 * j + 6], x[8 * j + 7]));
+        }
+        stage_full();
+        if (lane == 0) {
+            tma_store(&a.out, (int)(c0 + c), (int)row0, to);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
+// dh's partial sums in fp32, 32 columns at a time; each element gets one
+// addition per launch, so the order of the sum is the order of the pieces.
+__device__ __forceinline__ void epilogue_f32(const MmaArgs& a, const Unit& t, uint32_t tmem,
+                                             int64_t row0, int lane, uint32_t buf, int& flip)
+{
+    const int64_t c0 = (int64_t)t.n * BN;
+    if (row0 >= a.rows) return;
+#pragma unroll 1
+    for (int c = 0; c < BN; c += 32) {
+        if (c0 + c >= a.cols) break;
+        const uint32_t to = buf + flip * kWarpStage;
+        flip ^= 1;
+        stage_free(lane);
+        float x[32];
+        tmem_load32(tmem + c, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            stage16(to, lane, j, __float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                    __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
+        stage_full();
+        if (lane == 0) {
+            const int y = (int)(t.split * a.out_split_rows + row0);
+            if (a.add) tma_add(&a.out, (int)(c0 + c), y, to);
+            else tma_store(&a.out, (int)(c0 + c), y, to);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
+// ------------------------------------------------------------ the product --
+
+template <Kind K>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    k_mma(const __grid_constant__ MmaArgs a)
+{
+    using F = Form<K>;
+    constexpr int S = F::stages;
+    extern __shared__ uint8_t raw[];
+    // the swizzle pattern needs 1024-byte aligned stages, at the same place in both CTAs
+    const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
+    const uint32_t staging = smem + S * kStageBytes;
+    const uint32_t bars = staging + (F::out ? 4 * 2 * kWarpStage : 0);
+    const uint32_t full = bars, empty = bars + 8 * S;
+    const uint32_t sums_full = empty + 8 * S, sums_empty = sums_full + 16;
+    const uint32_t drained = sums_empty + 16;
+    const uint32_t slot = drained + 8;
+    volatile int* dead = reinterpret_cast<volatile int*>(raw + (slot + 4 - smem_u32(raw)));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full + 8 * s, 1);
+            mbar_init(empty + 8 * s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(sums_full + 8 * b, 1);
+            mbar_init(sums_empty + 8 * b, 8);           // 4 warps of each CTA
+        }
+        mbar_init(drained, 1);
+        *dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+            slot));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    uint32_t tmem;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
+    pdl_enter();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+
+    const int units = a.m_tiles * a.n_tiles * a.splits;
+    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    bool drain_failed = false;
+
+    if (warp == 0 && lane == 0) {                        // ---- loads
+        uint32_t it = 0;
+        bool ok = true;
+        for (int u = first; u < units && ok; u += stride) {
+            const Unit t = unit_at(a, u);
+            const int ra = t.m * BM + (int)rank * 128, rb = t.n * BN + (int)rank * 128;
+            for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+                const uint32_t s = it % S, ph = (it / S) & 1;
+                if (!(ok = mbar_wait(empty + 8 * s, ph ^ 1, a.wait_limit, dead))) break;
+                if (leader) mbar_expect(full + 8 * s, 2 * kStageBytes);
+                const uint32_t dst = smem + s * kStageBytes;
+                const uint32_t bar = in_leader(full + 8 * s);
+                load_operand<F::a_k>(dst, &a.a, ra, kb * BK, bar);
+                load_operand<F::b_k>(dst + kStageBytes / 2, &a.b, rb, kb * BK, bar);
+            }
+        }
+        // Before this CTA may leave: the products' last arrivals at its
+        // barriers; or, after a wait ran out, the copies that were issued (both
+        // CTAs' copies count on the leader's barriers).
+        const uint32_t from = it > (uint32_t)S ? it - S : 0;
+        if (ok) {
+            for (uint32_t j = from; j < it && ok; ++j)
+                ok = mbar_wait(empty + 8 * (j % S), (j / S) & 1, a.wait_limit, dead);
+        }
+        if (!ok && leader) {
+            int none = 0;
+            for (uint32_t j = from; j < it; ++j)
+                drain_failed |= !mbar_wait(full + 8 * (j % S), (j / S) & 1, kDrainLimit, &none);
+        }
+    } else if (warp == 1 && lane == 0 && leader) {       // ---- products
+        uint32_t it = 0;
+        int i = 0;
+        bool ok = true;
+        for (int u = first; u < units && ok; u += stride, ++i) {
+            const Unit t = unit_at(a, u);
+            const int b = i & 1;
+            if (!(ok = mbar_wait(sums_empty + 8 * b, ((i >> 1) & 1) ^ 1, a.wait_limit, dead)))
+                break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
+                const uint32_t s = it % S, ph = (it / S) & 1;
+                if (!(ok = mbar_wait(full + 8 * s, ph, a.wait_limit, dead))) break;
+                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+                const uint32_t at = smem + s * kStageBytes;
+                const uint64_t da = operand<F::a_k>(at), db = operand<F::b_k>(at + kStageBytes / 2);
+#pragma unroll
+                for (int q = 0; q < BK / 16; ++q)
+                    mma(tmem + b * BN, da + q * operand_step<F::a_k>(),
+                        db + q * operand_step<F::b_k>(), instruction<K>(), kb > t.k0 || q > 0);
+                mma_commit(empty + 8 * s);
+            }
+            if (ok) mma_commit(sums_full + 8 * b);
+        }
+        if (!ok) {                                       // products in flight
+            mma_commit(drained);
+            int none = 0;
+            drain_failed |= !mbar_wait(drained, 0, kDrainLimit, &none);
+        }
+    } else if (warp >= 4) {                              // ---- epilogue
+        const int q = warp - 4;                          // the warp's quarter of the lanes
+        const uint32_t buf = staging + q * 2 * kWarpStage;
+        int i = 0, flip = 0;
+        for (int u = first; u < units; u += stride, ++i) {
+            const Unit t = unit_at(a, u);
+            const int b = i & 1;
+            const bool ok = mbar_wait(sums_full + 8 * b, (i >> 1) & 1, a.wait_limit, dead);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t from = tmem + b * BN + ((uint32_t)(q * 32) << 16);
+            const int64_t row0 = (int64_t)t.m * BM + rank * 128 + q * 32;
+            if constexpr (K == kLse) epilogue_lse(a, t, from, row0 + lane);
+            else if constexpr (K == kDh) epilogue_f32(a, t, from, row0, lane, buf, flip);
+            else epilogue_bf16<K>(a, t, from, row0, lane, buf, flip);
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(in_leader(sums_empty + 8 * b));
+        }
+        if (F::out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    __syncwarp();
+    if (drain_failed && a.status) atomicOr(a.status, ZERO_DEV_DRAIN_FAILED);
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0 && *dead && a.status) atomicOr(a.status, ZERO_DEV_TIMEOUT);
+    cluster_sync();
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    if (warp == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+// ------------------------------------------------------------ small parts --
+
+// Joins a row's tiles: a block takes 32 rows, its 32 warps every 32nd tile.
+struct JoinArgs {
+    const float2* part;
+    const float* at_target;
+    const void* targets;
+    int64_t part_ld, T, V;
+    int32_t n_tiles, token_bytes;
+    float* loss;
+    float* lse;
+    int32_t* status;
+};
+
+__device__ __forceinline__ void join(float& m, float& s, float2 x)
+{
+    const float top = fmaxf(m, x.x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    s = s * exp2_fast(m - ref) + x.y * exp2_fast(x.x - ref);
+    m = top;
+}
+
+__global__ void __launch_bounds__(1024) k_xent_join(const __grid_constant__ JoinArgs a)
+{
+    pdl_enter();
+    __shared__ float2 all[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    float m = -INFINITY, s = 0.0f;
+    if (row < a.T) {
+#pragma unroll 4
+        for (int n = warp; n < a.n_tiles; n += 32) join(m, s, a.part[n * a.part_ld + row]);
+    }
+    all[lane][warp] = make_float2(m, s);
+    __syncthreads();
+    float2 x = all[warp][lane];                            // a row's 32 shares in a warp
+    m = x.x;
+    s = x.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float2 y = make_float2(__shfl_down_sync(0xFFFFFFFFu, m, o),
+                                     __shfl_down_sync(0xFFFFFFFFu, s, o));
+        join(m, s, y);
+    }
+    const int64_t r = (int64_t)blockIdx.x * 32 + warp;
+    if (lane == 0 && r < a.T) {
+        const float lse = m * kLn2 + logf(s);
+        a.lse[r] = lse;
+        const int64_t y = token_at(a.targets, a.token_bytes, r);
+        if (y >= a.V && a.status) atomicOr(a.status, ZERO_DEV_BAD_TOKEN);
+        a.loss[r] = y >= 0 && y < a.V ? lse - a.at_target[r] : 0.0f;
+    }
+}
+
+// h with the ignored rows zeroed: their P is zero, but zero times an Inf or a
+// NaN that such a row may hold would reach every row of the table's gradient.
+struct CleanArgs {
+    const uint16_t* h;
+    uint16_t* out;
+    const void* targets;
+    int64_t T, V, h_ld;
+    int32_t D, token_bytes;
+    int32_t* status;
+};
+
+__global__ void __launch_bounds__(256) k_clean(const __grid_constant__ CleanArgs a)
+{
+    pdl_enter();
+    const int lane = threadIdx.x & 31, nv = a.D >> 3;
+    const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    if (t >= a.T) return;
+    const int64_t y = token_at(a.targets, a.token_bytes, t);
+    if (y >= a.V && lane == 0 && a.status) atomicOr(a.status, ZERO_DEV_BAD_TOKEN);
+    const bool live = y >= 0 && y < a.V;
+#pragma unroll 4
+    for (int c = lane; c < nv; c += 32)
+        st16(a.out + t * a.D + c * 8, live ? ld16(a.h + t * a.h_ld + c * 8) : make_uint4(0, 0, 0, 0));
+}
+
+// dh from its splits' sums, added in order.
+struct FinishArgs {
+    const float* sums;
+    uint16_t* dh;
+    int64_t T, split_rows, dh_ld;
+    int32_t D, splits;
+};
+
+__global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishArgs a)
+{
+    pdl_enter();
+    const int lane = threadIdx.x & 31, nv = a.D >> 3;
+    const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    if (t >= a.T) return;
+    for (int c = lane; c < nv; c += 32) {
+        float f[8] = {};
+        for (int s = 0; s < a.splits; ++s) {
+            const float* p = a.sums + (s * a.split_rows + t) * a.D + c * 8;
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+            const float4 y = __ldcs(reinterpret_cast<const float4*>(p + 4));
+            f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+            f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+        }
+        st16_stream(a.dh + t * a.dh_ld + c * 8, bf_pack8(f));
+    }
+}
+
+// ------------------------------------------------------------------- host --
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder()
+{
+    static EncodeFn fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            f = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// A row-major matrix (row stride `ld` elements), in boxes of 128 bytes x box_rows.
+bool encode(CUtensorMap* map, const void* p, bool f32, int64_t cols, int64_t rows, int64_t ld,
+            int box_rows)
+{
+    const int elem = f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows};
+    const cuuint32_t steps[2] = {1, 1};
+    const EncodeFn fn = encoder();
+    return fn && fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    2, const_cast<void*>(p), dims, strides, box, steps,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int tiles(int64_t n) { return (int)((n + 255) / 256); }
+
+template <Kind K>
+cudaError_t run_mma(const MmaArgs& a, cudaStream_t st)
+{
+    static std::atomic<uint64_t> smem_set;
+    const cudaError_t e =
+        allow_smem(reinterpret_cast<const void*>(&k_mma<K>), smem_bytes<K>(), smem_set);
+    if (e != cudaSuccess) return e;
+    const int units = a.m_tiles * a.n_tiles * a.splits;
+    const int pairs = std::max(1, std::min(units, device_sms() / 2));
+    return launch(k_mma<K>, dim3((unsigned)(2 * pairs)), kThreads, smem_bytes<K>(), 1, st, a);
+}
+
+struct LossScratch {
+    int64_t part_ld, part, at_target, bytes;
+};
+
+LossScratch loss_scratch(int64_t T, int64_t V)
+{
+    LossScratch s;
+    s.part_ld = up(T, 32);
+    s.part = 0;
+    s.at_target = up(8 * s.part_ld * (int64_t)tiles(V), 256);
+    s.bytes = s.at_target + up(4 * T, 256);
+    return s;
+}
+
+// The backward pass's plan: the piece, the splits of dh's sum, the scratch.
+struct GradPlan {
+    int64_t piece, p, clean, sums, split_rows, bytes;
+    int32_t splits;
+};
+
+GradPlan grad_plan(int64_t T, int64_t V, int32_t D, int64_t piece)
+{
+    GradPlan g;
+    if (piece == 0) {
+        // P of a piece is at most 512 MiB; equal pieces
+        const int64_t most = std::max<int64_t>(kPieceAlign, (1ll << 28) / std::max<int64_t>(T, 1) /
+                                                                kPieceAlign * kPieceAlign);
+        const int64_t n = (V + most - 1) / most;
+        piece = (V + n - 1) / n;
+    }
+    g.piece = std::min(up(piece, kPieceAlign), up(V, kPieceAlign));
+    const int64_t t = (int64_t)tiles(T) * tiles(D);
+    const int64_t k_blocks = (std::min(V, g.piece) + BK - 1) / BK;
+    // few tokens: the sum over the piece is split so that every CTA pair has a part
+    g.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>(device_sms() / 2 / std::max<int64_t>(t, 1),
+                                                              k_blocks));
+    g.p = 0;
+    g.clean = up(2 * T * g.piece, 256);
+    g.sums = g.clean + up(2 * T * D, 256);
+    g.split_rows = up(T, 32);            // an output box never reaches into the next split
+    g.bytes = g.sums + up(4 * g.split_rows * D * g.splits, 256);
+    return g;
+}
+
+zero_status check_xent(int64_t T, int64_t V, int32_t D, int32_t target_bytes, int32_t flags,
+                       const int32_t* dev_status)
+{
+    LM_CHECK(check_sizes(T, V, D));
+    if (target_bytes != 4 && target_bytes != 8) return ZERO_ERR_INVALID_ARG;
+    if (flags & ~ZERO_FLAG_DEBUG_EXPIRE_WAITS) return ZERO_ERR_INVALID_ARG;
+    if (flags && !dev_status) return ZERO_ERR_NULL;
+    // the units of a launch are counted in 32 bits
+    if ((int64_t)tiles(T) * tiles(V) > INT32_MAX / 2 || (int64_t)tiles(V) * tiles(D) > INT32_MAX / 2 ||
+        (int64_t)tiles(T) * tiles(D) > INT32_MAX / 2)
+        return ZERO_ERR_SIZE;
+    return check_status(dev_status);
+}
+
+}  // namespace
+
+extern "C" int64_t zero_xent_scratch_bytes(int64_t T, int64_t V, int32_t D)
+{
+    if (check_sizes(T, V, D) != ZERO_OK) return -1;
+    return loss_scratch(T, V).bytes;
+}
+
+extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t* table, int64_t V,
+                                 int32_t D, const void* targets, int32_t target_bytes, int64_t T,
+                                 float* loss, float* lse, void* scratch, int64_t scratch_bytes,
+                                 int32_t flags, int32_t* dev_status, void* stream)
+{
+    LM_CHECK(check_xent(T, V, D, target_bytes, flags, dev_status));
+    LM_CHECK(check_ld(h_ld, D));
+    if (T == 0) return ZERO_OK;
+    LM_CHECK(check_ptr(h));
+    LM_CHECK(check_ptr(table));
+    LM_CHECK(check_tokens(targets, target_bytes));
+    LM_CHECK(check_ptr(loss, 4));
+    LM_CHECK(check_ptr(lse, 4));
+    LM_CHECK(check_ptr(scratch));
+    const LossScratch s = loss_scratch(T, V);
+    if (scratch_bytes < s.bytes) return ZERO_ERR_SIZE;
+    Spans sp;
+    sp.rows(h, T, h_ld, D, 2, false);
+    sp.add(table, 2 * V * D, false);
+    sp.add(targets, T * target_bytes, false);
+    sp.add(loss, 4 * T, true);
+    sp.add(lse, 4 * T, true);
+    sp.add(scratch, s.bytes, true);
+    sp.add(dev_status, 4, true);
+    LM_CHECK(sp.check());
+
+    uint8_t* base = static_cast<uint8_t*>(scratch);
+    MmaArgs a{};
+    if (!encode(&a.a, h, false, D, T, h_ld, 128) || !encode(&a.b, table, false, D, V, D, 128))
+        return ZERO_ERR_CUDA;
+    a.m_tiles = tiles(T);
+    a.n_tiles = tiles(V);
+    a.k_blocks = (D + BK - 1) / BK;
+    a.splits = 1;
+    a.m_fast = 1;
+    a.rows = T;
+    a.cols = V;
+    a.token_bytes = target_bytes;
+    a.targets = targets;
+    a.V = V;
+    a.part = reinterpret_cast<float2*>(base + s.part);
+    a.part_ld = s.part_ld;
+    a.at_target = reinterpret_cast<float*>(base + s.at_target);
+    a.status = dev_status;
+    a.wait_limit = flags & ZERO_FLAG_DEBUG_EXPIRE_WAITS ? 0 : kWaitLimit;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = run_mma<kLse>(a, st);
+    if (e == cudaSuccess) {
+        const JoinArgs j{a.part, a.at_target, targets, s.part_ld, T, V, a.n_tiles, target_bytes,
+                         loss, lse, dev_status};
+        e = launch(k_xent_join, dim3((unsigned)((T + 31) / 32)), 1024, 0, 1, st, j);
+    }
+    return status_of(e);
+}
+
+extern "C" int64_t zero_xent_grad_scratch_bytes(int64_t T, int64_t V, int32_t D, int64_t piece)
+{
+    if (check_sizes(T, V, D) != ZERO_OK || piece < 0 || piece % kPieceAlign != 0) return -1;
+    return grad_plan(T, V, D, piece).bytes;
+}
+
+extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uint16_t* table,
+                                      int64_t V, int32_t D, const void* targets,
+                                      int32_t target_bytes, int64_t T, const float* lse,
+                                      const float* dloss, uint16_t* dh, int64_t dh_ld,
+                                      uint16_t* dtable, int64_t piece, void* scratch,
+                                      int64_t scratch_bytes, int32_t flags, int32_t* dev_status,
+                                      void* stream)
+{
+    LM_CHECK(check_xent(T, V, D, target_bytes, flags, dev_status));
+    LM_CHECK(check_ld(h_ld, D));
+    LM_CHECK(check_ld(dh_ld, D));
+    if (piece < 0 || piece % kPieceAlign != 0) return ZERO_ERR_INVALID_ARG;
+    LM_CHECK(check_ptr(dtable));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) return status_of(cudaMemsetAsync(dtable, 0, (size_t)(2 * V * D), st));
+    LM_CHECK(check_ptr(h));
+    LM_CHECK(check_ptr(table));
+    LM_CHECK(check_tokens(targets, target_bytes));
+    LM_CHECK(check_ptr(lse, 4));
+    LM_CHECK(check_ptr(dloss, 4));
+    LM_CHECK(check_ptr(dh));
+    LM_CHECK(check_ptr(scratch));
+    const GradPlan g = grad_plan(T, V, D, piece);
+    if (scratch_bytes < g.bytes) return ZERO_ERR_SIZE;
+    Spans sp;
+    sp.rows(h, T, h_ld, D, 2, false);
+    sp.add(table, 2 * V * D, false);
+    sp.add(targets, T * target_bytes, false);
+    sp.add(lse, 4 * T, false);
+    sp.add(dloss, 4 * T, false);
+    sp.rows(dh, T, dh_ld, D, 2, true);
+    sp.add(dtable, 2 * V * D, true);
+    sp.add(scratch, g.bytes, true);
+    sp.add(dev_status, 4, true);
+    LM_CHECK(sp.check());
+
+    uint8_t* base = static_cast<uint8_t*>(scratch);
+    uint16_t* P = reinterpret_cast<uint16_t*>(base + g.p);
+    uint16_t* clean = reinterpret_cast<uint16_t*>(base + g.clean);
+    float* sums = reinterpret_cast<float*>(base + g.sums);
+    const unsigned row_blocks = (unsigned)((T + 7) / 8);
+    const CleanArgs ca{h, clean, targets, T, V, h_ld, D, target_bytes, dev_status};
+    cudaError_t e = launch(k_clean, dim3(row_blocks), 256, 0, 1, st, ca);
+
+    MmaArgs common{};
+    common.token_bytes = target_bytes;
+    common.targets = targets;
+    common.V = V;
+    common.lse = lse;
+    common.dloss = dloss;
+    common.status = dev_status;
+    common.wait_limit = flags & ZERO_FLAG_DEBUG_EXPIRE_WAITS ? 0 : kWaitLimit;
+    for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += g.piece) {
+        const int64_t n = std::min(g.piece, V - v0);
+        const uint16_t* rows = table + v0 * D;
+
+        MmaArgs p = common;                                 // P = f(h E^T)
+        if (!encode(&p.a, h, false, D, T, h_ld, 128) || !encode(&p.b, rows, false, D, n, D, 128) ||
+            !encode(&p.out, P, false, n, T, g.piece, 32))
+            return ZERO_ERR_CUDA;
+        p.m_tiles = tiles(T);
+        p.n_tiles = tiles(n);
+        p.k_blocks = (D + BK - 1) / BK;
+        p.splits = 1;
+        p.m_fast = 1;
+        p.rows = T;
+        p.cols = n;
+        p.v0 = v0;
+        if ((e = run_mma<kDlogits>(p, st)) != cudaSuccess) break;
+
+        MmaArgs d = common;                                 // dh += P E
+        if (!encode(&d.a, P, false, n, T, g.piece, 128) || !encode(&d.b, rows, false, D, n, D, 64) ||
+            !encode(&d.out, sums, true, D, g.split_rows * g.splits, D, 32))
+            return ZERO_ERR_CUDA;
+        d.m_tiles = tiles(T);
+        d.n_tiles = tiles(D);
+        d.k_blocks = (int32_t)((n + BK - 1) / BK);
+        d.splits = std::min(g.splits, d.k_blocks);
+        d.rows = T;
+        d.cols = D;
+        d.out_split_rows = g.split_rows;
+        d.add = v0 > 0;
+        if ((e = run_mma<kDh>(d, st)) != cudaSuccess) break;
+
+        MmaArgs w = common;                                 // dE = P^T h
+        if (!encode(&w.a, P, false, n, T, g.piece, 64) || !encode(&w.b, clean, false, D, T, D, 64) ||
+            !encode(&w.out, dtable + v0 * D, false, D, n, D, 32))
+            return ZERO_ERR_CUDA;
+        w.m_tiles = tiles(n);
+        w.n_tiles = tiles(D);
+        w.k_blocks = (int32_t)((T + BK - 1) / BK);
+        w.splits = 1;
+        w.rows = n;
+        w.cols = D;
+        e = run_mma<kDtable>(w, st);
+    }
+    if (e == cudaSuccess) {
+        const FinishArgs f{sums, dh, T, g.split_rows, dh_ld, D, g.splits};
+        e = launch(k_finish, dim3(row_blocks), 256, 0, 1, st, f);
+    }
+    return status_of(e);
+}
