@@ -703,9 +703,10 @@ int64_t zero_xent_grad_scratch_bytes(int64_t T, int64_t V, int32_t D, int64_t pi
 
 /*
  * Its gradients, from lse (zero_xent's) and the upstream gradient dloss[t] of
- * each token's loss: with P = bf16((exp(logit - lse) - [v == target]) * dloss),
+ * each token's loss: with u = the largest finite |dloss| of the tokens that count and
+ * P = bf16((exp(logit - lse) - [v == target]) * dloss / u),
  * zero in the rows of no token whatever h and dloss hold there,
- *   dh = bf16(P table),  dtable = bf16(P^T h)   (every row written).
+ *   dh = bf16(u P table),  dtable = bf16(u P^T h)   (every row written).
  * The vocabulary is taken `piece` rows at a time (a multiple of 256; 0: chosen
  * so that P takes at most 512 MiB); a larger piece needs more scratch.
  */

@@ -97,9 +97,11 @@ struct SortArgs {
     const void* tokens;
     int32_t token_bytes;
     int64_t T, V;
-    uint32_t* key[2];                // ping-pong lists; the result is in key[passes & 1]
-    uint32_t* pos[2];
-    uint32_t* counts;                // [kMaxCluster][kMaxBins]
+    uint32_t* key0;                  // ping-pong lists; after an odd number of
+    uint32_t* key1;                  // passes the result is in the second
+    uint32_t* pos0;
+    uint32_t* pos1;
+    uint32_t* counts;                // [2][kMaxCluster][kMaxBins], by turns
     int32_t passes, bits;            // digits of `bits` bits
     int32_t cluster;
     uint4* zero;                     // the gradient to fill, or null
@@ -117,7 +119,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
 {
     pdl_enter();
     extern __shared__ uint32_t warp_bins[];                 // [kSortWarps][bins]
-    __shared__ uint32_t base[kMaxBins], scan[kMaxBins];
+    __shared__ uint32_t base[kMaxBins], total[kMaxBins], warp_total[kMaxBins / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if ((int)blockIdx.x >= a.cluster) {                     // whole clusters of fillers
@@ -131,11 +133,13 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
     const int bins = 1 << a.bits;
     const int64_t part = (a.T + a.cluster - 1) / a.cluster;
     const int64_t lo = min((int64_t)blockIdx.x * part, a.T), hi = min(lo + part, a.T);
+    const bool one_round = part <= kSortRound;
+    uint32_t* mine = warp_bins + warp * bins;
     for (int pass = 0; pass < a.passes; ++pass) {
-        const uint32_t* key_in = a.key[pass & 1];
-        const uint32_t* pos_in = a.pos[pass & 1];
-        uint32_t* key_out = a.key[(pass & 1) ^ 1];
-        uint32_t* pos_out = a.pos[(pass & 1) ^ 1];
+        const uint32_t* key_in = pass & 1 ? a.key1 : a.key0;
+        const uint32_t* pos_in = pass & 1 ? a.pos1 : a.pos0;
+        uint32_t* key_out = pass & 1 ? a.key0 : a.key1;
+        uint32_t* pos_out = pass & 1 ? a.pos0 : a.pos1;
         const int shift = pass * a.bits;
         auto load = [&](int64_t i, uint32_t& k, uint32_t& p) {
             if (pass > 0) {                                 // written by the other blocks
@@ -148,107 +152,133 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
             k = v >= 0 && v < a.V ? (uint32_t)v : (uint32_t)a.V;
             p = (uint32_t)i;
         };
-
-        // how many items of each digit this block has
-        for (int b = tid; b < bins; b += kSortThreads) scan[b] = 0;
-        __syncthreads();
-        for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
-            uint32_t k, p;
-            load(i, k, p);
-            atomicAdd(&scan[(k >> shift) & (bins - 1)], 1u);
-        }
-        __syncthreads();
-        for (int b = tid; b < bins; b += kSortThreads)
-            __stcg(a.counts + blockIdx.x * kMaxBins + b, scan[b]);
-        cluster_sync();
-
-        // where this block's first item of each digit goes: the smaller
-        // digits of all blocks, then the same digit of the blocks before
-        uint32_t before = 0, total = 0;
-        if (tid < bins) {
-            for (int q = 0; q < a.cluster; ++q) {
-                const uint32_t n = __ldcg(a.counts + q * kMaxBins + tid);
-                total += n;
-                if (q < (int)blockIdx.x) before += n;
-            }
-        }
-        if (tid < kMaxBins) scan[tid] = tid < bins ? total : 0;
-        __syncthreads();
-        for (int o = 1; o < kMaxBins; o <<= 1) {
-            uint32_t x = 0;
-            if (tid < kMaxBins && tid >= o) x = scan[tid - o];
-            __syncthreads();
-            if (tid < kMaxBins) scan[tid] += x;
-            __syncthreads();
-        }
-        if (tid < bins) base[tid] = scan[tid] - total + before;
-        __syncthreads();
-
-        for (int64_t r0 = lo; r0 < hi; r0 += kSortRound) {
+        uint32_t k[kSortItems], p[kSortItems], rank[kSortItems];
+        // A round's items, a warp 32 * kSortItems consecutive ones in list order:
+        // each item's rank in its warp, each warp's first place in the block's
+        // items of a digit (in warp_bins), and the block's total of each digit.
+        auto rank_round = [&](int64_t r0) {
             for (int b = tid; b < kSortWarps * bins; b += kSortThreads) warp_bins[b] = 0;
-            __syncthreads();
-            // a warp owns 32 * kSortItems consecutive items, in list order
-            uint32_t k[kSortItems], p[kSortItems], rank[kSortItems];
-            uint32_t* mine = warp_bins + warp * bins;
             const int64_t w0 = r0 + warp * 32 * kSortItems + lane;
 #pragma unroll
-            for (int q = 0; q < kSortItems; ++q) {
-                const int64_t i = w0 + q * 32;
-                if (i < hi) load(i, k[q], p[q]);
-            }
+            for (int q = 0; q < kSortItems; ++q)
+                if (w0 + q * 32 < hi) load(w0 + q * 32, k[q], p[q]);
+            __syncthreads();
 #pragma unroll
             for (int q = 0; q < kSortItems; ++q) {
                 const bool in = w0 + q * 32 < hi;
                 const uint32_t d = in ? (k[q] >> shift) & (bins - 1) : 0xFFFFFFFFu;
                 const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
                 const int first = __ffs(same) - 1;
-                const uint32_t below = __popc(same & ((1u << lane) - 1));
                 uint32_t had = 0;
                 if (in && lane == first) {
                     had = mine[d];
                     mine[d] = had + __popc(same);
                 }
-                rank[q] = __shfl_sync(0xFFFFFFFFu, had, first) + below;
+                rank[q] = __shfl_sync(0xFFFFFFFFu, had, first) +
+                          __popc(same & ((1u << lane) - 1));
                 __syncwarp();
             }
             __syncthreads();
             for (int b = tid; b < bins; b += kSortThreads) {
-                uint32_t at = base[b];
+                uint32_t sum = 0;
+#pragma unroll 8
                 for (int w = 0; w < kSortWarps; ++w) {
                     const uint32_t n = warp_bins[w * bins + b];
-                    warp_bins[w * bins + b] = at;
-                    at += n;
+                    warp_bins[w * bins + b] = sum;
+                    sum += n;
                 }
-                base[b] = at;
+                total[b] = sum;
             }
             __syncthreads();
+        };
+
+        // how many items of each digit this block has
+        if (one_round) {
+            rank_round(lo);
+        } else {
+            for (int b = tid; b < bins; b += kSortThreads) total[b] = 0;
+            __syncthreads();
+            for (int64_t i = lo + tid; i < hi; i += kSortThreads) {
+                uint32_t kk, pp;
+                load(i, kk, pp);
+                atomicAdd(&total[(kk >> shift) & (bins - 1)], 1u);
+            }
+            __syncthreads();
+        }
+        // where this block's first item of each digit goes: the smaller
+        // digits of all blocks, then the same digit of the blocks before
+        uint32_t before = 0, sum = 0;
+        if (a.cluster > 1) {
+            uint32_t* counts = a.counts + (pass & 1) * kMaxCluster * kMaxBins;
+            if (tid < bins) __stcg(counts + blockIdx.x * kMaxBins + tid, total[tid]);
+            cluster_sync();
+            if (tid < bins) {
+                uint32_t n[kMaxCluster];
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q)
+                    n[q] = q < a.cluster ? __ldcg(counts + q * kMaxBins + tid) : 0;
+#pragma unroll
+                for (int q = 0; q < kMaxCluster; ++q) {
+                    sum += n[q];
+                    if (q < (int)blockIdx.x) before += n[q];
+                }
+            }
+        } else if (tid < bins) {
+            sum = total[tid];
+        }
+        if (tid < kMaxBins) {
+            uint32_t incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += x;
+            }
+            if (lane == 31) warp_total[warp] = incl;
+            before += incl - sum;
+        }
+        __syncthreads();
+        if (tid < bins) {
+            for (int w = 0; w < warp; ++w) before += warp_total[w];
+            base[tid] = before;
+        }
+        __syncthreads();
+
+        for (int64_t r0 = lo; r0 < hi; r0 += kSortRound) {
+            if (!one_round) rank_round(r0);
+            const int64_t w0 = r0 + warp * 32 * kSortItems + lane;
 #pragma unroll
             for (int q = 0; q < kSortItems; ++q) {
                 if (w0 + q * 32 < hi) {
-                    const uint32_t to = mine[(k[q] >> shift) & (bins - 1)] + rank[q];
+                    const uint32_t d = (k[q] >> shift) & (bins - 1);
+                    const uint32_t to = base[d] + mine[d] + rank[q];
                     __stcg(key_out + to, k[q]);
                     __stcg(pos_out + to, p[q]);
                 }
             }
-            __syncthreads();
+            if (!one_round) {
+                __syncthreads();
+                for (int b = tid; b < bins; b += kSortThreads) base[b] += total[b];
+                __syncthreads();
+            }
         }
-        cluster_sync();
+        if (pass + 1 < a.passes) cluster_sync();
     }
 }
 
 // ============================================================== gradient ==
-// The sorted list is cut into chunks of 32 places; a warp takes a chunk and
-// 256 columns (16 bytes a lane).  A token's run of at most 32 places is summed
+// The sorted list is cut into chunks of C places; a warp takes a chunk and
+// 256 columns (16 bytes a lane).  A token's run of at most C places is summed
 // by the warp of the chunk it starts in, which reads on into the next chunk
 // where the run does; it is written once, already rounded.  A longer run
 // leaves one fp32 part per chunk it meets, and k_embed_join adds those in
 // order.  So a frequent token is spread over as many warps as it has chunks,
 // and text's many rare tokens leave no parts at all.
 
-constexpr int kChunk = 32;
 constexpr int kColumns = 256;                // of a warp: 32 lanes x 8
-constexpr int kGradThreads = 256;
-constexpr int kGradBatch = 8;                // rows in flight
+constexpr int kGradThreads = 128;
+constexpr int kJoinThreads = 256;
+constexpr int kBatch = 8;                    // rows in flight
+constexpr int64_t kFewWarps = 2432;          // 16 for each of 152 SMs
 
 struct GradArgs {
     const uint16_t* dy;
@@ -257,11 +287,53 @@ struct GradArgs {
     uint16_t* grad;
     float* parts;                            // [2 * chunks][D]: a chunk's head and tail
     int64_t T, V, dy_ld;
-    int32_t D, slices, accumulate;
+    int32_t D, slices, chunks, accumulate;
     float scale;
 };
 
-__device__ __forceinline__ void add_row(float (&acc)[8], const uint4& x)
+// What a warp finds out about a chunk from the keys around it.
+struct ChunkRuns {
+    uint32_t cur, next;                      // lane i: the key at place i, and at place C + i
+    int skip;                                // leading places that belong to an earlier chunk's run
+    bool head_long, tail_long;               // a long run covers [0, skip) / [tail, C)
+    int tail;                                // where the tail run starts, C if it ends in the chunk
+    int n;                                   // places with a token, in the chunk
+    int more;                                // places of the tail run after the chunk, if not long
+};
+
+template <int C>
+__device__ __forceinline__ ChunkRuns chunk_runs(const uint32_t* key, int64_t T, int64_t V,
+                                                int64_t c, int lane)
+{
+    constexpr uint32_t ALL = 0xFFFFFFFFu, PLACES = C == 32 ? ALL : (1u << (C & 31)) - 1;
+    ChunkRuns r;
+    const uint32_t none = (uint32_t)V;
+    const int64_t i = c * C + lane;
+    const uint32_t prev = c > 0 && lane < C ? key[i - C] : none;
+    r.cur = lane < C && i < T ? key[i] : none;
+    r.next = lane < C && i + C < T ? key[i + C] : none;
+    const uint32_t first = __shfl_sync(ALL, r.cur, 0);
+    const uint32_t last = __shfl_sync(ALL, r.cur, C - 1);
+    r.n = __popc(__ballot_sync(ALL, r.cur != none) & PLACES);
+    const uint32_t not_head = __ballot_sync(ALL, r.cur != first) & PLACES;
+    const uint32_t not_tail = __ballot_sync(ALL, r.cur != last) & PLACES;
+    const uint32_t prev_not = __ballot_sync(ALL, prev != first) & PLACES;
+    const uint32_t next_not = __ballot_sync(ALL, r.next != last) & PLACES;
+    const int lead = not_head ? __ffs(not_head) - 1 : C;         // of the first key
+    const int before = prev_not ? C - 32 + __clz(prev_not) : C;  // places just before the chunk
+    const int after = next_not ? __ffs(next_not) - 1 : C;        // places just after it
+    r.skip = first != none && before > 0 ? lead : 0;
+    r.head_long = r.skip > 0 && before + lead > C;
+    // the tail run: starts in this chunk and goes on in the next
+    const bool goes_on = last != none && after > 0;
+    const int start = not_tail ? 32 - __clz(not_tail) : 0;
+    r.tail = goes_on && !(start == 0 && r.skip > 0) ? start : C;
+    r.tail_long = r.tail < C && (C - r.tail) + after > C;
+    r.more = r.tail < C && !r.tail_long ? after : 0;
+    return r;
+}
+
+__device__ __forceinline__ void add8(float (&acc)[8], const uint4& x)
 {
     float f[8];
     bf_unpack8(x, f);
@@ -269,113 +341,71 @@ __device__ __forceinline__ void add_row(float (&acc)[8], const uint4& x)
     for (int q = 0; q < 8; ++q) acc[q] += f[q];
 }
 
-__device__ __forceinline__ void write_row(const GradArgs& a, uint32_t v, int col, float (&acc)[8])
-{
-    uint16_t* p = a.grad + (int64_t)v * a.D + col;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) acc[q] *= a.scale;
-    if (a.accumulate) {
-        float f[8];
-        bf_unpack8(ld16(p), f);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) acc[q] += f[q];
-    }
-    st16(p, bf_pack8(acc));
-}
-
-// What a warp finds out about a chunk from the keys around it.
-struct ChunkRuns {
-    uint32_t cur, next;                      // this lane's key in the chunk, and 32 places on
-    int skip;                                // leading places that belong to an earlier chunk's run
-    bool head_long, tail_long;               // a long run covers [0, skip) / [tail, 32)
-    int tail;                                // where the tail run starts, 32 if it ends in the chunk
-    int n;                                   // places with a token, in the chunk
-    int more;                                // places of the tail run after the chunk, if not long
-};
-
-__device__ __forceinline__ ChunkRuns chunk_runs(const uint32_t* key, int64_t T, int64_t V,
-                                                int64_t c, int lane)
-{
-    ChunkRuns r;
-    const uint32_t none = (uint32_t)V;
-    const int64_t i = c * kChunk + lane;
-    const uint32_t prev = c > 0 ? key[i - kChunk] : none;
-    r.cur = i < T ? key[i] : none;
-    r.next = i + kChunk < T ? key[i + kChunk] : none;
-    const uint32_t first = __shfl_sync(0xFFFFFFFFu, r.cur, 0);
-    const uint32_t last = __shfl_sync(0xFFFFFFFFu, r.cur, 31);
-    r.n = __popc(__ballot_sync(0xFFFFFFFFu, r.cur != none));
-    const uint32_t not_head = __ballot_sync(0xFFFFFFFFu, r.cur != first);
-    const uint32_t not_tail = __ballot_sync(0xFFFFFFFFu, r.cur != last);
-    const uint32_t prev_not = __ballot_sync(0xFFFFFFFFu, prev != first);
-    const uint32_t next_not = __ballot_sync(0xFFFFFFFFu, r.next != last);
-    const int lead = not_head ? __ffs(not_head) - 1 : 32;        // of the first key
-    const int before = prev_not ? __clz(prev_not) : 32;          // places just before the chunk
-    const int after = next_not ? __ffs(next_not) - 1 : 32;       // places just after it
-    r.skip = first != none && before > 0 ? lead : 0;
-    r.head_long = r.skip > 0 && (before + lead > kChunk);
-    // the tail run: starts in this chunk and goes on in the next
-    const bool goes_on = last != none && after > 0;
-    const int start = not_tail ? 32 - __clz(not_tail) : 0;
-    r.tail = goes_on && !(start == 0 && r.skip > 0) ? start : 32;
-    r.tail_long = r.tail < 32 && (32 - r.tail) + after > kChunk;
-    r.more = r.tail < 32 && !r.tail_long ? after : 0;
-    return r;
-}
-
+template <int C, bool ACC>
 __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_constant__ GradArgs a)
 {
     pdl_enter();
+    constexpr uint32_t ALL = 0xFFFFFFFFu;
     const int lane = threadIdx.x & 31;
     const int64_t w = ((int64_t)blockIdx.x * kGradThreads + threadIdx.x) >> 5;
     const int64_t c = w / a.slices;
-    if (c * kChunk >= a.T) return;
+    if (c >= a.chunks) return;
     const int col = (int)(w % a.slices) * kColumns + lane * 8;
     const bool on = col < a.D;
-    const ChunkRuns r = chunk_runs(a.key, a.T, a.V, c, lane);
+    const int64_t i0 = c * C;
+    const uint32_t pos_cur = lane < C && i0 + lane < a.T ? a.pos[i0 + lane] : 0;
+    const uint32_t pos_next = lane < C && i0 + C + lane < a.T ? a.pos[i0 + C + lane] : 0;
+    const ChunkRuns r = chunk_runs<C>(a.key, a.T, a.V, c, lane);
     if (r.n == 0) return;
-    const int64_t i0 = c * kChunk;
-    const uint32_t pos_cur = i0 + lane < a.T ? a.pos[i0 + lane] : 0;
-    const uint32_t pos_next = i0 + kChunk + lane < a.T ? a.pos[i0 + kChunk + lane] : 0;
 
-    // places [from, to) of the chunk and the 32 after it, a run at a time
+    // places [from, to) of the chunk and the C after it, a batch of rows at a
+    // time: the rows, and what the gradient holds where a run ends, are all
+    // asked for before the first is added
     const int from = r.head_long ? 0 : r.skip;
     const int to = r.n + r.more;
     float acc[8] = {};
-    for (int b = from; b < to; b += kGradBatch) {
-        uint4 x[kGradBatch];
+    for (int b = from; b < to; b += kBatch) {
+        uint4 x[kBatch], old[ACC ? kBatch : 1];
+        uint32_t v[kBatch];
+        uint32_t ends = 0;                                   // bit q: place b + q ends a run
 #pragma unroll
-        for (int q = 0; q < kGradBatch; ++q) {
-            const int s = b + q;
-            const uint32_t p0 = __shfl_sync(0xFFFFFFFFu, pos_cur, s & 31);
-            const uint32_t p1 = __shfl_sync(0xFFFFFFFFu, pos_next, s & 31);
-            const int64_t t = s < 32 ? p0 : p1;
-            x[q] = on && s < to ? ld16_stream(a.dy + t * a.dy_ld + col) : make_uint4(0, 0, 0, 0);
+        for (int q = 0; q < kBatch; ++q) {
+            const int s = b + q, n = s + 1;
+            const uint32_t p0 = __shfl_sync(ALL, pos_cur, s & (C - 1));
+            const uint32_t p1 = __shfl_sync(ALL, pos_next, s & (C - 1));
+            const uint32_t k0 = __shfl_sync(ALL, r.cur, s & (C - 1));
+            const uint32_t k1 = __shfl_sync(ALL, r.next, s & (C - 1));
+            const uint32_t n0 = __shfl_sync(ALL, r.cur, n & (C - 1));
+            const uint32_t n1 = __shfl_sync(ALL, r.next, n & (C - 1));
+            const int64_t t = s < C ? p0 : p1;
+            v[q] = s < C ? k0 : k1;
+            const bool in = s < to;
+            x[q] = on && in ? ld16_stream(a.dy + t * a.dy_ld + col) : make_uint4(0, 0, 0, 0);
+            const bool end = in && (n == to || (n < C ? n0 : n1) != v[q]);
+            if (end) ends |= 1u << q;
+            if constexpr (ACC) {
+                const bool part = (r.head_long && s < r.skip) ||
+                                  (r.tail_long && s >= r.tail && s < C);
+                old[q] = on && end && !part ? ld16(a.grad + (int64_t)v[q] * a.D + col)
+                                            : make_uint4(0, 0, 0, 0);
+            }
         }
 #pragma unroll
-        for (int q = 0; q < kGradBatch; ++q) {
+        for (int q = 0; q < kBatch; ++q) {
             const int s = b + q;
-            if (s >= to) break;
-            add_row(acc, x[q]);
-            const uint32_t k0 = __shfl_sync(0xFFFFFFFFu, r.cur, s & 31);
-            const uint32_t k1 = __shfl_sync(0xFFFFFFFFu, r.next, s & 31);
-            const uint32_t v = s < 32 ? k0 : k1;
-            const uint32_t n0 = __shfl_sync(0xFFFFFFFFu, r.cur, (s + 1) & 31);
-            const uint32_t n1 = __shfl_sync(0xFFFFFFFFu, r.next, (s + 1) & 31);
-            const uint32_t after = s + 1 < 32 ? n0 : n1;
-            const bool ends = s + 1 == to || after != v || (s + 1 == 32 && r.more == 0);
-            if (!ends) continue;
-            if (on) {
-                const bool head = r.head_long && s < r.skip;
-                const bool tail = r.tail_long && s >= r.tail;
-                if (head || tail) {
-                    float* to_part = a.parts + (2 * c + (tail ? 1 : 0)) * a.D + col;
-                    *reinterpret_cast<float4*>(to_part) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                    *reinterpret_cast<float4*>(to_part + 4) =
-                        make_float4(acc[4], acc[5], acc[6], acc[7]);
-                } else {
-                    write_row(a, v, col, acc);
-                }
+            add8(acc, x[q]);
+            if (!(ends >> q & 1)) continue;
+            const bool head = r.head_long && s < r.skip, tail = r.tail_long && s >= r.tail;
+            if (on && (head || tail)) {
+                float* part = a.parts + (2 * c + (tail ? 1 : 0)) * a.D + col;
+                *reinterpret_cast<float4*>(part) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                *reinterpret_cast<float4*>(part + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            } else if (on) {
+                float f[8] = {};
+                if constexpr (ACC) bf_unpack8(old[q], f);
+#pragma unroll
+                for (int z = 0; z < 8; ++z) f[z] += acc[z] * a.scale;
+                st16(a.grad + (int64_t)v[q] * a.D + col, bf_pack8(f));
             }
 #pragma unroll
             for (int z = 0; z < 8; ++z) acc[z] = 0.0f;
@@ -383,50 +413,97 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_consta
     }
 }
 
-// Joins the parts of each long run: the block of the chunk where the run
-// starts adds the tail part of that chunk and the head parts of the next
-// ones.  Each of its 8 warps adds a consecutive share of them, and the shares
-// are added in order.
-__global__ void __launch_bounds__(kGradThreads) k_embed_join(const __grid_constant__ GradArgs a)
+// Joins the parts of each long run: the chunk where the run starts has a tail
+// part, the next ones head parts.  A block looks at 8 chunks (one a warp, a
+// grid's stride apart, since frequent tokens lie together) and then sums the
+// runs it found, its 8 warps a consecutive share of the parts each, and the
+// shares in order.
+template <int C>
+__global__ void __launch_bounds__(kJoinThreads) k_embed_join(const __grid_constant__ GradArgs a)
 {
     pdl_enter();
-    constexpr int W = kGradThreads / 32;
+    constexpr int W = kJoinThreads / 32;
     __shared__ float share[W][kColumns];
+    __shared__ uint32_t run_key[W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = blockIdx.x / a.slices;
+    const int groups = (a.chunks + W - 1) / W;
+    const int group = blockIdx.x / a.slices;
     const int col = (int)(blockIdx.x % a.slices) * kColumns + lane * 8;
-    const ChunkRuns r = chunk_runs(a.key, a.T, a.V, c, lane);
-    if (!r.tail_long) return;                                  // the same in every warp
-    const uint32_t v = __shfl_sync(0xFFFFFFFFu, r.cur, 31);
-    int64_t lo = (c + 1) * kChunk, hi = a.T;                   // the first place past the run
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (a.key[mid] > v) hi = mid;
-        else lo = mid + 1;
+    {
+        const int64_t c = group + (int64_t)warp * groups;
+        uint32_t v = (uint32_t)a.V;
+        if (c < a.chunks) {
+            const ChunkRuns r = chunk_runs<C>(a.key, a.T, a.V, c, lane);
+            if (r.tail_long) v = __shfl_sync(0xFFFFFFFFu, r.cur, C - 1);
+        }
+        if (lane == 0) run_key[warp] = v;
     }
-    const int64_t parts = (lo - 1) / kChunk - c + 1;           // one of each chunk it meets
-    const int64_t each = (parts + W - 1) / W;
-    const int64_t p0 = min(warp * each, parts), p1 = min(p0 + each, parts);
-    float acc[8] = {};
-    if (col < a.D) {
+    __syncthreads();
+    for (int k = 0; k < W; ++k) {
+        const uint32_t v = run_key[k];
+        if (v == (uint32_t)a.V) continue;                      // the same in every warp
+        const int64_t c = group + (int64_t)k * groups;
+        int64_t lo = (c + 1) * C, hi = a.T;                    // the first place past the run
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (a.key[mid] > v) hi = mid;
+            else lo = mid + 1;
+        }
+        const int64_t parts = (lo - 1) / C - c + 1;            // one of each chunk it meets
+        const int64_t each = (parts + W - 1) / W;
+        const int64_t p0 = min(warp * each, parts), p1 = min(p0 + each, parts);
+        float acc[8] = {};
+        if (col < a.D) {
 #pragma unroll 4
-        for (int64_t p = p0; p < p1; ++p) {
-            const float* s = a.parts + (2 * (c + p) + (p == 0 ? 1 : 0)) * a.D + col;
-            const float4 x = *reinterpret_cast<const float4*>(s);
-            const float4 y = *reinterpret_cast<const float4*>(s + 4);
-            acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
-            acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+            for (int64_t p = p0; p < p1; ++p) {
+                const float* s = a.parts + (2 * (c + p) + (p == 0 ? 1 : 0)) * a.D + col;
+                const float4 x = *reinterpret_cast<const float4*>(s);
+                const float4 y = *reinterpret_cast<const float4*>(s + 4);
+                acc[0] += x.x; acc[1] += x.y; acc[2] += x.z; acc[3] += x.w;
+                acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) share[warp][q * 32 + lane] = acc[q];
+        __syncthreads();
+        if (warp == 0 && col < a.D) {
+            for (int j = 1; j < W; ++j)
+#pragma unroll
+                for (int q = 0; q < 8; ++q) acc[q] += share[j][q * 32 + lane];
+            uint16_t* p = a.grad + (int64_t)v * a.D + col;
+            float f[8] = {};
+            if (a.accumulate) bf_unpack8(ld16(p), f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[q] += acc[q] * a.scale;
+            st16(p, bf_pack8(f));
         }
     }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) share[warp][lane * 8 + q] = acc[q];
-    __syncthreads();
-    if (warp == 0 && col < a.D) {
-        for (int k = 1; k < W; ++k)
-#pragma unroll
-            for (int q = 0; q < 8; ++q) acc[q] += share[k][lane * 8 + q];
-        write_row(a, v, col, acc);
+}
+
+// Chunks of 32 places leave the fewest parts; with few tokens chunks of 8
+// give four times the warps, each with one batch of rows to wait for.
+int chunk_places(int64_t T, int32_t D)
+{
+    const int64_t warps = (T + 31) / 32 * ((D + kColumns - 1) / kColumns);
+    return warps >= kFewWarps ? 32 : 8;
+}
+
+template <int C>
+cudaError_t launch_grad(GradArgs a, cudaStream_t st)
+{
+    a.chunks = (int32_t)((a.T + C - 1) / C);
+    const int64_t warps = (int64_t)a.chunks * a.slices;
+    const int per = kGradThreads / 32;
+    const dim3 grid((unsigned)((warps + per - 1) / per));
+    cudaError_t e = launch(a.accumulate ? k_embed_grad<C, true> : k_embed_grad<C, false>, grid,
+                           kGradThreads, 0, 1, st, a);
+    if (e == cudaSuccess && a.T > C) {
+        constexpr int W = kJoinThreads / 32;
+        const int64_t groups = (a.chunks + W - 1) / W;
+        e = launch(k_embed_join<C>, dim3((unsigned)(groups * a.slices)), kJoinThreads, 0, 1, st, a);
     }
+    return e;
 }
 
 struct GradScratch {
@@ -442,8 +519,9 @@ GradScratch grad_scratch(int64_t T, int32_t D)
     s.pos0 = 2 * list;
     s.pos1 = 3 * list;
     s.counts = 4 * list;
-    s.parts = s.counts + 4 * kMaxCluster * kMaxBins;
-    s.bytes = s.parts + 8 * ((T + kChunk - 1) / kChunk) * (int64_t)D;
+    s.parts = s.counts + 2 * 4 * kMaxCluster * kMaxBins;
+    const int C = chunk_places(T, D);
+    s.bytes = s.parts + 8 * ((T + C - 1) / C) * (int64_t)D;
     return s;
 }
 
@@ -513,9 +591,8 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     LM_CHECK(check_tokens(tokens, token_bytes));
     LM_CHECK(check_ptr(scratch));
     LM_CHECK(check_status(dev_status));
-    const int64_t chunks = (T + kChunk - 1) / kChunk;
     const int64_t slices = (D + kColumns - 1) / kColumns;
-    if (chunks * slices > INT32_MAX) return ZERO_ERR_SIZE;         // a launch's blocks
+    if ((T + 31) / 32 * slices > INT32_MAX) return ZERO_ERR_SIZE;  // a launch's warps
     const GradScratch g = grad_scratch(T, D);
     if (scratch_bytes < g.bytes) return ZERO_ERR_SIZE;
     Spans sp;
@@ -532,10 +609,10 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     s.token_bytes = token_bytes;
     s.T = T;
     s.V = V;
-    s.key[0] = reinterpret_cast<uint32_t*>(base + g.key0);
-    s.key[1] = reinterpret_cast<uint32_t*>(base + g.key1);
-    s.pos[0] = reinterpret_cast<uint32_t*>(base + g.pos0);
-    s.pos[1] = reinterpret_cast<uint32_t*>(base + g.pos1);
+    s.key0 = reinterpret_cast<uint32_t*>(base + g.key0);
+    s.key1 = reinterpret_cast<uint32_t*>(base + g.key1);
+    s.pos0 = reinterpret_cast<uint32_t*>(base + g.pos0);
+    s.pos1 = reinterpret_cast<uint32_t*>(base + g.pos1);
     s.counts = reinterpret_cast<uint32_t*>(base + g.counts);
     int key_bits = 1;                                      // keys run to V itself
     while (key_bits < 32 && (V >> key_bits) != 0) ++key_bits;
@@ -561,8 +638,8 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
 
     GradArgs a{};
     a.dy = dy;
-    a.key = s.key[s.passes & 1];
-    a.pos = s.pos[s.passes & 1];
+    a.key = s.passes & 1 ? s.key1 : s.key0;
+    a.pos = s.passes & 1 ? s.pos1 : s.pos0;
     a.grad = grad;
     a.parts = reinterpret_cast<float*>(base + g.parts);
     a.T = T;
@@ -572,10 +649,6 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     a.slices = (int32_t)slices;
     a.accumulate = accumulate;
     a.scale = scale;
-    const int64_t warps = chunks * slices;
-    const int per = kGradThreads / 32;
-    e = launch(k_embed_grad, dim3((unsigned)((warps + per - 1) / per)), kGradThreads, 0, 1, st, a);
-    if (e == cudaSuccess && T > kChunk)
-        e = launch(k_embed_join, dim3((unsigned)warps), kGradThreads, 0, 1, st, a);
+    e = chunk_places(T, D) == 32 ? launch_grad<32>(a, st) : launch_grad<8>(a, st);
     return status_of(e);
 }

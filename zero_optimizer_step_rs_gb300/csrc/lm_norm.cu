@@ -64,12 +64,16 @@ __device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d)
            (uint32_t)(d & 255) << 24;
 }
 
+// Signed bytes as floats without the conversion unit, which has a quarter of
+// the other units' rate: with its sign bit flipped a byte is code + 128, and as
+// the low bits of 2^23 it is that much above 2^23.
 __device__ __forceinline__ void unpack_codes(const uint2& q, float (&f)[8])
 {
+    const uint32_t x = q.x ^ 0x80808080u, y = q.y ^ 0x80808080u;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        f[k] = (float)(int8_t)(q.x >> (8 * k));
-        f[4 + k] = (float)(int8_t)(q.y >> (8 * k));
+        f[k] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7540 | k)) - 8388736.0f;
+        f[4 + k] = __uint_as_float(__byte_perm(y, 0x4B000000u, 0x7540 | k)) - 8388736.0f;
     }
 }
 
@@ -229,7 +233,7 @@ struct NormGradArgs {
 // As k_norm, but a row's threads walk over many rows and keep the sums of dw
 // in registers; a block's row groups are added in order at its end.
 template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_norm_grad(const __grid_constant__ NormGradArgs a)
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 128 ? 1024 / TPR : 8) k_norm_grad(const __grid_constant__ NormGradArgs a)
 {
     constexpr int THREADS = TPR > 128 ? TPR : 128;
     constexpr int GROUPS = THREADS / TPR;
@@ -261,21 +265,23 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_norm_grad(const __gri
                 if (a.dsum) vs[k] = ld16_stream(a.dsum + t * a.dsum_ld + c * 8);
             }
         }
+        // xhat and dy * w are made twice, from the registers that hold the
+        // loads: keeping them would cost 16 registers a vector, and with them
+        // the resident warps that keep enough loads in flight
         float inner = 0.0f;
-        float xh[NV][8], u[NV][8];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = lane + k * TPR;
-            float w[8] = {};
+            float w[8] = {}, xh[8], d[8];
             if (c < nv) bf_unpack8(ld16(a.w + c * 8), w);
-            unpack_codes(vq[k], xh[k]);
-            bf_unpack8(vd[k], u[k]);
+            unpack_codes(vq[k], xh);
+            bf_unpack8(vd[k], d);
+            sc[k] *= rstd;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                xh[k][q] *= sc[k] * rstd;
-                dw[k][q] = fmaf(u[k][q], xh[k][q], dw[k][q]);
-                u[k][q] *= w[q];
-                inner = fmaf(u[k][q], xh[k][q], inner);
+                const float p = d[q] * (xh[q] * sc[k]);
+                dw[k][q] += p;
+                inner = fmaf(p, w[q], inner);
             }
         }
         inner = row_sum<TPR>(inner, slots, slot) / (float)a.D;
@@ -284,10 +290,15 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128) k_norm_grad(const __gri
         for (int k = 0; k < NV; ++k) {
             const int c = lane + k * TPR;
             if (in && c < nv) {
-                float s[8];
+                float s[8], w[8], xh[8], d[8];
+                bf_unpack8(ld16(a.w + c * 8), w);
+                unpack_codes(vq[k], xh);
+                bf_unpack8(vd[k], d);
                 bf_unpack8(vs[k], s);
+                const float back = sc[k] * inner;
 #pragma unroll
-                for (int q = 0; q < 8; ++q) s[q] += rstd * (u[k][q] - xh[k][q] * inner);
+                for (int q = 0; q < 8; ++q)
+                    s[q] = fmaf(rstd, fmaf(d[q], w[q], -xh[q] * back), s[q]);
                 st16_stream(a.dx + t * a.dx_ld + c * 8, bf_pack8(s));
             }
         }
@@ -354,15 +365,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_norm_join(const __grid_constan
     }
 }
 
-int grad_blocks(int64_t T)
-{
-    return (int)std::min<int64_t>(T, 1216);          // at most 8 for each of 152 SMs
-}
+// The most blocks that k_norm_grad takes: 8 for each of 152 SMs, so 8 fp32 rows
+// of parts per SM.
+int grad_blocks(int64_t T) { return (int)std::min<int64_t>(T, 1216); }
 
 }  // namespace
 
 // The widths each form takes: a row of up to 512 columns is one warp's, wider
-// ones are shared by 128 to 512 threads with two or four vectors each.
+// ones are shared by 128 to 1024 threads with one or two vectors each.
 #define NORM_FORMS(F)                  \
     if (D <= 256) return F(32, 1);     \
     if (D <= 512) return F(32, 2);     \
@@ -370,7 +380,7 @@ int grad_blocks(int64_t T)
     if (D <= 2048) return F(128, 2);   \
     if (D <= 4096) return F(256, 2);   \
     if (D <= 8192) return F(512, 2);   \
-    return F(512, 4)
+    return F(1024, 2)
 
 extern "C" zero_status zero_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual,
                                  int64_t residual_ld, const uint16_t* weight, int64_t T, int32_t D,
@@ -516,7 +526,13 @@ extern "C" zero_status zero_norm_grad(const uint16_t* dy, int64_t dy_ld, const u
     a.D = D;
     auto run = [&](void (*kernel)(NormGradArgs), int tpr) {
         const int threads = tpr > 128 ? tpr : 128, groups = threads / tpr;
-        a.blocks = (int)std::min<int64_t>((T + groups - 1) / groups, grad_blocks(T));
+        // as many blocks as are resident at once: a second wave would be a short one
+        int per_sm = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) !=
+                cudaSuccess || per_sm < 1)
+            per_sm = 1;
+        a.blocks = (int)std::min<int64_t>(
+            {(T + groups - 1) / groups, (int64_t)grad_blocks(T), (int64_t)per_sm * device_sms()});
         cudaError_t e = launch(kernel, dim3((unsigned)a.blocks), threads, 0, 1, st, a);
         if (e == cudaSuccess)
             e = launch(k_norm_join, dim3((unsigned)((D + kJoinCols - 1) / kJoinCols)),

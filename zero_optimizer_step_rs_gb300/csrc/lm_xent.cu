@@ -4,15 +4,18 @@
 //
 //   l = h E^T (bf16 products, fp32 sums), lse_t = log sum_v exp(l_tv),
 //   loss_t = lse_t - l_{t, y_t}                       (0 for an ignored token)
-//   P_tv = (exp(l_tv - lse_t) - [v = y_t]) * dloss_t  (0 in an ignored row)
-//   dh = P E,  dE = P^T h
+//   P_tv = (exp(l_tv - lse_t) - [v = y_t]) * dloss_t / u   (0 in an ignored row)
+//   dh = u P E,  dE = u P^T h,  u = max_t |dloss_t|
 //
 // Forward is one matrix product whose epilogue keeps, per row and tile of 256
 // vocabulary rows, a running maximum and the sum of exponentials relative to
 // it; a small second kernel joins the tiles.  Backward keeps nothing but lse: for
 // a piece of the vocabulary at a time it makes the logits again, turns them
 // into P in bf16 (the one rounding before the sums; P is an operand of the
-// tensor cores), and multiplies P with both operands.  The gradient of the
+// tensor cores), and multiplies P with both operands.  Where all tokens weigh
+// the same, as in a mean, dloss / u is exactly 1 and the large entry of a row, exp
+// - 1 near -1, loses next to nothing in bf16; with dloss itself in P its rounding
+// would be the whole row's error.  The gradient of the
 // table's piece is final and written once; dh is summed over the pieces in
 // fp32 and rounded once at the end.
 //
@@ -95,6 +98,7 @@ struct MmaArgs {
     int64_t V, v0;                     // the vocabulary, and where the piece starts
     const float* lse;
     const float* dloss;
+    const float* unit;                 // u
     float2* part;                      // kLse: [n_tiles][part_ld] (maximum, sum)
     int64_t part_ld;
     float* at_target;                  // kLse: the target's logit
@@ -374,8 +378,10 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
         y = target_of(a, row);
         live = y >= 0;
         lse2 = live ? a.lse[row] * kLog2e : 0.0f;
-        g = live ? a.dloss[row] : 0.0f;
+        g = live ? a.dloss[row] / *a.unit : 0.0f;
         y -= a.v0 + c0;
+    } else {
+        g = *a.unit;
     }
 #pragma unroll 1
     for (int c = 0; c < BN; c += 64) {
@@ -399,10 +405,10 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
                     for (int i = 0; i < 32; ++i)
                         if (i == at) x[i] -= 1.0f;
                 }
-                if (live) {
+            }
+            if (live) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] *= g;
-                }
+                for (int i = 0; i < 32; ++i) x[i] *= g;
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -646,9 +652,12 @@ __global__ void __launch_bounds__(1024) k_xent_join(const __grid_constant__ Join
 
 // h with the ignored rows zeroed: their P is zero, but zero times an Inf or a
 // NaN that such a row may hold would reach every row of the table's gradient.
+// Block 0 also finds u, the largest finite |dloss| of the tokens that count.
 struct CleanArgs {
     const uint16_t* h;
     uint16_t* out;
+    const float* dloss;
+    float* unit;
     const void* targets;
     int64_t T, V, h_ld;
     int32_t D, token_bytes;
@@ -659,6 +668,24 @@ __global__ void __launch_bounds__(256) k_clean(const __grid_constant__ CleanArgs
 {
     pdl_enter();
     const int lane = threadIdx.x & 31, nv = a.D >> 3;
+    if (blockIdx.x == 0) {
+        __shared__ float best[8];
+        float u = 0.0f;
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < a.T; i += 256) {
+            const int64_t y = token_at(a.targets, a.token_bytes, i);
+            const float g = fabsf(a.dloss[i]);
+            if (y >= 0 && y < a.V && g < INFINITY) u = fmaxf(u, g);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) u = fmaxf(u, __shfl_xor_sync(0xFFFFFFFFu, u, o));
+        if (lane == 0) best[threadIdx.x >> 5] = u;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int k = 1; k < 8; ++k) u = fmaxf(u, best[k]);
+            *a.unit = u > 0.0f ? u : 1.0f;
+        }
+    }
     const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
     if (t >= a.T) return;
     const int64_t y = token_at(a.targets, a.token_bytes, t);
@@ -672,6 +699,7 @@ __global__ void __launch_bounds__(256) k_clean(const __grid_constant__ CleanArgs
 // dh from its splits' sums, added in order.
 struct FinishArgs {
     const float* sums;
+    const float* unit;
     uint16_t* dh;
     int64_t T, split_rows, dh_ld;
     int32_t D, splits;
@@ -683,6 +711,7 @@ __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishAr
     const int lane = threadIdx.x & 31, nv = a.D >> 3;
     const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
     if (t >= a.T) return;
+    const float unit = *a.unit;
     for (int c = lane; c < nv; c += 32) {
         float f[8] = {};
         for (int s = 0; s < a.splits; ++s) {
@@ -692,6 +721,8 @@ __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishAr
             f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
             f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
         }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] *= unit;
         st16_stream(a.dh + t * a.dh_ld + c * 8, bf_pack8(f));
     }
 }
@@ -766,7 +797,7 @@ LossScratch loss_scratch(int64_t T, int64_t V)
 
 // The backward pass's plan: the piece, the splits of dh's sum, the scratch.
 struct GradPlan {
-    int64_t piece, p, clean, sums, split_rows, bytes;
+    int64_t piece, p, clean, sums, unit, split_rows, bytes;
     int32_t splits;
 };
 
@@ -790,7 +821,8 @@ GradPlan grad_plan(int64_t T, int64_t V, int32_t D, int64_t piece)
     g.clean = up(2 * T * g.piece, 256);
     g.sums = g.clean + up(2 * T * D, 256);
     g.split_rows = up(T, 32);            // an output box never reaches into the next split
-    g.bytes = g.sums + up(4 * g.split_rows * D * g.splits, 256);
+    g.unit = g.sums + up(4 * g.split_rows * D * g.splits, 256);
+    g.bytes = g.unit + 256;
     return g;
 }
 
@@ -918,7 +950,8 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
     uint16_t* clean = reinterpret_cast<uint16_t*>(base + g.clean);
     float* sums = reinterpret_cast<float*>(base + g.sums);
     const unsigned row_blocks = (unsigned)((T + 7) / 8);
-    const CleanArgs ca{h, clean, targets, T, V, h_ld, D, target_bytes, dev_status};
+    float* unit = reinterpret_cast<float*>(base + g.unit);
+    const CleanArgs ca{h, clean, dloss, unit, targets, T, V, h_ld, D, target_bytes, dev_status};
     cudaError_t e = launch(k_clean, dim3(row_blocks), 256, 0, 1, st, ca);
 
     MmaArgs common{};
@@ -927,6 +960,7 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
     common.V = V;
     common.lse = lse;
     common.dloss = dloss;
+    common.unit = unit;
     common.status = dev_status;
     common.wait_limit = flags & ZERO_FLAG_DEBUG_EXPIRE_WAITS ? 0 : kWaitLimit;
     for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += g.piece) {
@@ -974,7 +1008,7 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         e = run_mma<kDtable>(w, st);
     }
     if (e == cudaSuccess) {
-        const FinishArgs f{sums, dh, T, g.split_rows, dh_ld, D, g.splits};
+        const FinishArgs f{sums, unit, dh, T, g.split_rows, dh_ld, D, g.splits};
         e = launch(k_finish, dim3(row_blocks), 256, 0, 1, st, f);
     }
     return status_of(e);
