@@ -169,8 +169,8 @@ def test_scratch_sizes():
     assert L.zero_xent_grad_scratch_bytes(5, 10, 64, 100) == -1
     with pytest.raises(ValueError):
         z.zero_xent_grad_scratch_bytes(5, 10, 60)
-    # the loss keeps 8 bytes per row and 256 vocabulary rows, not the logits
-    assert z.zero_xent_scratch_bytes(8192, 128256, 2048) < 8192 * 128256 * 4 / 100
+    # the loss keeps 8 bytes per row and 128 (or more) vocabulary rows, not the logits
+    assert z.zero_xent_scratch_bytes(8192, 128256, 2048) < 8192 * 128256 * 4 / 50
     # a smaller piece of the vocabulary takes less
     small = z.zero_xent_grad_scratch_bytes(8192, 128256, 2048, 1024)
     assert small < z.zero_xent_grad_scratch_bytes(8192, 128256, 2048) < 8192 * 128256 * 2

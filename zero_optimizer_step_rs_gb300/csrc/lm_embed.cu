@@ -117,7 +117,6 @@ __device__ __forceinline__ void cluster_sync()
 
 __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ SortArgs a)
 {
-    pdl_enter();
     extern __shared__ uint32_t warp_bins[];                 // [kSortWarps][bins]
     __shared__ uint32_t base[kMaxBins], total[kMaxBins], warp_total[kMaxBins / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -497,11 +496,11 @@ cudaError_t launch_grad(GradArgs a, cudaStream_t st)
     const int per = kGradThreads / 32;
     const dim3 grid((unsigned)((warps + per - 1) / per));
     cudaError_t e = launch(a.accumulate ? k_embed_grad<C, true> : k_embed_grad<C, false>, grid,
-                           kGradThreads, 0, 1, st, a);
+                           kGradThreads, 0, st, a);
     if (e == cudaSuccess && a.T > C) {
         constexpr int W = kJoinThreads / 32;
         const int64_t groups = (a.chunks + W - 1) / W;
-        e = launch(k_embed_join<C>, dim3((unsigned)(groups * a.slices)), kJoinThreads, 0, 1, st, a);
+        e = launch(k_embed_join<C>, dim3((unsigned)(groups * a.slices)), kJoinThreads, 0, st, a);
     }
     return e;
 }
@@ -561,7 +560,7 @@ extern "C" zero_status zero_embed(const uint16_t* table, int64_t V, int32_t D, c
     while ((1 << a.lanes_log2) < 32 && (1 << a.lanes_log2) < D / 8) ++a.lanes_log2;
     const int rows = kLookupThreads >> a.lanes_log2;
     const int64_t blocks = (T + rows - 1) / rows;
-    return status_of(launch(k_lookup, dim3((unsigned)blocks), kLookupThreads, 0, 1,
+    return status_of(launch(k_lookup, dim3((unsigned)blocks), kLookupThreads, 0,
                             static_cast<cudaStream_t>(stream), a));
 }
 
@@ -632,8 +631,8 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     static std::atomic<uint64_t> smem_set;
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_sort), kSortSmem, smem_set);
     if (e == cudaSuccess)
-        e = launch(k_sort, dim3((unsigned)(s.cluster + fillers)), kSortThreads,
-                   kSortWarps * (4 << s.bits), s.cluster, st, s);
+        e = launch_clusters(k_sort, dim3((unsigned)(s.cluster + fillers)), kSortThreads,
+                            kSortWarps * (4 << s.bits), s.cluster, st, s);
     if (e != cudaSuccess) return status_of(e);
 
     GradArgs a{};

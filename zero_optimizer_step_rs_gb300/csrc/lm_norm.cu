@@ -230,56 +230,103 @@ struct NormGradArgs {
     int32_t D, blocks;
 };
 
-// As k_norm, but a row's threads walk over many rows and keep the sums of dw
-// in registers; a block's row groups are added in order at its end.
+// Copies from global memory into the thread's own place in shared memory, which
+// only that thread reads: no barrier, only the thread's own wait.  `bytes` 0
+// fills with zeros and reads nothing.
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes)
+{
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
+                     "r"(bytes), "n"(N)
+                     : "memory");
+}
+
+// Rows that a thread has asked for ahead of the one it works on, plus that one.
 template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 128 ? 1024 / TPR : 8) k_norm_grad(const __grid_constant__ NormGradArgs a)
+__host__ __device__ constexpr int grad_stages() { return TPR * NV <= 512 ? 3 : 2; }
+template <int TPR, int NV>
+__host__ __device__ constexpr int grad_smem()
+{
+    return grad_stages<TPR, NV>() * NV * (TPR > 128 ? TPR : 128) * (16 + 16 + 8 + 4);
+}
+
+// As k_norm, but a row's threads walk over many rows and keep the sums of dw
+// in registers; a block's row groups are added in order at its end.  A row has
+// one barrier in its middle, so without loads for later rows a block has
+// nothing in flight for half of the time (measured 5.2 TB/s at 32768 x 2048);
+// registers for them cost the warps that hide the rest, so they wait in shared
+// memory.
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 128 ? 1024 / TPR : 6)
+    k_norm_grad(const __grid_constant__ NormGradArgs a)
 {
     constexpr int THREADS = TPR > 128 ? TPR : 128;
     constexpr int GROUPS = THREADS / TPR;
+    constexpr int S = grad_stages<TPR, NV>();
     pdl_enter();
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float slots[2][32];
+    uint4* ring_d = reinterpret_cast<uint4*>(ring) + threadIdx.x;            // [S][NV][THREADS]
+    uint4* ring_s = ring_d + S * NV * THREADS;
+    uint2* ring_q = reinterpret_cast<uint2*>(ring + S * NV * THREADS * 32) + threadIdx.x;
+    float* ring_c = reinterpret_cast<float*>(ring + S * NV * THREADS * 40) + threadIdx.x;
     const int group = threadIdx.x / TPR, lane = threadIdx.x % TPR;
     const int nv = a.D >> 3;
     const int nb = (a.D + kBlock - 1) / kBlock;
-    float dw[NV][8] = {};
-    int slot = 0;
-    // every group of a block makes the same number of rounds (barriers)
-    for (int64_t t0 = (int64_t)blockIdx.x * GROUPS; t0 < a.T; t0 += (int64_t)gridDim.x * GROUPS) {
-        const int64_t t = t0 + group;
-        const bool in = t < a.T;
-        uint4 vd[NV], vs[NV];
-        uint2 vq[NV];
-        float sc[NV];
-        const float rstd = in ? a.rstd[t] : 0.0f;
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+    const int64_t t00 = (int64_t)blockIdx.x * GROUPS;
+
+    auto ask = [&](int64_t t, int stage) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = lane + k * TPR;
-            vd[k] = vs[k] = make_uint4(0, 0, 0, 0);
-            vq[k] = make_uint2(0, 0);
-            sc[k] = 0.0f;
-            if (in && c < nv) {
-                vd[k] = ld16_stream(a.dy + t * a.dy_ld + c * 8);
-                vq[k] = __ldcs(reinterpret_cast<const uint2*>(a.codes + t * a.D + c * 8));
-                sc[k] = a.scales[t * nb + c / kLanesPerBlock];
-                if (a.dsum) vs[k] = ld16_stream(a.dsum + t * a.dsum_ld + c * 8);
-            }
+            const bool in = t < a.T && c < nv;
+            const int64_t r = in ? t : 0;
+            const int e = in ? c * 8 : 0, at = (stage * NV + k) * THREADS;
+            copy_async<16>((uint32_t)__cvta_generic_to_shared(ring_d + at), a.dy + r * a.dy_ld + e,
+                           in ? 16 : 0);
+            copy_async<8>((uint32_t)__cvta_generic_to_shared(ring_q + at), a.codes + r * a.D + e,
+                          in ? 8 : 0);
+            copy_async<4>((uint32_t)__cvta_generic_to_shared(ring_c + at),
+                          a.scales + r * nb + e / kBlock, in ? 4 : 0);
+            if (a.dsum)
+                copy_async<16>((uint32_t)__cvta_generic_to_shared(ring_s + at),
+                               a.dsum + r * a.dsum_ld + e, in ? 16 : 0);
         }
-        // xhat and dy * w are made twice, from the registers that hold the
-        // loads: keeping them would cost 16 registers a vector, and with them
-        // the resident warps that keep enough loads in flight
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    float dw[NV][8] = {};
+    int slot = 0, stage = 0;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) ask(t00 + group + s * step, s);
+    float rstd_next = t00 + group < a.T ? a.rstd[t00 + group] : 0.0f;
+    // every group of a block makes the same number of rounds (barriers)
+    for (int64_t t0 = t00; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + group;
+        const bool in = t < a.T;
+        const float rstd = rstd_next;
+        rstd_next = t + step < a.T ? a.rstd[t + step] : 0.0f;
+        ask(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);      // the stage freed last
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        // xhat and dy * w are made twice, from what shared memory holds:
+        // keeping them would cost 16 registers a vector
         float inner = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR;
+            const int c = lane + k * TPR, at = (stage * NV + k) * THREADS;
             float w[8] = {}, xh[8], d[8];
             if (c < nv) bf_unpack8(ld16(a.w + c * 8), w);
-            unpack_codes(vq[k], xh);
-            bf_unpack8(vd[k], d);
-            sc[k] *= rstd;
+            unpack_codes(ring_q[at], xh);
+            bf_unpack8(ring_d[at], d);
+            const float sc = ring_c[at] * rstd;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float p = d[q] * (xh[q] * sc[k]);
+                const float p = d[q] * (xh[q] * sc);
                 dw[k][q] += p;
                 inner = fmaf(p, w[q], inner);
             }
@@ -288,21 +335,23 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 128 ? 1024 / TPR 
         slot ^= 1;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR;
+            const int c = lane + k * TPR, at = (stage * NV + k) * THREADS;
             if (in && c < nv) {
-                float s[8], w[8], xh[8], d[8];
+                float s[8] = {}, w[8], xh[8], d[8];
                 bf_unpack8(ld16(a.w + c * 8), w);
-                unpack_codes(vq[k], xh);
-                bf_unpack8(vd[k], d);
-                bf_unpack8(vs[k], s);
-                const float back = sc[k] * inner;
+                unpack_codes(ring_q[at], xh);
+                bf_unpack8(ring_d[at], d);
+                if (a.dsum) bf_unpack8(ring_s[at], s);
+                const float back = ring_c[at] * rstd * inner;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     s[q] = fmaf(rstd, fmaf(d[q], w[q], -xh[q] * back), s[q]);
                 st16_stream(a.dx + t * a.dx_ld + c * 8, bf_pack8(s));
             }
         }
+        stage = stage == S - 1 ? 0 : stage + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     float* part = a.parts + (int64_t)blockIdx.x * a.D;
     if constexpr (GROUPS == 1) {
 #pragma unroll
@@ -364,6 +413,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_norm_join(const __grid_constan
         *reinterpret_cast<uint2*>(a.dw + col) = make_uint2(bf_pack(p.x, p.y), bf_pack(p.z, p.w));
     }
 }
+
+template <int TPR, int NV>
+std::atomic<uint64_t> grad_smem_set;
 
 // The most blocks that k_norm_grad takes: 8 for each of 152 SMs, so 8 fp32 rows
 // of parts per SM.
@@ -438,7 +490,7 @@ extern "C" zero_status zero_norm(const uint16_t* x, int64_t x_ld, const uint16_t
     status_of(launch(k_norm<tpr, nv>,                                                          \
                      dim3((unsigned)((T + (tpr > 128 ? 1 : 128 / tpr) - 1) /                   \
                                      (tpr > 128 ? 1 : 128 / tpr))),                            \
-                     tpr > 128 ? tpr : 128, 0, 1, st, a))
+                     tpr > 128 ? tpr : 128, 0, st, a))
     NORM_FORMS(NORM_GO);
 #undef NORM_GO
 }
@@ -464,7 +516,7 @@ extern "C" zero_status zero_norm_replay(const int8_t* codes, const float* scales
     LM_CHECK(sp.check());
     const ReplayArgs a{codes, scales, rstd, weight, y, T, y_ld, D};
     const int per = kReplayThreads / 32;
-    return status_of(launch(k_replay, dim3((unsigned)((T + per - 1) / per)), kReplayThreads, 0, 1,
+    return status_of(launch(k_replay, dim3((unsigned)((T + per - 1) / per)), kReplayThreads, 0,
                             static_cast<cudaStream_t>(stream), a));
 }
 
@@ -524,22 +576,24 @@ extern "C" zero_status zero_norm_grad(const uint16_t* dy, int64_t dy_ld, const u
     a.dsum_ld = dsum_ld;
     a.dx_ld = dx_ld;
     a.D = D;
-    auto run = [&](void (*kernel)(NormGradArgs), int tpr) {
+    auto run = [&](void (*kernel)(NormGradArgs), int tpr, int smem, std::atomic<uint64_t>& done) {
         const int threads = tpr > 128 ? tpr : 128, groups = threads / tpr;
         // as many blocks as are resident at once: a second wave would be a short one
+        cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
         int per_sm = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, 0) !=
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
                 cudaSuccess || per_sm < 1)
             per_sm = 1;
         a.blocks = (int)std::min<int64_t>(
             {(T + groups - 1) / groups, (int64_t)grad_blocks(T), (int64_t)per_sm * device_sms()});
-        cudaError_t e = launch(kernel, dim3((unsigned)a.blocks), threads, 0, 1, st, a);
+        if (e == cudaSuccess)
+            e = launch(kernel, dim3((unsigned)a.blocks), threads, smem, st, a);
         if (e == cudaSuccess)
             e = launch(k_norm_join, dim3((unsigned)((D + kJoinCols - 1) / kJoinCols)),
-                       kJoinThreads, 0, 1, st, a);
+                       kJoinThreads, 0, st, a);
         return status_of(e);
     };
-#define GRAD_GO(tpr, nv) run(k_norm_grad<tpr, nv>, tpr)
+#define GRAD_GO(tpr, nv) run(k_norm_grad<tpr, nv>, tpr, grad_smem<tpr, nv>(), grad_smem_set<tpr, nv>)
     NORM_FORMS(GRAD_GO);
 #undef GRAD_GO
 }

@@ -26,8 +26,8 @@
 // tile of fp32 sums in tensor memory, 128 rows in each CTA, two tiles deep, so
 // that one tile's epilogue runs under the next tile's products.  Warp 0 of each
 // CTA brings its half of both operands into shared memory with TMA (64 wide
-// along the summed dimension, 128-byte swizzle, 6 or 7 stages), one thread of
-// the first CTA issues the products, warps 4-7 run the epilogue.  An operand
+// along the summed dimension, 128-byte swizzle, 6 stages), one thread of
+// the first CTA issues the products, warps 4-11 run the epilogue.  An operand
 // may be contiguous along the summed dimension or along the other one; both
 // are read as they lie in memory, nothing is transposed.
 //
@@ -46,13 +46,15 @@ using namespace lm;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-constexpr int BM = 256, BN = 256, BK = 64;         // a CTA pair's tile and one stage's depth
-constexpr int kThreads = 256;
+constexpr int BM = 256, BN = 256, BK = 64;         // a CTA pair's largest tile, a stage's depth
+constexpr int kEpilogueWarps = 8;                  // two for each quarter of the tensor memory
+constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kStageBytes = 2 * 128 * BK * 2;      // per CTA: 128 rows of each operand
 constexpr int kPieceAlign = 256;
-constexpr uint32_t kWaitLimit = 1u << 22;
-constexpr uint32_t kDrainLimit = 1u << 24;
-constexpr int kWarpStage = 4096;                   // an epilogue warp's output buffer (two of them)
+constexpr uint64_t kWaitLimit = 1000000000;        // ns that a wait may take
+constexpr uint64_t kDrainLimit = 1000000000;
+constexpr int kWarpStage = 4096;                   // an epilogue warp's output buffer
+constexpr int kStaging = kEpilogueWarps * kWarpStage;
 
 enum Kind { kLse, kDlogits, kDtable, kDh };
 
@@ -61,7 +63,7 @@ struct Form;
 template <>
 struct Form<kLse> {
     static constexpr bool a_k = true, b_k = true, out = false;
-    static constexpr int stages = 7;
+    static constexpr int stages = 6;
 };
 template <>
 struct Form<kDlogits> {
@@ -79,15 +81,17 @@ struct Form<kDh> {
     static constexpr int stages = 6;
 };
 
+constexpr int kShares = 2 * 128 * 8;               // kLse: the second half's (maximum, sum)
+
 template <Kind K>
 constexpr int smem_bytes()
 {
-    return 1024 + Form<K>::stages * kStageBytes + (Form<K>::out ? 4 * 2 * kWarpStage : 0) + 256;
+    return 1024 + Form<K>::stages * kStageBytes + (Form<K>::out ? kStaging : kShares) + 256;
 }
 
 struct MmaArgs {
     CUtensorMap a, b, out;
-    int32_t m_tiles, n_tiles;          // tiles of 256 x 256
+    int32_t m_tiles, n_tiles, bn;      // tiles of 256 x bn
     int32_t k_blocks, splits;          // blocks of 64 along the summed dimension; its splits
     int32_t m_fast;                    // which tile coordinate runs fastest
     int64_t rows, cols;                // of the result (cols: of the piece)
@@ -103,7 +107,7 @@ struct MmaArgs {
     int64_t part_ld;
     float* at_target;                  // kLse: the target's logit
     int32_t* status;
-    uint32_t wait_limit;
+    uint64_t wait_limit;               // ns
 };
 
 // ------------------------------------------------------------ PTX pieces --
@@ -155,14 +159,41 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
         : "memory");
     return ok != 0;
 }
-// Wait for a phase; gives up after `limit` tries, or once another role of the
-// CTA has given up.  False: the caller leaves its loop.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t limit,
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Wait for a phase; gives up after `limit` ns (at once if that is 0), or once
+// another role of the CTA has given up.  False: the caller leaves its loop.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit,
                                           volatile int* dead)
 {
-    for (uint32_t i = 0; i < limit; ++i) {
+    if (limit != 0) {
         if (mbar_try(bar, parity)) return true;
-        if ((i & 63) == 63 && *dead) return false;
+        const uint64_t start = now_ns();
+        do {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i)
+                if (mbar_try(bar, parity)) return true;
+        } while (!*dead && now_ns() - start < limit);
+    }
+    *dead = 1;
+    return false;
+}
+// The same by a whole warp, whose lanes stay together.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, uint64_t limit,
+                                          volatile int* dead)
+{
+    if (limit != 0) {
+        if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
+        const uint64_t start = now_ns();
+        do {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i)
+                if (__all_sync(0xFFFFFFFFu, mbar_try(bar, parity))) return true;
+        } while (!__any_sync(0xFFFFFFFFu, *dead || now_ns() - start >= limit));
     }
     *dead = 1;
     return false;
@@ -249,12 +280,12 @@ __host__ __device__ constexpr uint64_t operand_step()               // 16 furthe
 {
     return (K_MAJOR ? 32 : 2048) >> 4;
 }
-// fp32 sums, bf16 operands, 256 x 256
+// fp32 sums, bf16 operands, 256 x bn
 template <Kind K>
-__host__ __device__ constexpr uint32_t instruction()
+__device__ __forceinline__ uint32_t instruction(int bn)
 {
     return 1u << 4 | 1u << 7 | 1u << 10 | (Form<K>::a_k ? 0u : 1u << 15) |
-           (Form<K>::b_k ? 0u : 1u << 16) | (uint32_t)(BN >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
+           (Form<K>::b_k ? 0u : 1u << 16) | (uint32_t)(bn >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
 }
 
 // One operand's 128 rows of a stage.
@@ -299,16 +330,30 @@ __device__ __forceinline__ int64_t target_of(const MmaArgs& a, int64_t row)
     return y < a.V ? y : -1;
 }
 
-// The row's running maximum (in units of log 2) and sum over the tile's columns.
-__device__ __forceinline__ void epilogue_lse(const MmaArgs& a, const Unit& t, uint32_t tmem,
-                                             int64_t row)
+// The joint (maximum, sum) of two parts of a row; maxima in units of log 2.
+__device__ __forceinline__ void join(float& m, float& s, float2 x)
 {
-    const int64_t c0 = (int64_t)t.n * BN;
-    const int live = (int)min((int64_t)BN, a.V - c0);
+    const float top = fmaxf(m, x.x);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    s = s * exp2_fast(m - ref) + x.y * exp2_fast(x.x - ref);
+    m = top;
+}
+
+// The row's running maximum and sum over the tile's columns, 128 of them by
+// each of two warps: the second leaves its part in `share` and arrives at
+// `ready`, the first joins the two.  There are two of both, used by turns; a
+// tile's are free again once the first warp has given up the tile's sums, without
+// which the products two tiles on do not start.
+__device__ __forceinline__ bool epilogue_lse(const MmaArgs& a, const Unit& t, uint32_t tmem,
+                                             int64_t row, int half, float2* share, uint32_t ready,
+                                             uint32_t parity, volatile int* dead)
+{
+    const int64_t c0 = (int64_t)t.n * a.bn;
+    const int live = (int)min((int64_t)a.bn, a.V - c0);
     const int64_t y = target_of(a, row) - c0;                // of the tile, if in it
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 32) {
+    for (int c = half * 128; c < half * 128 + 128; c += 32) {
         if (c >= live) break;
         float x[32];
         tmem_load32(tmem + c, x);
@@ -325,6 +370,7 @@ __device__ __forceinline__ void epilogue_lse(const MmaArgs& a, const Unit& t, ui
                 if (i == at) v = x[i];
             a.at_target[row] = v;
         }
+        __syncwarp();                                        // together at the next load
         float m = x[0];
 #pragma unroll
         for (int i = 1; i < 32; ++i) m = fmaxf(m, x[i]);
@@ -337,7 +383,19 @@ __device__ __forceinline__ void epilogue_lse(const MmaArgs& a, const Unit& t, ui
         sum += (s[0] + s[1]) + (s[2] + s[3]);
         top = m;
     }
-    if (row < a.rows) a.part[(int64_t)t.n * a.part_ld + row] = make_float2(top, sum);
+    if (half == 1) {
+        *share = make_float2(top, sum);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(ready) : "memory");
+        return true;
+    }
+    const bool ok = warp_wait(ready, parity, a.wait_limit, dead);
+    if (ok && row < a.rows) {
+        join(top, sum, *share);
+        a.part[(int64_t)t.n * a.part_ld + row] = make_float2(top, sum);
+    }
+    return ok;
 }
 
 // 16 bytes at (row, chunk) of a 32-row buffer of 128-byte rows, 128-byte swizzle.
@@ -350,10 +408,10 @@ __device__ __forceinline__ void stage16(uint32_t buf, int row, int chunk, uint32
                  : "memory");
 }
 
-// A buffer is free once at most one later store still reads its own.
+// The buffer is free once the last store has read it.
 __device__ __forceinline__ void stage_free(int lane)
 {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
 }
 __device__ __forceinline__ void stage_full()
@@ -363,12 +421,12 @@ __device__ __forceinline__ void stage_full()
 }
 
 // The tile's 128 rows of this CTA in bf16 (P, or the table's gradient): 64
-// columns at a time through the warp's two buffers.
+// columns at a time through the warp's buffer, 128 columns a warp.
 template <Kind K>
 __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, uint32_t tmem,
-                                              int64_t row0, int lane, uint32_t buf, int& flip)
+                                              int64_t row0, int lane, int half, uint32_t to)
 {
-    const int64_t c0 = (int64_t)t.n * BN;
+    const int64_t c0 = (int64_t)t.n * a.bn;
     if (row0 >= a.rows) return;
     const int64_t row = row0 + lane;
     int64_t y = -1;
@@ -384,11 +442,8 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
         g = *a.unit;
     }
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 64) {
+    for (int c = half * 128; c < min(a.bn, half * 128 + 128); c += 64) {
         if (c0 + c >= a.cols) break;
-        const uint32_t to = buf + flip * kWarpStage;
-        flip ^= 1;
-        stage_free(lane);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float x[32];
@@ -405,11 +460,13 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
                     for (int i = 0; i < 32; ++i)
                         if (i == at) x[i] -= 1.0f;
                 }
+                __syncwarp();
             }
             if (live) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] *= g;
             }
+            if (h == 0) stage_free(lane);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 stage16(to, lane, 4 * h + j, bf_pack(x[8 * j], x[8 * j + 1]),
@@ -427,18 +484,16 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
 // dh's partial sums in fp32, 32 columns at a time; each element gets one
 // addition per launch, so the order of the sum is the order of the pieces.
 __device__ __forceinline__ void epilogue_f32(const MmaArgs& a, const Unit& t, uint32_t tmem,
-                                             int64_t row0, int lane, uint32_t buf, int& flip)
+                                             int64_t row0, int lane, int half, uint32_t to)
 {
-    const int64_t c0 = (int64_t)t.n * BN;
+    const int64_t c0 = (int64_t)t.n * a.bn;
     if (row0 >= a.rows) return;
 #pragma unroll 1
-    for (int c = 0; c < BN; c += 32) {
+    for (int c = half * 128; c < min(a.bn, half * 128 + 128); c += 32) {
         if (c0 + c >= a.cols) break;
-        const uint32_t to = buf + flip * kWarpStage;
-        flip ^= 1;
-        stage_free(lane);
         float x[32];
         tmem_load32(tmem + c, x);
+        stage_free(lane);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             stage16(to, lane, j, __float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
@@ -456,7 +511,7 @@ __device__ __forceinline__ void epilogue_f32(const MmaArgs& a, const Unit& t, ui
 // ------------------------------------------------------------ the product --
 
 template <Kind K>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     k_mma(const __grid_constant__ MmaArgs a)
 {
     using F = Form<K>;
@@ -465,11 +520,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the swizzle pattern needs 1024-byte aligned stages, at the same place in both CTAs
     const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t staging = smem + S * kStageBytes;
-    const uint32_t bars = staging + (F::out ? 4 * 2 * kWarpStage : 0);
+    const uint32_t bars = staging + (F::out ? kStaging : kShares);
     const uint32_t full = bars, empty = bars + 8 * S;
     const uint32_t sums_full = empty + 8 * S, sums_empty = sums_full + 16;
     const uint32_t drained = sums_empty + 16;
-    const uint32_t slot = drained + 8;
+    const uint32_t shared_full = drained + 8;            // kLse: [2][4], a quarter's second half
+    const uint32_t slot = shared_full + 64;
     volatile int* dead = reinterpret_cast<volatile int*>(raw + (slot + 4 - smem_u32(raw)));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -482,9 +538,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(sums_full + 8 * b, 1);
-            mbar_init(sums_empty + 8 * b, 8);           // 4 warps of each CTA
+            mbar_init(sums_empty + 8 * b, 2 * kEpilogueWarps);    // of both CTAs
         }
         mbar_init(drained, 1);
+        for (int q = 0; q < 8; ++q) mbar_init(shared_full + 8 * q, 1);
         *dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -499,7 +556,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     uint32_t tmem;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
-    pdl_enter();
     asm volatile("fence.proxy.async.global;" ::: "memory");
 
     const int units = a.m_tiles * a.n_tiles * a.splits;
@@ -509,13 +565,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0 && lane == 0) {                        // ---- loads
         uint32_t it = 0;
         bool ok = true;
+        // both CTAs' boxes of a stage (a box always counts in full)
+        const uint32_t stage_tx = 2 * (kStageBytes / 2 + (F::b_k ? a.bn / 2 * 128 : kStageBytes / 2));
         for (int u = first; u < units && ok; u += stride) {
             const Unit t = unit_at(a, u);
-            const int ra = t.m * BM + (int)rank * 128, rb = t.n * BN + (int)rank * 128;
+            const int ra = t.m * BM + (int)rank * 128, rb = t.n * a.bn + (int)rank * (a.bn / 2);
             for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
                 const uint32_t s = it % S, ph = (it / S) & 1;
                 if (!(ok = mbar_wait(empty + 8 * s, ph ^ 1, a.wait_limit, dead))) break;
-                if (leader) mbar_expect(full + 8 * s, 2 * kStageBytes);
+                if (leader) mbar_expect(full + 8 * s, stage_tx);
                 const uint32_t dst = smem + s * kStageBytes;
                 const uint32_t bar = in_leader(full + 8 * s);
                 load_operand<F::a_k>(dst, &a.a, ra, kb * BK, bar);
@@ -536,6 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 drain_failed |= !mbar_wait(full + 8 * (j % S), (j / S) & 1, kDrainLimit, &none);
         }
     } else if (warp == 1 && lane == 0 && leader) {       // ---- products
+        const uint32_t idesc = instruction<K>(a.bn);
         uint32_t it = 0;
         int i = 0;
         bool ok = true;
@@ -554,7 +613,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int q = 0; q < BK / 16; ++q)
                     mma(tmem + b * BN, da + q * operand_step<F::a_k>(),
-                        db + q * operand_step<F::b_k>(), instruction<K>(), kb > t.k0 || q > 0);
+                        db + q * operand_step<F::b_k>(), idesc, kb > t.k0 || q > 0);
                 mma_commit(empty + 8 * s);
             }
             if (ok) mma_commit(sums_full + 8 * b);
@@ -565,20 +624,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             drain_failed |= !mbar_wait(drained, 0, kDrainLimit, &none);
         }
     } else if (warp >= 4) {                              // ---- epilogue
-        const int q = warp - 4;                          // the warp's quarter of the lanes
-        const uint32_t buf = staging + q * 2 * kWarpStage;
-        int i = 0, flip = 0;
+        const int q = warp & 3;                          // the warp's quarter of the lanes
+        const int half = (warp - 4) >> 2;                // and half of the columns
+        const uint32_t buf = staging + (warp - 4) * kWarpStage;
+        float2* share = reinterpret_cast<float2*>(raw + (staging - smem_u32(raw))) + q * 32 + lane;
+        int i = 0;
         for (int u = first; u < units; u += stride, ++i) {
             const Unit t = unit_at(a, u);
             const int b = i & 1;
-            const bool ok = mbar_wait(sums_full + 8 * b, (i >> 1) & 1, a.wait_limit, dead);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (!warp_wait(sums_full + 8 * b, (i >> 1) & 1, a.wait_limit, dead)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t from = tmem + b * BN + ((uint32_t)(q * 32) << 16);
             const int64_t row0 = (int64_t)t.m * BM + rank * 128 + q * 32;
-            if constexpr (K == kLse) epilogue_lse(a, t, from, row0 + lane);
-            else if constexpr (K == kDh) epilogue_f32(a, t, from, row0, lane, buf, flip);
-            else epilogue_bf16<K>(a, t, from, row0, lane, buf, flip);
+            if constexpr (K == kLse) {
+                if (!epilogue_lse(a, t, from, row0 + lane, half, share + b * 128,
+                                  shared_full + 8 * (4 * b + q), (i >> 1) & 1, dead))
+                    break;
+            } else if constexpr (K == kDh) epilogue_f32(a, t, from, row0, lane, half, buf);
+            else epilogue_bf16<K>(a, t, from, row0, lane, half, buf);
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(in_leader(sums_empty + 8 * b));
@@ -609,14 +672,6 @@ struct JoinArgs {
     float* lse;
     int32_t* status;
 };
-
-__device__ __forceinline__ void join(float& m, float& s, float2 x)
-{
-    const float top = fmaxf(m, x.x);
-    const float ref = top == -INFINITY ? 0.0f : top;
-    s = s * exp2_fast(m - ref) + x.y * exp2_fast(x.x - ref);
-    m = top;
-}
 
 __global__ void __launch_bounds__(1024) k_xent_join(const __grid_constant__ JoinArgs a)
 {
@@ -708,23 +763,24 @@ struct FinishArgs {
 __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishArgs a)
 {
     pdl_enter();
-    const int lane = threadIdx.x & 31, nv = a.D >> 3;
-    const int64_t t = ((int64_t)blockIdx.x * 256 + threadIdx.x) >> 5;
+    const int nv = a.D >> 3;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t t = i / nv;
     if (t >= a.T) return;
+    const int c = (int)(i - t * nv) * 8;
     const float unit = *a.unit;
-    for (int c = lane; c < nv; c += 32) {
-        float f[8] = {};
-        for (int s = 0; s < a.splits; ++s) {
-            const float* p = a.sums + (s * a.split_rows + t) * a.D + c * 8;
-            const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
-            const float4 y = __ldcs(reinterpret_cast<const float4*>(p + 4));
-            f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-            f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) f[q] *= unit;
-        st16_stream(a.dh + t * a.dh_ld + c * 8, bf_pack8(f));
+    float f[8] = {};
+#pragma unroll 4
+    for (int s = 0; s < a.splits; ++s) {
+        const float* p = a.sums + (s * a.split_rows + t) * a.D + c;
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+        const float4 y = __ldcs(reinterpret_cast<const float4*>(p + 4));
+        f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+        f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
     }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[q] *= unit;
+    st16_stream(a.dh + t * a.dh_ld + c, bf_pack8(f));
 }
 
 // ------------------------------------------------------------------- host --
@@ -767,7 +823,28 @@ bool encode(CUtensorMap* map, const void* p, bool f32, int64_t cols, int64_t row
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int tiles(int64_t n) { return (int)((n + 255) / 256); }
+int tiles(int64_t n, int width = 256) { return (int)((n + width - 1) / width); }
+
+// The tile width along n (a multiple of `step`, 128 to 256): the one for which
+// the CTA pair with the most tiles has the least to do, a tile's time being
+// taken as that of its columns and 64 more (it reads the same 256 rows of the
+// other operand however narrow it is: without the 64, tiles of 128 and 192
+// were chosen at 8192 x 128256 x 2048 and made the gradient 40 % slower).  With
+// many tiles that is 256; with few it evens out the last round.
+int tile_width(int64_t n, int64_t m_tiles, int64_t splits, int step)
+{
+    const int64_t pairs = std::max(1, device_sms() / 2);
+    int best = 256;
+    int64_t least = INT64_MAX;
+    for (int w = 256; w >= 128; w -= step) {
+        const int64_t cost = (m_tiles * tiles(n, w) * splits + pairs - 1) / pairs * (w + 64);
+        if (cost < least) {
+            least = cost;
+            best = w;
+        }
+    }
+    return best;
+}
 
 template <Kind K>
 cudaError_t run_mma(const MmaArgs& a, cudaStream_t st)
@@ -778,7 +855,8 @@ cudaError_t run_mma(const MmaArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return e;
     const int units = a.m_tiles * a.n_tiles * a.splits;
     const int pairs = std::max(1, std::min(units, device_sms() / 2));
-    return launch(k_mma<K>, dim3((unsigned)(2 * pairs)), kThreads, smem_bytes<K>(), 1, st, a);
+    return launch_clusters(k_mma<K>, dim3((unsigned)(2 * pairs)), kThreads, smem_bytes<K>(), 2, st,
+                           a);
 }
 
 struct LossScratch {
@@ -790,7 +868,7 @@ LossScratch loss_scratch(int64_t T, int64_t V)
     LossScratch s;
     s.part_ld = up(T, 32);
     s.part = 0;
-    s.at_target = up(8 * s.part_ld * (int64_t)tiles(V), 256);
+    s.at_target = up(8 * s.part_ld * (int64_t)tiles(V, 128), 256);      // of the narrowest tiles
     s.bytes = s.at_target + up(4 * T, 256);
     return s;
 }
@@ -834,8 +912,8 @@ zero_status check_xent(int64_t T, int64_t V, int32_t D, int32_t target_bytes, in
     if (flags & ~ZERO_FLAG_DEBUG_EXPIRE_WAITS) return ZERO_ERR_INVALID_ARG;
     if (flags && !dev_status) return ZERO_ERR_NULL;
     // the units of a launch are counted in 32 bits
-    if ((int64_t)tiles(T) * tiles(V) > INT32_MAX / 2 || (int64_t)tiles(V) * tiles(D) > INT32_MAX / 2 ||
-        (int64_t)tiles(T) * tiles(D) > INT32_MAX / 2)
+    const int64_t t = tiles(T, 128), v = tiles(V, 128), d = tiles(D, 128);
+    if (t * v > INT32_MAX / 2 || v * d > INT32_MAX / 2 || t * d > INT32_MAX / 2)
         return ZERO_ERR_SIZE;
     return check_status(dev_status);
 }
@@ -876,10 +954,11 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
 
     uint8_t* base = static_cast<uint8_t*>(scratch);
     MmaArgs a{};
-    if (!encode(&a.a, h, false, D, T, h_ld, 128) || !encode(&a.b, table, false, D, V, D, 128))
-        return ZERO_ERR_CUDA;
     a.m_tiles = tiles(T);
-    a.n_tiles = tiles(V);
+    a.bn = tile_width(V, a.m_tiles, 1, 16);
+    a.n_tiles = tiles(V, a.bn);
+    if (!encode(&a.a, h, false, D, T, h_ld, 128) || !encode(&a.b, table, false, D, V, D, a.bn / 2))
+        return ZERO_ERR_CUDA;
     a.k_blocks = (D + BK - 1) / BK;
     a.splits = 1;
     a.m_fast = 1;
@@ -898,7 +977,7 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
     if (e == cudaSuccess) {
         const JoinArgs j{a.part, a.at_target, targets, s.part_ld, T, V, a.n_tiles, target_bytes,
                          loss, lse, dev_status};
-        e = launch(k_xent_join, dim3((unsigned)((T + 31) / 32)), 1024, 0, 1, st, j);
+        e = launch(k_xent_join, dim3((unsigned)((T + 31) / 32)), 1024, 0, st, j);
     }
     return status_of(e);
 }
@@ -952,7 +1031,7 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
     const unsigned row_blocks = (unsigned)((T + 7) / 8);
     float* unit = reinterpret_cast<float*>(base + g.unit);
     const CleanArgs ca{h, clean, dloss, unit, targets, T, V, h_ld, D, target_bytes, dev_status};
-    cudaError_t e = launch(k_clean, dim3(row_blocks), 256, 0, 1, st, ca);
+    cudaError_t e = launch(k_clean, dim3(row_blocks), 256, 0, st, ca);
 
     MmaArgs common{};
     common.token_bytes = target_bytes;
@@ -968,11 +1047,13 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         const uint16_t* rows = table + v0 * D;
 
         MmaArgs p = common;                                 // P = f(h E^T)
-        if (!encode(&p.a, h, false, D, T, h_ld, 128) || !encode(&p.b, rows, false, D, n, D, 128) ||
+        p.m_tiles = tiles(T);
+        p.bn = tile_width(n, p.m_tiles, 1, 64);
+        p.n_tiles = tiles(n, p.bn);
+        if (!encode(&p.a, h, false, D, T, h_ld, 128) ||
+            !encode(&p.b, rows, false, D, n, D, p.bn / 2) ||
             !encode(&p.out, P, false, n, T, g.piece, 32))
             return ZERO_ERR_CUDA;
-        p.m_tiles = tiles(T);
-        p.n_tiles = tiles(n);
         p.k_blocks = (D + BK - 1) / BK;
         p.splits = 1;
         p.m_fast = 1;
@@ -985,10 +1066,11 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         if (!encode(&d.a, P, false, n, T, g.piece, 128) || !encode(&d.b, rows, false, D, n, D, 64) ||
             !encode(&d.out, sums, true, D, g.split_rows * g.splits, D, 32))
             return ZERO_ERR_CUDA;
-        d.m_tiles = tiles(T);
-        d.n_tiles = tiles(D);
         d.k_blocks = (int32_t)((n + BK - 1) / BK);
         d.splits = std::min(g.splits, d.k_blocks);
+        d.m_tiles = tiles(T);
+        d.bn = tile_width(D, d.m_tiles, d.splits, 64);
+        d.n_tiles = tiles(D, d.bn);
         d.rows = T;
         d.cols = D;
         d.out_split_rows = g.split_rows;
@@ -1000,7 +1082,8 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
             !encode(&w.out, dtable + v0 * D, false, D, n, D, 32))
             return ZERO_ERR_CUDA;
         w.m_tiles = tiles(n);
-        w.n_tiles = tiles(D);
+        w.bn = tile_width(D, w.m_tiles, 1, 64);
+        w.n_tiles = tiles(D, w.bn);
         w.k_blocks = (int32_t)((T + BK - 1) / BK);
         w.splits = 1;
         w.rows = n;
@@ -1009,7 +1092,7 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
     }
     if (e == cudaSuccess) {
         const FinishArgs f{sums, unit, dh, T, g.split_rows, dh_ld, D, g.splits};
-        e = launch(k_finish, dim3(row_blocks), 256, 0, 1, st, f);
+        e = launch(k_finish, dim3((unsigned)((T * (D / 8) + 255) / 256)), 256, 0, st, f);
     }
     return status_of(e);
 }

@@ -21,6 +21,7 @@ from .binding import (ZERO_NORM_BLOCK, ZERO_OK, ZeroError, _check, lib)
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _bf16, _f32, _i8 = torch.bfloat16, torch.float32, torch.int8
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
 def _stream(stream, t):
@@ -31,43 +32,45 @@ def _stream(stream, t):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _cuda(t, dtype, name):
+def _refuse(t, dtype, shape, name):
+    """Says why a tensor was refused.  (The checks themselves are one condition:
+    for a small call they are a good part of its time.)"""
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name}: " + ("columns" if t.dim() == 2 else "elements") +
+                     " must be contiguous")
 
 
-def _rows(t, T, D, name):
+def _rows(t, shape, name):
     """Address and row stride of a [T, D] bf16 matrix with contiguous columns."""
-    _cuda(t, _bf16, name)
-    if t.shape != (T, D):
-        raise ValueError(f"{name}: expected shape ({T}, {D}), got {tuple(t.shape)}")
-    ld, step = t.stride()
-    if step != 1:
-        raise ValueError(f"{name}: columns must be contiguous")
-    return t.data_ptr(), ld if T > 1 else D
+    if t.dtype is _bf16 and t.is_cuda and t.shape == shape:
+        ld, step = t.stride()
+        if step == 1:
+            return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+    _refuse(t, _bf16, shape, name)
 
 
 def _dense(t, dtype, shape, name):
     """Address of a contiguous tensor of that type and shape."""
-    _cuda(t, dtype, name)
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: tensor must be contiguous")
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, dtype, shape, name)
 
 
 def _ids(t, name):
     """Address, bytes an id, and number of the token ids."""
-    if t.dtype not in (torch.int32, torch.int64):
+    width = _ID_BYTES.get(t.dtype)
+    if width is None:
         raise TypeError(f"{name}: expected int32 or int64, got {t.dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
     if t.dim() != 1 or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous vector")
-    return t.data_ptr(), t.element_size(), t.shape[0]
+    return t.data_ptr(), width, t.shape[0]
 
 
 def _scratch(t):
@@ -81,9 +84,8 @@ def _scratch(t):
 def _status(t):
     if t is None:
         return None
-    _cuda(t, torch.int32, "dev_status")
-    if t.numel() < 1:
-        raise ValueError("dev_status: need 1 element")
+    if t.dtype is not torch.int32 or not t.is_cuda or t.numel() < 1:
+        raise ValueError("dev_status: expected an int32 CUDA tensor")
     return t.data_ptr()
 
 
@@ -105,7 +107,7 @@ def zero_embed(table, tokens, out, scale: float = 1.0, dev_status=None, stream=N
     """out[t] = scale * table[tokens[t]] (zeros for a negative id)."""
     V, D = _table(table, "table")
     ids, width, T = _ids(tokens, "tokens")
-    dst, ld = _rows(out, T, D, "out")
+    dst, ld = _rows(out, (T, D), "out")
     code = lib().zero_embed(_dense(table, _bf16, (V, D), "table"), V, D, ids, width, T, scale, dst,
                             ld, _status(dev_status), _stream(stream, table))
     if code != ZERO_OK:
@@ -122,7 +124,7 @@ def zero_embed_grad(dy, tokens, grad, scratch, scale: float = 1.0, accumulate: b
     with accumulate, added to what the rows met hold."""
     V, D = _table(grad, "grad")
     ids, width, T = _ids(tokens, "tokens")
-    src, ld = _rows(dy, T, D, "dy")
+    src, ld = _rows(dy, (T, D), "dy")
     room, size = _scratch(scratch)
     _check(lib().zero_embed_grad(src, ld, ids, width, T, scale, V, D,
                                  _dense(grad, _bf16, (V, D), "grad"), 1 if accumulate else 0, room,
@@ -138,10 +140,10 @@ def zero_norm(x, weight, y, codes, scales, rstd, residual=None, sum_out=None, ep
     and the 8-bit checkpoint (codes [T, D] int8, scales [T, ceil(D / 128)]
     fp32; None for both keeps none) with rstd [T] fp32."""
     T, D = _table(x, "x")
-    src, x_ld = _rows(x, T, D, "x")
-    dst, y_ld = _rows(y, T, D, "y")
-    res, res_ld = _rows(residual, T, D, "residual") if residual is not None else (None, 0)
-    total, sum_ld = _rows(sum_out, T, D, "sum_out") if sum_out is not None else (None, 0)
+    src, x_ld = _rows(x, (T, D), "x")
+    dst, y_ld = _rows(y, (T, D), "y")
+    res, res_ld = _rows(residual, (T, D), "residual") if residual is not None else (None, 0)
+    total, sum_ld = _rows(sum_out, (T, D), "sum_out") if sum_out is not None else (None, 0)
     blocks = (T, -(-D // ZERO_NORM_BLOCK))
     _check(lib().zero_norm(src, x_ld, res, res_ld, _dense(weight, _bf16, (D,), "weight"), T, D, eps,
                            dst, y_ld, total, sum_ld,
@@ -160,7 +162,7 @@ def _checkpoint(codes, scales, rstd, weight):
 def zero_norm_replay(codes, scales, rstd, weight, y, stream=None) -> None:
     """The normalised activation rebuilt from the checkpoint."""
     T, D, kept = _checkpoint(codes, scales, rstd, weight)
-    dst, ld = _rows(y, T, D, "y")
+    dst, ld = _rows(y, (T, D), "y")
     _check(lib().zero_norm_replay(*kept, T, D, dst, ld, _stream(stream, y)), "zero_norm_replay")
 
 
@@ -173,9 +175,9 @@ def zero_norm_grad(dy, codes, scales, rstd, weight, dx, dweight, scratch, dsum=N
     """dx (the gradient of x and of the residual alike, dsum added) and
     dweight [D] bf16, from the checkpoint."""
     T, D, kept = _checkpoint(codes, scales, rstd, weight)
-    src, dy_ld = _rows(dy, T, D, "dy")
-    dst, dx_ld = _rows(dx, T, D, "dx")
-    extra, dsum_ld = _rows(dsum, T, D, "dsum") if dsum is not None else (None, 0)
+    src, dy_ld = _rows(dy, (T, D), "dy")
+    dst, dx_ld = _rows(dx, (T, D), "dx")
+    extra, dsum_ld = _rows(dsum, (T, D), "dsum") if dsum is not None else (None, 0)
     room, size = _scratch(scratch)
     _check(lib().zero_norm_grad(src, dy_ld, extra, dsum_ld, *kept, T, D, dst, dx_ld,
                                 _dense(dweight, _bf16, (D,), "dweight"), room, size,
@@ -194,7 +196,7 @@ def zero_xent(h, table, targets, loss, lse, scratch, flags: int = 0, dev_status=
     logits are never stored; a negative target has no loss."""
     V, D = _table(table, "table")
     ids, width, T = _ids(targets, "targets")
-    src, ld = _rows(h, T, D, "h")
+    src, ld = _rows(h, (T, D), "h")
     room, size = _scratch(scratch)
     _check(lib().zero_xent(src, ld, _dense(table, _bf16, (V, D), "table"), V, D, ids, width, T,
                            _dense(loss, _f32, (T,), "loss"), _dense(lse, _f32, (T,), "lse"), room,
@@ -213,8 +215,8 @@ def zero_xent_grad(h, table, targets, lse, dloss, dh, dtable, scratch, piece: in
     time (a multiple of 256; 0: the library's choice)."""
     V, D = _table(table, "table")
     ids, width, T = _ids(targets, "targets")
-    src, h_ld = _rows(h, T, D, "h")
-    dst, dh_ld = _rows(dh, T, D, "dh")
+    src, h_ld = _rows(h, (T, D), "h")
+    dst, dh_ld = _rows(dh, (T, D), "dh")
     room, size = _scratch(scratch)
     _check(lib().zero_xent_grad(src, h_ld, _dense(table, _bf16, (V, D), "table"), V, D, ids, width,
                                 T, _dense(lse, _f32, (T,), "lse"),
