@@ -159,22 +159,27 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
             for (int b = tid; b < kSortWarps * bins; b += kSortThreads) warp_bins[b] = 0;
             const int64_t w0 = r0 + warp * 32 * kSortItems + lane;
 #pragma unroll
-            for (int q = 0; q < kSortItems; ++q)
+            for (int q = 0; q < kSortItems; ++q) {
+                k[q] = 0;
                 if (w0 + q * 32 < hi) load(w0 + q * 32, k[q], p[q]);
+            }
             __syncthreads();
 #pragma unroll
             for (int q = 0; q < kSortItems; ++q) {
                 const bool in = w0 + q * 32 < hi;
-                const uint32_t d = in ? (k[q] >> shift) & (bins - 1) : 0xFFFFFFFFu;
-                const uint32_t same = __match_any_sync(0xFFFFFFFFu, d);
-                const int first = __ffs(same) - 1;
-                uint32_t had = 0;
-                if (in && lane == first) {
-                    had = mine[d];
-                    mine[d] = had + __popc(same);
+                const uint32_t d = (k[q] >> shift) & (bins - 1);
+                // the lanes with the same digit, a vote for each of its bits
+                // (the match instruction took several times as long)
+                uint32_t same = __ballot_sync(0xFFFFFFFFu, in);
+                for (int b = 0; b < a.bits; ++b) {
+                    const uint32_t set = __ballot_sync(0xFFFFFFFFu, d >> b & 1);
+                    same &= d >> b & 1 ? set : ~set;
                 }
-                rank[q] = __shfl_sync(0xFFFFFFFFu, had, first) +
-                          __popc(same & ((1u << lane) - 1));
+                const uint32_t below = __popc(same & ((1u << lane) - 1));
+                const uint32_t had = in ? mine[d] : 0;
+                __syncwarp();
+                if (in && below == 0) mine[d] = had + __popc(same);
+                rank[q] = had + below;
                 __syncwarp();
             }
             __syncthreads();
@@ -362,38 +367,42 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_consta
     // asked for before the first is added
     const int from = r.head_long ? 0 : r.skip;
     const int to = r.n + r.more;
+    // bit s: place s is the last of its run (or of what is summed here)
+    uint64_t ends;
+    {
+        constexpr uint32_t PLACES = C == 32 ? ALL : (1u << (C & 31)) - 1;
+        const uint32_t up = __shfl_down_sync(ALL, r.cur, 1), first_next = __shfl_sync(ALL, r.next, 0);
+        const uint32_t a0 =
+            __ballot_sync(ALL, r.cur != (lane == C - 1 ? first_next : up)) & PLACES;
+        ends = a0 | 1ull << (to - 1);
+        // the tail run goes on: its last place is to - 1, past the chunk
+        if (r.more > 0) ends &= ~(((1ull << r.more) - 1) << (C - 1));
+    }
+    const uint16_t* dy = a.dy + col;
+    uint16_t* grad = a.grad + col;
     float acc[8] = {};
     for (int b = from; b < to; b += kBatch) {
         uint4 x[kBatch], old[ACC ? kBatch : 1];
-        uint32_t v[kBatch];
-        uint32_t ends = 0;                                   // bit q: place b + q ends a run
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int s = b + q, n = s + 1;
-            const uint32_t p0 = __shfl_sync(ALL, pos_cur, s & (C - 1));
-            const uint32_t p1 = __shfl_sync(ALL, pos_next, s & (C - 1));
-            const uint32_t k0 = __shfl_sync(ALL, r.cur, s & (C - 1));
-            const uint32_t k1 = __shfl_sync(ALL, r.next, s & (C - 1));
-            const uint32_t n0 = __shfl_sync(ALL, r.cur, n & (C - 1));
-            const uint32_t n1 = __shfl_sync(ALL, r.next, n & (C - 1));
-            const int64_t t = s < C ? p0 : p1;
-            v[q] = s < C ? k0 : k1;
-            const bool in = s < to;
-            x[q] = on && in ? ld16_stream(a.dy + t * a.dy_ld + col) : make_uint4(0, 0, 0, 0);
-            const bool end = in && (n == to || (n < C ? n0 : n1) != v[q]);
-            if (end) ends |= 1u << q;
+            const int s = b + q;
+            const uint32_t t = __shfl_sync(ALL, s < C ? pos_cur : pos_next, s & (C - 1));
+            x[q] = make_uint4(0, 0, 0, 0);
+            if (on && s < to) x[q] = ld16_stream(dy + t * a.dy_ld);
             if constexpr (ACC) {
-                const bool part = (r.head_long && s < r.skip) ||
-                                  (r.tail_long && s >= r.tail && s < C);
-                old[q] = on && end && !part ? ld16(a.grad + (int64_t)v[q] * a.D + col)
-                                            : make_uint4(0, 0, 0, 0);
+                const uint32_t v = __shfl_sync(ALL, s < C ? r.cur : r.next, s & (C - 1));
+                const bool part = (r.head_long && s < r.skip) || (r.tail_long && s >= r.tail);
+                old[q] = make_uint4(0, 0, 0, 0);
+                if (on && s < to && (ends >> s & 1) && !part)
+                    old[q] = ld16(grad + (int64_t)v * a.D);
             }
         }
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
             const int s = b + q;
             add8(acc, x[q]);
-            if (!(ends >> q & 1)) continue;
+            if (s >= to || !(ends >> s & 1)) continue;             // the same for the whole warp
+            const uint32_t v = __shfl_sync(ALL, s < C ? r.cur : r.next, s & (C - 1));
             const bool head = r.head_long && s < r.skip, tail = r.tail_long && s >= r.tail;
             if (on && (head || tail)) {
                 float* part = a.parts + (2 * c + (tail ? 1 : 0)) * a.D + col;
@@ -404,7 +413,7 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_consta
                 if constexpr (ACC) bf_unpack8(old[q], f);
 #pragma unroll
                 for (int z = 0; z < 8; ++z) f[z] += acc[z] * a.scale;
-                st16(a.grad + (int64_t)v[q] * a.D + col, bf_pack8(f));
+                st16(grad + (int64_t)v * a.D, bf_pack8(f));
             }
 #pragma unroll
             for (int z = 0; z < 8; ++z) acc[z] = 0.0f;
@@ -442,11 +451,15 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const __grid_consta
         const uint32_t v = run_key[k];
         if (v == (uint32_t)a.V) continue;                      // the same in every warp
         const int64_t c = group + (int64_t)k * groups;
-        int64_t lo = (c + 1) * C, hi = a.T;                    // the first place past the run
+        // the first place past the run, by 32 probes at a time
+        int64_t lo = (c + 1) * C, hi = a.T;
         while (lo < hi) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (a.key[mid] > v) hi = mid;
-            else lo = mid + 1;
+            const int64_t gap = (hi - lo + 31) / 32, at = lo + lane * gap;
+            const uint32_t past =
+                __ballot_sync(0xFFFFFFFFu, at >= hi || a.key[at < hi ? at : hi - 1] > v);
+            const int k = past ? __ffs(past) - 1 : 32;         // probes before k are in the run
+            if (past) hi = min(hi, lo + k * gap);
+            if (k > 0) lo += (k - 1) * gap + 1;
         }
         const int64_t parts = (lo - 1) / C - c + 1;            // one of each chunk it meets
         const int64_t each = (parts + W - 1) / W;

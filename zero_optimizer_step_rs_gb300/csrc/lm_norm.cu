@@ -230,18 +230,15 @@ struct NormGradArgs {
     int32_t D, blocks;
 };
 
-// Copies from global memory into the thread's own place in shared memory, which
-// only that thread reads: no barrier, only the thread's own wait.  `bytes` 0
-// fills with zeros and reads nothing.
+// A copy of N bytes from global memory into the thread's own place in shared
+// memory, which only that thread reads: no barrier, only its own wait.
 template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int bytes)
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
 {
     if constexpr (N == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src),
-                     "r"(bytes), "n"(N)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N)
                      : "memory");
 }
 
@@ -270,86 +267,108 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 128 ? 1024 / TPR 
     pdl_enter();
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float slots[2][32];
-    uint4* ring_d = reinterpret_cast<uint4*>(ring) + threadIdx.x;            // [S][NV][THREADS]
-    uint4* ring_s = ring_d + S * NV * THREADS;
-    uint2* ring_q = reinterpret_cast<uint2*>(ring + S * NV * THREADS * 32) + threadIdx.x;
-    float* ring_c = reinterpret_cast<float*>(ring + S * NV * THREADS * 40) + threadIdx.x;
+    // a stage: [NV][THREADS] of dy, dsum (16 bytes), codes (8) and scales (4)
+    constexpr int N = NV * THREADS, STAGE = N * 44;
+    const uint8_t* mine = ring + threadIdx.x * 16;
     const int group = threadIdx.x / TPR, lane = threadIdx.x % TPR;
     const int nv = a.D >> 3;
-    const int nb = (a.D + kBlock - 1) / kBlock;
     const int64_t step = (int64_t)gridDim.x * GROUPS;
-    const int64_t t00 = (int64_t)blockIdx.x * GROUPS;
+    const int64_t first = (int64_t)blockIdx.x * GROUPS + group;
 
-    auto ask = [&](int64_t t, int stage) {
+    // where the row to ask for next lies; a thread past the row's end asks for
+    // nothing and keeps the zeros that its places start with
+    const int nb = (a.D + kBlock - 1) / kBlock;
+    const uint16_t* p_d = a.dy + first * a.dy_ld + lane * 8;
+    const uint16_t* p_s = a.dsum ? a.dsum + first * a.dsum_ld + lane * 8 : nullptr;
+    const int8_t* p_q = a.codes + first * a.D + lane * 8;
+    const float* p_c = a.scales + first * nb + lane / kLanesPerBlock;
+    const int64_t d_step = step * a.dy_ld, s_step = step * a.dsum_ld;
+    const int64_t q_step = step * a.D, c_step = step * nb;
+    const uint32_t at16 = (uint32_t)__cvta_generic_to_shared(mine);
+    const uint32_t at8 = at16 + N * 32 - threadIdx.x * 8;
+    const uint32_t at4 = at16 + N * 40 - threadIdx.x * 12;
+    auto ask = [&](bool in, uint32_t stage) {
+        if (in) {
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR;
-            const bool in = t < a.T && c < nv;
-            const int64_t r = in ? t : 0;
-            const int e = in ? c * 8 : 0, at = (stage * NV + k) * THREADS;
-            copy_async<16>((uint32_t)__cvta_generic_to_shared(ring_d + at), a.dy + r * a.dy_ld + e,
-                           in ? 16 : 0);
-            copy_async<8>((uint32_t)__cvta_generic_to_shared(ring_q + at), a.codes + r * a.D + e,
-                          in ? 8 : 0);
-            copy_async<4>((uint32_t)__cvta_generic_to_shared(ring_c + at),
-                          a.scales + r * nb + e / kBlock, in ? 4 : 0);
-            if (a.dsum)
-                copy_async<16>((uint32_t)__cvta_generic_to_shared(ring_s + at),
-                               a.dsum + r * a.dsum_ld + e, in ? 16 : 0);
+            for (int k = 0; k < NV; ++k) {
+                if (lane + k * TPR >= nv) break;
+                copy_async<16>(at16 + stage + k * THREADS * 16, p_d + k * TPR * 8);
+                copy_async<8>(at8 + stage + k * THREADS * 8, p_q + k * TPR * 8);
+                copy_async<4>(at4 + stage + k * THREADS * 4, p_c + k * (TPR / kLanesPerBlock));
+                if (p_s) copy_async<16>(at16 + stage + N * 16 + k * THREADS * 16, p_s + k * TPR * 8);
+            }
         }
+        p_d += d_step;
+        if (p_s) p_s += s_step;
+        p_q += q_step;
+        p_c += c_step;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    for (int i = threadIdx.x; i < S * STAGE / 4; i += THREADS)
+        reinterpret_cast<uint32_t*>(ring)[i] = 0;
+    __syncthreads();
 
-    float dw[NV][8] = {};
-    int slot = 0, stage = 0;
+    uint4 w4[NV];
 #pragma unroll
-    for (int s = 0; s < S - 1; ++s) ask(t00 + group + s * step, s);
-    float rstd_next = t00 + group < a.T ? a.rstd[t00 + group] : 0.0f;
-    // every group of a block makes the same number of rounds (barriers)
-    for (int64_t t0 = t00; t0 < a.T; t0 += step) {
-        const int64_t t = t0 + group;
-        const bool in = t < a.T;
+    for (int k = 0; k < NV; ++k)
+        w4[k] = lane + k * TPR < nv ? ld16(a.w + (lane + k * TPR) * 8) : make_uint4(0, 0, 0, 0);
+    float dw[NV][8] = {};
+    uint32_t stage = 0;                                   // offset of the row at hand
+    int slot = 0;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) ask(first + s * step < a.T, s * STAGE);
+    float rstd_next = first < a.T ? a.rstd[first] : 0.0f;
+    uint16_t* p_x = a.dx + first * a.dx_ld + lane * 8;
+    const float inv = 1.0f / (float)a.D;
+    // (barriers: where a row has more than a warp, the block has one row at a time)
+    for (int64_t t = first; t < a.T; t += step, p_x += step * a.dx_ld) {
         const float rstd = rstd_next;
         rstd_next = t + step < a.T ? a.rstd[t + step] : 0.0f;
-        ask(t + (S - 1) * step, stage == 0 ? S - 1 : stage - 1);      // the stage freed last
+        ask(t + (S - 1) * step < a.T, stage == 0 ? (S - 1) * STAGE : stage - STAGE);
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
         // xhat and dy * w are made twice, from what shared memory holds:
         // keeping them would cost 16 registers a vector
         float inner = 0.0f;
+        const uint8_t* here = mine + stage;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR, at = (stage * NV + k) * THREADS;
-            float w[8] = {}, xh[8], d[8];
-            if (c < nv) bf_unpack8(ld16(a.w + c * 8), w);
-            unpack_codes(ring_q[at], xh);
-            bf_unpack8(ring_d[at], d);
-            const float sc = ring_c[at] * rstd;
+            float w[8], xh[8], d[8];
+            bf_unpack8(w4[k], w);
+            unpack_codes(*reinterpret_cast<const uint2*>(here + N * 32 - threadIdx.x * 8 +
+                                                         k * THREADS * 8), xh);
+            bf_unpack8(*reinterpret_cast<const uint4*>(here + k * THREADS * 16), d);
+            const float sc = *reinterpret_cast<const float*>(here + N * 40 - threadIdx.x * 12 +
+                                                             k * THREADS * 4) * rstd;
+            float part = 0.0f;
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const float p = d[q] * (xh[q] * sc);
-                dw[k][q] += p;
-                inner = fmaf(p, w[q], inner);
+                const float p = d[q] * xh[q];
+                dw[k][q] = fmaf(p, sc, dw[k][q]);
+                part = fmaf(p, w[q], part);
             }
+            inner = fmaf(part, sc, inner);
         }
-        inner = row_sum<TPR>(inner, slots, slot) / (float)a.D;
+        inner = row_sum<TPR>(inner, slots, slot) * inv;
         slot ^= 1;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR, at = (stage * NV + k) * THREADS;
-            if (in && c < nv) {
-                float s[8] = {}, w[8], xh[8], d[8];
-                bf_unpack8(ld16(a.w + c * 8), w);
-                unpack_codes(ring_q[at], xh);
-                bf_unpack8(ring_d[at], d);
-                if (a.dsum) bf_unpack8(ring_s[at], s);
-                const float back = ring_c[at] * rstd * inner;
+            if (lane + k * TPR >= nv) break;
+            float s[8] = {}, w[8], xh[8], d[8];
+            bf_unpack8(w4[k], w);
+            unpack_codes(*reinterpret_cast<const uint2*>(here + N * 32 - threadIdx.x * 8 +
+                                                         k * THREADS * 8), xh);
+            bf_unpack8(*reinterpret_cast<const uint4*>(here + k * THREADS * 16), d);
+            if (p_s) bf_unpack8(*reinterpret_cast<const uint4*>(here + N * 16 +
+                                                                k * THREADS * 16), s);
+            const float back =
+                -*reinterpret_cast<const float*>(here + N * 40 - threadIdx.x * 12 +
+                                                 k * THREADS * 4) * rstd * inner;
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    s[q] = fmaf(rstd, fmaf(d[q], w[q], -xh[q] * back), s[q]);
-                st16_stream(a.dx + t * a.dx_ld + c * 8, bf_pack8(s));
-            }
+            for (int q = 0; q < 8; ++q)
+                s[q] = fmaf(rstd, fmaf(xh[q], back, d[q] * w[q]), s[q]);
+            st16_stream(p_x + k * TPR * 8, bf_pack8(s));
         }
-        stage = stage == S - 1 ? 0 : stage + 1;
+        stage = stage == (S - 1) * STAGE ? 0 : stage + STAGE;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     float* part = a.parts + (int64_t)blockIdx.x * a.D;

@@ -363,7 +363,7 @@ __device__ __forceinline__ bool epilogue_lse(const MmaArgs& a, const Unit& t, ui
                 if (c + i >= live) x[i] = -INFINITY;
         }
         const int at = (int)(y - c);
-        if (y >= c && y < c + 32) {
+        if (y >= c && y < min(c + 32, live)) {        // not the next tile's first columns
             float v = 0.0f;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
