@@ -90,7 +90,9 @@ constexpr int smem_bytes()
 }
 
 struct MmaArgs {
-    CUtensorMap a, b, out;
+    CUtensorMap a, b;
+    void* out;                         // bf16, or fp32 for kDh
+    int64_t out_ld;
     int32_t m_tiles, n_tiles, bn;      // tiles of 256 x bn
     int32_t k_blocks, splits;          // blocks of 64 along the summed dimension; its splits
     int32_t m_fast;                    // which tile coordinate runs fastest
@@ -115,6 +117,15 @@ struct MmaArgs {
 __device__ __forceinline__ uint32_t smem_u32(const void* p)
 {
     return (uint32_t)__cvta_generic_to_shared(p);
+}
+// True in one lane of a converged warp.  The compiler knows that what it guards
+// runs in a single lane: tensor instructions under `lane == 0` instead cost the
+// loop that feeds the tensor cores 17 % of its time.
+__device__ __forceinline__ bool elect()
+{
+    uint32_t p;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(p));
+    return p != 0;
 }
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -152,7 +163,7 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
 {
     uint32_t ok;
     asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; "
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; "
         "selp.u32 %0, 1, 0, p; }"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -165,7 +176,7 @@ __device__ __forceinline__ uint64_t now_ns()
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// Wait for a phase; gives up after `limit` ns (at once if that is 0), or once
+// One thread waits for a phase; gives up after `limit` ns (at once if that is 0), or once
 // another role of the CTA has given up.  False: the caller leaves its loop.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_t limit,
                                           volatile int* dead)
@@ -206,21 +217,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 "
         "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
         "l"(map), "r"(leader_bar), "r"(x), "r"(y)
-        : "memory");
-}
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, uint32_t src)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     map),
-                 "r"(x), "r"(y), "r"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void tma_add(const CUtensorMap* map, int x, int y, uint32_t src)
-{
-    asm volatile(
-        "cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-            map),
-        "r"(x), "r"(y), "r"(src)
         : "memory");
 }
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
@@ -315,8 +311,12 @@ __device__ __forceinline__ Unit unit_at(const MmaArgs& a, int u)
     const int hi = q / fast, lo = q - hi * fast;
     t.m = a.m_fast ? lo : hi;
     t.n = a.m_fast ? hi : lo;
-    t.k0 = (int)((int64_t)a.k_blocks * t.split / a.splits);
-    t.k1 = (int)((int64_t)a.k_blocks * (t.split + 1) / a.splits);
+    t.k0 = 0;
+    t.k1 = a.k_blocks;
+    if (a.splits > 1) {
+        t.k0 = (int)((int64_t)a.k_blocks * t.split / a.splits);
+        t.k1 = (int)((int64_t)a.k_blocks * (t.split + 1) / a.splits);
+    }
     return t;
 }
 
@@ -408,15 +408,25 @@ __device__ __forceinline__ void stage16(uint32_t buf, int row, int chunk, uint32
                  : "memory");
 }
 
-// The buffer is free once the last store has read it.
-__device__ __forceinline__ void stage_free(int lane)
+// Writes a staged buffer out, 8 lanes to a 128-byte row.  (Bulk tensor stores
+// from the same buffers wait in the copy engine behind the loads that run
+// ahead; with one or two buffers a warp that made the epilogue, not the
+// products, the bound where the summed dimension is short.)
+template <typename Store>
+__device__ __forceinline__ void write_rows(uint32_t buf, int lane, Store&& store)
 {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
-}
-__device__ __forceinline__ void stage_full()
-{
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int row = j * 4 + (lane >> 3), chunk = lane & 7;
+        const uint32_t p = buf + row * 128 + ((chunk ^ (row & 7)) << 4);
+        uint4 x;
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(p)
+                     : "memory");
+        store(row, chunk, x);
+    }
     __syncwarp();
 }
 
@@ -466,18 +476,20 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
 #pragma unroll
                 for (int i = 0; i < 32; ++i) x[i] *= g;
             }
-            if (h == 0) stage_free(lane);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 stage16(to, lane, 4 * h + j, bf_pack(x[8 * j], x[8 * j + 1]),
                         bf_pack(x[8 * j + 2], x[8 * j + 3]), bf_pack(x[8 * j + 4], x[8 * j + 5]),
                         bf_pack(x[8 * j + 6], x[8 * j + 7]));
         }
-        stage_full();
-        if (lane == 0) {
-            tma_store(&a.out, (int)(c0 + c), (int)row0, to);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        uint16_t* out = static_cast<uint16_t*>(a.out) + row0 * a.out_ld + c0 + c;
+        write_rows(to, lane, [&](int r, int chunk, const uint4& x) {
+            // 8 columns at once: P's rows are padded to whole pieces, D is a multiple of 8
+            if (row0 + r < a.rows && c0 + c + chunk * 8 < a.cols) {
+                if constexpr (K == kDlogits) st16(out + r * a.out_ld + chunk * 8, x);
+                else st16_stream(out + r * a.out_ld + chunk * 8, x);
+            }
+        });
     }
 }
 
@@ -493,18 +505,23 @@ __device__ __forceinline__ void epilogue_f32(const MmaArgs& a, const Unit& t, ui
         if (c0 + c >= a.cols) break;
         float x[32];
         tmem_load32(tmem + c, x);
-        stage_free(lane);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             stage16(to, lane, j, __float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
                     __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
-        stage_full();
-        if (lane == 0) {
-            const int y = (int)(t.split * a.out_split_rows + row0);
-            if (a.add) tma_add(&a.out, (int)(c0 + c), y, to);
-            else tma_store(&a.out, (int)(c0 + c), y, to);
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        float* out = static_cast<float*>(a.out) + (t.split * a.out_split_rows + row0) * a.out_ld +
+                     c0 + c;
+        write_rows(to, lane, [&](int r, int chunk, uint4 x) {
+            if (row0 + r >= a.rows || c0 + c + chunk * 4 >= a.cols) return;
+            float4* at = reinterpret_cast<float4*>(out + r * a.out_ld + chunk * 4);
+            float4 f = make_float4(__uint_as_float(x.x), __uint_as_float(x.y),
+                                   __uint_as_float(x.z), __uint_as_float(x.w));
+            if (a.add) {
+                const float4 g = *at;
+                f.x += g.x; f.y += g.y; f.z += g.z; f.w += g.w;
+            }
+            *at = f;
+        });
     }
 }
 
@@ -562,66 +579,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
     bool drain_failed = false;
 
-    if (warp == 0 && lane == 0) {                        // ---- loads
-        uint32_t it = 0;
+    if (warp == 0) {                                     // ---- loads
+        uint32_t s = 0, ph = 0, issued = 0;              // stage, its phase, loads so far
         bool ok = true;
         // both CTAs' boxes of a stage (a box always counts in full)
         const uint32_t stage_tx = 2 * (kStageBytes / 2 + (F::b_k ? a.bn / 2 * 128 : kStageBytes / 2));
+        const uint32_t leader_full = in_leader(full);
         for (int u = first; u < units && ok; u += stride) {
             const Unit t = unit_at(a, u);
             const int ra = t.m * BM + (int)rank * 128, rb = t.n * a.bn + (int)rank * (a.bn / 2);
-            for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
-                const uint32_t s = it % S, ph = (it / S) & 1;
-                if (!(ok = mbar_wait(empty + 8 * s, ph ^ 1, a.wait_limit, dead))) break;
-                if (leader) mbar_expect(full + 8 * s, stage_tx);
-                const uint32_t dst = smem + s * kStageBytes;
-                const uint32_t bar = in_leader(full + 8 * s);
-                load_operand<F::a_k>(dst, &a.a, ra, kb * BK, bar);
-                load_operand<F::b_k>(dst + kStageBytes / 2, &a.b, rb, kb * BK, bar);
+            for (int kb = t.k0; kb < t.k1; ++kb) {
+                if (!(ok = warp_wait(empty + 8 * s, ph ^ 1, a.wait_limit, dead))) break;
+                if (elect()) {
+                    if (leader) mbar_expect(full + 8 * s, stage_tx);
+                    const uint32_t dst = smem + s * kStageBytes, bar = leader_full + 8 * s;
+                    load_operand<F::a_k>(dst, &a.a, ra, kb * BK, bar);
+                    load_operand<F::b_k>(dst + kStageBytes / 2, &a.b, rb, kb * BK, bar);
+                }
+                __syncwarp();
+                ++issued;
+                if (++s == S) { s = 0; ph ^= 1; }
             }
         }
         // Before this CTA may leave: the products' last arrivals at its
         // barriers; or, after a wait ran out, the copies that were issued (both
         // CTAs' copies count on the leader's barriers).
-        const uint32_t from = it > (uint32_t)S ? it - S : 0;
+        const uint32_t from = issued > (uint32_t)S ? issued - S : 0;
         if (ok) {
-            for (uint32_t j = from; j < it && ok; ++j)
-                ok = mbar_wait(empty + 8 * (j % S), (j / S) & 1, a.wait_limit, dead);
+            for (uint32_t j = from; j < issued && ok; ++j)
+                ok = warp_wait(empty + 8 * (j % S), (j / S) & 1, a.wait_limit, dead);
         }
-        if (!ok && leader) {
+        if (!ok && leader && lane == 0) {
             int none = 0;
-            for (uint32_t j = from; j < it; ++j)
+            for (uint32_t j = from; j < issued; ++j)
                 drain_failed |= !mbar_wait(full + 8 * (j % S), (j / S) & 1, kDrainLimit, &none);
         }
-    } else if (warp == 1 && lane == 0 && leader) {       // ---- products
+    } else if (warp == 1 && leader) {                    // ---- products
         const uint32_t idesc = instruction<K>(a.bn);
-        uint32_t it = 0;
+        uint32_t s = 0, ph = 0;
         int i = 0;
         bool ok = true;
         for (int u = first; u < units && ok; u += stride, ++i) {
             const Unit t = unit_at(a, u);
-            const int b = i & 1;
-            if (!(ok = mbar_wait(sums_empty + 8 * b, ((i >> 1) & 1) ^ 1, a.wait_limit, dead)))
+            const int b = i & 1, nk = t.k1 - t.k0;
+            if (!(ok = warp_wait(sums_empty + 8 * b, ((i >> 1) & 1) ^ 1, a.wait_limit, dead)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            for (int kb = t.k0; kb < t.k1; ++kb, ++it) {
-                const uint32_t s = it % S, ph = (it / S) & 1;
-                if (!(ok = mbar_wait(full + 8 * s, ph, a.wait_limit, dead))) break;
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t at = smem + s * kStageBytes;
-                const uint64_t da = operand<F::a_k>(at), db = operand<F::b_k>(at + kStageBytes / 2);
+            // the next stage is looked at before this one's products are issued
+            bool ready = __all_sync(0xFFFFFFFFu, mbar_try(full + 8 * s, ph));
+            for (int k = 0; k < nk; ++k) {
+                if (!ready && !(ok = warp_wait(full + 8 * s, ph, a.wait_limit, dead))) break;
+                const uint32_t at = smem + s * kStageBytes, done = empty + 8 * s;
+                if (++s == S) { s = 0; ph ^= 1; }
+                if (k + 1 < nk) ready = __all_sync(0xFFFFFFFFu, mbar_try(full + 8 * s, ph));
+                if (elect()) {
+                    const uint64_t da = operand<F::a_k>(at), db = operand<F::b_k>(at + kStageBytes / 2);
 #pragma unroll
-                for (int q = 0; q < BK / 16; ++q)
-                    mma(tmem + b * BN, da + q * operand_step<F::a_k>(),
-                        db + q * operand_step<F::b_k>(), idesc, kb > t.k0 || q > 0);
-                mma_commit(empty + 8 * s);
+                    for (int q = 0; q < BK / 16; ++q)
+                        mma(tmem + b * BN, da + q * operand_step<F::a_k>(),
+                            db + q * operand_step<F::b_k>(), idesc, k > 0 || q > 0);
+                    mma_commit(done);
+                }
+                __syncwarp();
             }
-            if (ok) mma_commit(sums_full + 8 * b);
+            if (ok && elect()) mma_commit(sums_full + 8 * b);
+            __syncwarp();
         }
         if (!ok) {                                       // products in flight
-            mma_commit(drained);
+            if (elect()) mma_commit(drained);
+            __syncwarp();
             int none = 0;
-            drain_failed |= !mbar_wait(drained, 0, kDrainLimit, &none);
+            if (lane == 0) drain_failed |= !mbar_wait(drained, 0, kDrainLimit, &none);
         }
     } else if (warp >= 4) {                              // ---- epilogue
         const int q = warp & 3;                          // the warp's quarter of the lanes
@@ -646,7 +674,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(in_leader(sums_empty + 8 * b));
         }
-        if (F::out && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     if (drain_failed && a.status) atomicOr(a.status, ZERO_DEV_DRAIN_FAILED);
@@ -806,19 +833,16 @@ EncodeFn encoder()
     return fn;
 }
 
-// A row-major matrix (row stride `ld` elements), in boxes of 128 bytes x box_rows.
-bool encode(CUtensorMap* map, const void* p, bool f32, int64_t cols, int64_t rows, int64_t ld,
-            int box_rows)
+// A row-major bf16 matrix (row stride `ld` elements), in boxes of 64 columns.
+bool encode(CUtensorMap* map, const void* p, int64_t cols, int64_t rows, int64_t ld, int box_rows)
 {
-    const int elem = f32 ? 4 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)(ld * elem)};
-    const cuuint32_t box[2] = {(cuuint32_t)(128 / elem), (cuuint32_t)box_rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     const cuuint32_t steps[2] = {1, 1};
     const EncodeFn fn = encoder();
-    return fn && fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    2, const_cast<void*>(p), dims, strides, box, steps,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides,
+                    box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -898,7 +922,7 @@ GradPlan grad_plan(int64_t T, int64_t V, int32_t D, int64_t piece)
     g.p = 0;
     g.clean = up(2 * T * g.piece, 256);
     g.sums = g.clean + up(2 * T * D, 256);
-    g.split_rows = up(T, 32);            // an output box never reaches into the next split
+    g.split_rows = T;
     g.unit = g.sums + up(4 * g.split_rows * D * g.splits, 256);
     g.bytes = g.unit + 256;
     return g;
@@ -957,7 +981,7 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
     a.m_tiles = tiles(T);
     a.bn = tile_width(V, a.m_tiles, 1, 16);
     a.n_tiles = tiles(V, a.bn);
-    if (!encode(&a.a, h, false, D, T, h_ld, 128) || !encode(&a.b, table, false, D, V, D, a.bn / 2))
+    if (!encode(&a.a, h, D, T, h_ld, 128) || !encode(&a.b, table, D, V, D, a.bn / 2))
         return ZERO_ERR_CUDA;
     a.k_blocks = (D + BK - 1) / BK;
     a.splits = 1;
@@ -1050,10 +1074,10 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         p.m_tiles = tiles(T);
         p.bn = tile_width(n, p.m_tiles, 1, 64);
         p.n_tiles = tiles(n, p.bn);
-        if (!encode(&p.a, h, false, D, T, h_ld, 128) ||
-            !encode(&p.b, rows, false, D, n, D, p.bn / 2) ||
-            !encode(&p.out, P, false, n, T, g.piece, 32))
+        if (!encode(&p.a, h, D, T, h_ld, 128) || !encode(&p.b, rows, D, n, D, p.bn / 2))
             return ZERO_ERR_CUDA;
+        p.out = P;
+        p.out_ld = g.piece;
         p.k_blocks = (D + BK - 1) / BK;
         p.splits = 1;
         p.m_fast = 1;
@@ -1063,9 +1087,10 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         if ((e = run_mma<kDlogits>(p, st)) != cudaSuccess) break;
 
         MmaArgs d = common;                                 // dh += P E
-        if (!encode(&d.a, P, false, n, T, g.piece, 128) || !encode(&d.b, rows, false, D, n, D, 64) ||
-            !encode(&d.out, sums, true, D, g.split_rows * g.splits, D, 32))
+        if (!encode(&d.a, P, n, T, g.piece, 128) || !encode(&d.b, rows, D, n, D, 64))
             return ZERO_ERR_CUDA;
+        d.out = sums;
+        d.out_ld = D;
         d.k_blocks = (int32_t)((n + BK - 1) / BK);
         d.splits = std::min(g.splits, d.k_blocks);
         d.m_tiles = tiles(T);
@@ -1078,9 +1103,10 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         if ((e = run_mma<kDh>(d, st)) != cudaSuccess) break;
 
         MmaArgs w = common;                                 // dE = P^T h
-        if (!encode(&w.a, P, false, n, T, g.piece, 64) || !encode(&w.b, clean, false, D, T, D, 64) ||
-            !encode(&w.out, dtable + v0 * D, false, D, n, D, 32))
+        if (!encode(&w.a, P, n, T, g.piece, 64) || !encode(&w.b, clean, D, T, D, 64))
             return ZERO_ERR_CUDA;
+        w.out = dtable + v0 * D;
+        w.out_ld = D;
         w.m_tiles = tiles(n);
         w.bn = tile_width(D, w.m_tiles, 1, 64);
         w.n_tiles = tiles(D, w.bn);
