@@ -56,49 +56,39 @@ constexpr uint64_t kDrainLimit = 1000000000;
 constexpr int kWarpStage = 4096;                   // an epilogue warp's output buffer
 constexpr int kStaging = kEpilogueWarps * kWarpStage;
 
-enum Kind { kLse, kDlogits, kDtable, kDh };
-
-template <Kind K>
-struct Form;
-template <>
-struct Form<kLse> {
-    static constexpr bool a_k = true, b_k = true, out = false;
-    static constexpr int stages = 6;
-};
-template <>
-struct Form<kDlogits> {
-    static constexpr bool a_k = true, b_k = true, out = true;
-    static constexpr int stages = 6;
-};
-template <>
-struct Form<kDtable> {
-    static constexpr bool a_k = false, b_k = false, out = true;
-    static constexpr int stages = 6;
-};
-template <>
-struct Form<kDh> {
-    static constexpr bool a_k = true, b_k = false, out = true;
-    static constexpr int stages = 6;
-};
+// The loss; a piece's P; both gradients of a piece (two products in one launch).
+enum Kind { kLse, kP, kGrads };
 
 constexpr int kShares = 2 * 128 * 8;               // kLse: the second half's (maximum, sum)
+
+constexpr int kStages = 6;
 
 template <Kind K>
 constexpr int smem_bytes()
 {
-    return 1024 + Form<K>::stages * kStageBytes + (Form<K>::out ? kStaging : kShares) + 256;
+    return 1024 + kStages * kStageBytes + (K == kLse ? kShares : kStaging) + 256;
 }
 
-struct MmaArgs {
+// One product: its operands, its result and how it is cut into units of work.
+struct Product {
     CUtensorMap a, b;
-    void* out;                         // bf16, or fp32 for kDh
+    void* out;                         // bf16; dh's sums: fp32
     int64_t out_ld;
     int32_t m_tiles, n_tiles, bn;      // tiles of 256 x bn
     int32_t k_blocks, splits;          // blocks of 64 along the summed dimension; its splits
     int32_t m_fast;                    // which tile coordinate runs fastest
-    int64_t rows, cols;                // of the result (cols: of the piece)
-    int64_t out_split_rows;            // rows between the splits' results (kDh)
-    int32_t add;                       // kDh: add to what is there
+    int64_t rows, cols;                // of the result (of the piece)
+    int32_t units() const { return m_tiles * n_tiles * splits; }
+};
+
+struct MmaArgs {
+    Product x, y;                      // kGrads: dh (x) and the table's gradient (y); else x
+    int32_t x_units, y_units;
+    // y's units beyond x's: the pairs from `light` on have one unit of x less and
+    // first take `extra` of y's units among themselves
+    int32_t light, extra;
+    int64_t out_split_rows;            // kGrads: rows between the splits of dh
+    int32_t add;                       // kGrads: dh's sums are added to what is there
     int32_t token_bytes;
     const void* targets;
     int64_t V, v0;                     // the vocabulary, and where the piece starts
@@ -260,62 +250,86 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// Shared-memory operand descriptors, 128-byte swizzle.  Contiguous along the
-// summed dimension: rows of 128 bytes, 1024 bytes between groups of 8 rows.
+// How an operand lies in shared memory (128-byte swizzle).  Contiguous along
+// the summed dimension: rows of 128 bytes, 1024 bytes between groups of 8 rows.
 // Contiguous along the other one: two chunks of 64 x 64, 8192 bytes apart,
 // 1024 bytes between groups of 8 along the summed dimension.
 template <bool K_MAJOR>
-__device__ __forceinline__ uint64_t operand(uint32_t addr)
-{
-    const uint64_t lead = K_MAJOR ? 1 : 8192 >> 4;
-    return (uint64_t)((addr >> 4) & 0x3FFF) | lead << 16 | (uint64_t)(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
-}
-template <bool K_MAJOR>
-__host__ __device__ constexpr uint64_t operand_step()               // 16 further along the summed dimension
-{
-    return (K_MAJOR ? 32 : 2048) >> 4;
-}
+struct Layout {
+    static __device__ __forceinline__ uint64_t descriptor(uint32_t addr)
+    {
+        const uint64_t lead = K_MAJOR ? 1 : 8192 >> 4;
+        return (uint64_t)((addr >> 4) & 0x3FFF) | lead << 16 | (uint64_t)(1024 >> 4) << 32 |
+               1ull << 46 | 2ull << 61;
+    }
+    static constexpr uint64_t step = (K_MAJOR ? 32 : 2048) >> 4;     // 16 along the sum
+    // 128 rows of a stage
+    static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* map, int row, int k,
+                                                uint32_t bar)
+    {
+        if constexpr (K_MAJOR) {
+            tma_load(dst, map, k, row, bar);
+        } else {
+            tma_load(dst, map, row, k, bar);
+            tma_load(dst + 8192, map, row + 64, k, bar);
+        }
+    }
+};
 // fp32 sums, bf16 operands, 256 x bn
-template <Kind K>
+template <bool A_K, bool B_K>
 __device__ __forceinline__ uint32_t instruction(int bn)
 {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (Form<K>::a_k ? 0u : 1u << 15) |
-           (Form<K>::b_k ? 0u : 1u << 16) | (uint32_t)(bn >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
+    return 1u << 4 | 1u << 7 | 1u << 10 | (A_K ? 0u : 1u << 15) | (B_K ? 0u : 1u << 16) |
+           (uint32_t)(bn >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
+}
+// One stage's four products.
+template <bool A_K, bool B_K>
+__device__ __forceinline__ void products(uint32_t d, uint32_t at, int bn, bool add)
+{
+    const uint64_t da = Layout<A_K>::descriptor(at);
+    const uint64_t db = Layout<B_K>::descriptor(at + kStageBytes / 2);
+    const uint32_t idesc = instruction<A_K, B_K>(bn);
+#pragma unroll
+    for (int q = 0; q < BK / 16; ++q)
+        mma(d, da + q * Layout<A_K>::step, db + q * Layout<B_K>::step, idesc, add || q > 0);
 }
 
-// One operand's 128 rows of a stage.
-template <bool K_MAJOR>
-__device__ __forceinline__ void load_operand(uint32_t dst, const CUtensorMap* map, int row, int k,
-                                             uint32_t bar)
+// The i-th unit of work of a CTA pair, or -1: x's units by turns, then (for
+// the pairs that got one less) the extra ones of y, then the rest of y by turns.
+__device__ __forceinline__ int unit_of(const MmaArgs& a, int pair, int pairs, int i)
 {
-    if constexpr (K_MAJOR) {
-        tma_load(dst, map, k, row, bar);
-    } else {
-        tma_load(dst, map, row, k, bar);
-        tma_load(dst + 8192, map, row + 64, k, bar);
+    const int nx = pair < a.x_units ? (a.x_units - pair + pairs - 1) / pairs : 0;
+    if (i < nx) return pair + i * pairs;
+    i -= nx;
+    if (pair >= a.light) {
+        const int lights = pairs - a.light, q = pair - a.light;
+        const int ne = q < a.extra ? (a.extra - q + lights - 1) / lights : 0;
+        if (i < ne) return a.x_units + q + i * lights;
+        i -= ne;
     }
+    const int j = a.extra + pair + i * pairs;
+    return j < a.y_units ? a.x_units + j : -1;
 }
 
 struct Unit {
     int m, n, k0, k1, split;
 };
 
-__device__ __forceinline__ Unit unit_at(const MmaArgs& a, int u)
+__device__ __forceinline__ Unit unit_at(const Product& p, int u)
 {
     Unit t;
-    const int tiles = a.m_tiles * a.n_tiles;
+    const int tiles = p.m_tiles * p.n_tiles;
     t.split = u / tiles;
     const int q = u - t.split * tiles;
-    const int fast = a.m_fast ? a.m_tiles : a.n_tiles;
+    const int fast = p.m_fast ? p.m_tiles : p.n_tiles;
     const int hi = q / fast, lo = q - hi * fast;
-    t.m = a.m_fast ? lo : hi;
-    t.n = a.m_fast ? hi : lo;
+    t.m = p.m_fast ? lo : hi;
+    t.n = p.m_fast ? hi : lo;
     t.k0 = 0;
-    t.k1 = a.k_blocks;
-    if (a.splits > 1) {
-        t.k0 = (int)((int64_t)a.k_blocks * t.split / a.splits);
-        t.k1 = (int)((int64_t)a.k_blocks * (t.split + 1) / a.splits);
+    t.k1 = p.k_blocks;
+    if (p.splits > 1) {
+        t.k0 = (int)((int64_t)p.k_blocks * t.split / p.splits);
+        t.k1 = (int)((int64_t)p.k_blocks * (t.split + 1) / p.splits);
     }
     return t;
 }
@@ -325,7 +339,7 @@ __device__ __forceinline__ Unit unit_at(const MmaArgs& a, int u)
 // A row's target, or -1 where it takes part in nothing.
 __device__ __forceinline__ int64_t target_of(const MmaArgs& a, int64_t row)
 {
-    if (row >= a.rows) return -1;
+    if (row >= a.x.rows) return -1;
     const int64_t y = token_at(a.targets, a.token_bytes, row);
     return y < a.V ? y : -1;
 }
@@ -348,8 +362,8 @@ __device__ __forceinline__ bool epilogue_lse(const MmaArgs& a, const Unit& t, ui
                                              int64_t row, int half, float2* share, uint32_t ready,
                                              uint32_t parity, volatile int* dead)
 {
-    const int64_t c0 = (int64_t)t.n * a.bn;
-    const int live = (int)min((int64_t)a.bn, a.V - c0);
+    const int64_t c0 = (int64_t)t.n * a.x.bn;
+    const int live = (int)min((int64_t)a.x.bn, a.V - c0);
     const int64_t y = target_of(a, row) - c0;                // of the tile, if in it
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
@@ -391,7 +405,7 @@ __device__ __forceinline__ bool epilogue_lse(const MmaArgs& a, const Unit& t, ui
         return true;
     }
     const bool ok = warp_wait(ready, parity, a.wait_limit, dead);
-    if (ok && row < a.rows) {
+    if (ok && row < a.x.rows) {
         join(top, sum, *share);
         a.part[(int64_t)t.n * a.part_ld + row] = make_float2(top, sum);
     }
@@ -432,17 +446,18 @@ __device__ __forceinline__ void write_rows(uint32_t buf, int lane, Store&& store
 
 // The tile's 128 rows of this CTA in bf16 (P, or the table's gradient): 64
 // columns at a time through the warp's buffer, 128 columns a warp.
-template <Kind K>
-__device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, uint32_t tmem,
-                                              int64_t row0, int lane, int half, uint32_t to)
+template <bool P>
+__device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Product& p, const Unit& t,
+                                              uint32_t tmem, int64_t row0, int lane, int half,
+                                              uint32_t to)
 {
-    const int64_t c0 = (int64_t)t.n * a.bn;
-    if (row0 >= a.rows) return;
+    const int64_t c0 = (int64_t)t.n * p.bn;
+    if (row0 >= p.rows) return;
     const int64_t row = row0 + lane;
     int64_t y = -1;
     float lse2 = 0.0f, g = 0.0f;
     bool live = true;
-    if constexpr (K == kDlogits) {
+    if constexpr (P) {
         y = target_of(a, row);
         live = y >= 0;
         lse2 = live ? a.lse[row] * kLog2e : 0.0f;
@@ -452,13 +467,13 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
         g = *a.unit;
     }
 #pragma unroll 1
-    for (int c = half * 128; c < min(a.bn, half * 128 + 128); c += 64) {
-        if (c0 + c >= a.cols) break;
+    for (int c = half * 128; c < min(p.bn, half * 128 + 128); c += 64) {
+        if (c0 + c >= p.cols) break;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float x[32];
             tmem_load32(tmem + c + 32 * h, x);
-            if constexpr (K == kDlogits) {
+            if constexpr (P) {
                 const int at = (int)(y - (c + 32 * h));
                 const bool here = live && y >= c + 32 * h && y < c + 32 * h + 32;
 #pragma unroll
@@ -482,12 +497,12 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
                         bf_pack(x[8 * j + 2], x[8 * j + 3]), bf_pack(x[8 * j + 4], x[8 * j + 5]),
                         bf_pack(x[8 * j + 6], x[8 * j + 7]));
         }
-        uint16_t* out = static_cast<uint16_t*>(a.out) + row0 * a.out_ld + c0 + c;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + row0 * p.out_ld + c0 + c;
         write_rows(to, lane, [&](int r, int chunk, const uint4& x) {
             // 8 columns at once: P's rows are padded to whole pieces, D is a multiple of 8
-            if (row0 + r < a.rows && c0 + c + chunk * 8 < a.cols) {
-                if constexpr (K == kDlogits) st16(out + r * a.out_ld + chunk * 8, x);
-                else st16_stream(out + r * a.out_ld + chunk * 8, x);
+            if (row0 + r < p.rows && c0 + c + chunk * 8 < p.cols) {
+                if constexpr (P) st16(out + r * p.out_ld + chunk * 8, x);
+                else st16_stream(out + r * p.out_ld + chunk * 8, x);
             }
         });
     }
@@ -498,22 +513,23 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Unit& t, u
 __device__ __forceinline__ void epilogue_f32(const MmaArgs& a, const Unit& t, uint32_t tmem,
                                              int64_t row0, int lane, int half, uint32_t to)
 {
-    const int64_t c0 = (int64_t)t.n * a.bn;
-    if (row0 >= a.rows) return;
+    const Product& p = a.x;
+    const int64_t c0 = (int64_t)t.n * p.bn;
+    if (row0 >= p.rows) return;
 #pragma unroll 1
-    for (int c = half * 128; c < min(a.bn, half * 128 + 128); c += 32) {
-        if (c0 + c >= a.cols) break;
+    for (int c = half * 128; c < min(p.bn, half * 128 + 128); c += 32) {
+        if (c0 + c >= p.cols) break;
         float x[32];
         tmem_load32(tmem + c, x);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             stage16(to, lane, j, __float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
                     __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
-        float* out = static_cast<float*>(a.out) + (t.split * a.out_split_rows + row0) * a.out_ld +
+        float* out = static_cast<float*>(p.out) + (t.split * a.out_split_rows + row0) * p.out_ld +
                      c0 + c;
         write_rows(to, lane, [&](int r, int chunk, uint4 x) {
-            if (row0 + r >= a.rows || c0 + c + chunk * 4 >= a.cols) return;
-            float4* at = reinterpret_cast<float4*>(out + r * a.out_ld + chunk * 4);
+            if (row0 + r >= p.rows || c0 + c + chunk * 4 >= p.cols) return;
+            float4* at = reinterpret_cast<float4*>(out + r * p.out_ld + chunk * 4);
             float4 f = make_float4(__uint_as_float(x.x), __uint_as_float(x.y),
                                    __uint_as_float(x.z), __uint_as_float(x.w));
             if (a.add) {
@@ -531,13 +547,12 @@ template <Kind K>
 __global__ void __launch_bounds__(kThreads, 1)
     k_mma(const __grid_constant__ MmaArgs a)
 {
-    using F = Form<K>;
-    constexpr int S = F::stages;
+    constexpr int S = kStages;
     extern __shared__ uint8_t raw[];
     // the swizzle pattern needs 1024-byte aligned stages, at the same place in both CTAs
     const uint32_t smem = (smem_u32(raw) + 1023u) & ~1023u;
     const uint32_t staging = smem + S * kStageBytes;
-    const uint32_t bars = staging + (F::out ? kStaging : kShares);
+    const uint32_t bars = staging + (K == kLse ? kShares : kStaging);
     const uint32_t full = bars, empty = bars + 8 * S;
     const uint32_t sums_full = empty + 8 * S, sums_empty = sums_full + 16;
     const uint32_t drained = sums_empty + 16;
@@ -575,26 +590,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(tmem) : "r"(slot));
     asm volatile("fence.proxy.async.global;" ::: "memory");
 
-    const int units = a.m_tiles * a.n_tiles * a.splits;
-    const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     bool drain_failed = false;
 
     if (warp == 0) {                                     // ---- loads
         uint32_t s = 0, ph = 0, issued = 0;              // stage, its phase, loads so far
         bool ok = true;
-        // both CTAs' boxes of a stage (a box always counts in full)
-        const uint32_t stage_tx = 2 * (kStageBytes / 2 + (F::b_k ? a.bn / 2 * 128 : kStageBytes / 2));
         const uint32_t leader_full = in_leader(full);
-        for (int u = first; u < units && ok; u += stride) {
-            const Unit t = unit_at(a, u);
-            const int ra = t.m * BM + (int)rank * 128, rb = t.n * a.bn + (int)rank * (a.bn / 2);
+        for (int i = 0, u; ok && (u = unit_of(a, pair, pairs, i)) >= 0; ++i) {
+            const bool first = K != kGrads || u < a.x_units;
+            const Product& p = first ? a.x : a.y;
+            const Unit t = unit_at(p, first ? u : u - a.x_units);
+            const int ra = t.m * BM + (int)rank * 128, rb = t.n * p.bn + (int)rank * (p.bn / 2);
+            // both CTAs' boxes of a stage (a box always counts in full)
+            const uint32_t stage_tx =
+                2 * (kStageBytes / 2 + (K == kGrads ? kStageBytes / 2 : p.bn / 2 * 128));
             for (int kb = t.k0; kb < t.k1; ++kb) {
                 if (!(ok = warp_wait(empty + 8 * s, ph ^ 1, a.wait_limit, dead))) break;
                 if (elect()) {
                     if (leader) mbar_expect(full + 8 * s, stage_tx);
                     const uint32_t dst = smem + s * kStageBytes, bar = leader_full + 8 * s;
-                    load_operand<F::a_k>(dst, &a.a, ra, kb * BK, bar);
-                    load_operand<F::b_k>(dst + kStageBytes / 2, &a.b, rb, kb * BK, bar);
+                    if (first) Layout<true>::load(dst, &p.a, ra, kb * BK, bar);
+                    else Layout<false>::load(dst, &p.a, ra, kb * BK, bar);
+                    Layout<K != kGrads>::load(dst + kStageBytes / 2, &p.b, rb, kb * BK, bar);
                 }
                 __syncwarp();
                 ++issued;
@@ -615,13 +633,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 drain_failed |= !mbar_wait(full + 8 * (j % S), (j / S) & 1, kDrainLimit, &none);
         }
     } else if (warp == 1 && leader) {                    // ---- products
-        const uint32_t idesc = instruction<K>(a.bn);
         uint32_t s = 0, ph = 0;
-        int i = 0;
         bool ok = true;
-        for (int u = first; u < units && ok; u += stride, ++i) {
-            const Unit t = unit_at(a, u);
-            const int b = i & 1, nk = t.k1 - t.k0;
+        for (int i = 0, u; ok && (u = unit_of(a, pair, pairs, i)) >= 0; ++i) {
+            const bool first = K != kGrads || u < a.x_units;
+            const Product& p = first ? a.x : a.y;
+            const Unit t = unit_at(p, first ? u : u - a.x_units);
+            const int b = i & 1, nk = t.k1 - t.k0, bn = p.bn;
             if (!(ok = warp_wait(sums_empty + 8 * b, ((i >> 1) & 1) ^ 1, a.wait_limit, dead)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -633,11 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (++s == S) { s = 0; ph ^= 1; }
                 if (k + 1 < nk) ready = __all_sync(0xFFFFFFFFu, mbar_try(full + 8 * s, ph));
                 if (elect()) {
-                    const uint64_t da = operand<F::a_k>(at), db = operand<F::b_k>(at + kStageBytes / 2);
-#pragma unroll
-                    for (int q = 0; q < BK / 16; ++q)
-                        mma(tmem + b * BN, da + q * operand_step<F::a_k>(),
-                            db + q * operand_step<F::b_k>(), idesc, k > 0 || q > 0);
+                    if (first) products<true, K != kGrads>(tmem + b * BN, at, bn, k > 0);
+                    else products<false, false>(tmem + b * BN, at, bn, k > 0);
                     mma_commit(done);
                 }
                 __syncwarp();
@@ -656,9 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = (warp - 4) >> 2;                // and half of the columns
         const uint32_t buf = staging + (warp - 4) * kWarpStage;
         float2* share = reinterpret_cast<float2*>(raw + (staging - smem_u32(raw))) + q * 32 + lane;
-        int i = 0;
-        for (int u = first; u < units; u += stride, ++i) {
-            const Unit t = unit_at(a, u);
+        for (int i = 0, u; (u = unit_of(a, pair, pairs, i)) >= 0; ++i) {
+            const bool first = K != kGrads || u < a.x_units;
+            const Product& p = first ? a.x : a.y;
+            const Unit t = unit_at(p, first ? u : u - a.x_units);
             const int b = i & 1;
             if (!warp_wait(sums_full + 8 * b, (i >> 1) & 1, a.wait_limit, dead)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -668,8 +684,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!epilogue_lse(a, t, from, row0 + lane, half, share + b * 128,
                                   shared_full + 8 * (4 * b + q), (i >> 1) & 1, dead))
                     break;
-            } else if constexpr (K == kDh) epilogue_f32(a, t, from, row0, lane, half, buf);
-            else epilogue_bf16<K>(a, t, from, row0, lane, half, buf);
+            } else if constexpr (K == kP) {
+                epilogue_bf16<true>(a, p, t, from, row0, lane, half, buf);
+            } else if (first) {
+                epilogue_f32(a, t, from, row0, lane, half, buf);
+            } else {
+                epilogue_bf16<false>(a, p, t, from, row0, lane, half, buf);
+            }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(in_leader(sums_empty + 8 * b));
@@ -871,14 +892,28 @@ int tile_width(int64_t n, int64_t m_tiles, int64_t splits, int step)
 }
 
 template <Kind K>
-cudaError_t run_mma(const MmaArgs& a, cudaStream_t st)
+cudaError_t run_mma(MmaArgs& a, cudaStream_t st)
 {
     static std::atomic<uint64_t> smem_set;
     const cudaError_t e =
         allow_smem(reinterpret_cast<const void*>(&k_mma<K>), smem_bytes<K>(), smem_set);
     if (e != cudaSuccess) return e;
-    const int units = a.m_tiles * a.n_tiles * a.splits;
-    const int pairs = std::max(1, std::min(units, device_sms() / 2));
+    const int pairs = std::max(1, std::min(a.x.units() + (K == kGrads ? a.y.units() : 0),
+                                           device_sms() / 2));
+    a.x_units = a.x.units();
+    a.y_units = K == kGrads ? a.y.units() : 0;
+    a.light = pairs;
+    if (K == kGrads && a.x_units % pairs != 0) {
+        // Units of x are long and do not come out even over the pairs; those that
+        // got one less take as many of y's as last as long.
+        a.light = a.x_units % pairs;
+        // (A unit takes no less than its epilogue, about 12 stages' time.)
+        const auto cost = [](const Product& p) {
+            return (int64_t)std::max(12, (p.k_blocks + p.splits - 1) / p.splits) * (p.bn + 64);
+        };
+        const int64_t each = (cost(a.x) + cost(a.y) / 2) / cost(a.y);
+        a.extra = (int32_t)std::min<int64_t>(a.y_units, each * (pairs - a.light));
+    }
     return launch_clusters(k_mma<K>, dim3((unsigned)(2 * pairs)), kThreads, smem_bytes<K>(), 2, st,
                            a);
 }
@@ -978,16 +1013,17 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
 
     uint8_t* base = static_cast<uint8_t*>(scratch);
     MmaArgs a{};
-    a.m_tiles = tiles(T);
-    a.bn = tile_width(V, a.m_tiles, 1, 16);
-    a.n_tiles = tiles(V, a.bn);
-    if (!encode(&a.a, h, D, T, h_ld, 128) || !encode(&a.b, table, D, V, D, a.bn / 2))
+    Product& x = a.x;
+    x.m_tiles = tiles(T);
+    x.bn = tile_width(V, x.m_tiles, 1, 16);
+    x.n_tiles = tiles(V, x.bn);
+    if (!encode(&x.a, h, D, T, h_ld, 128) || !encode(&x.b, table, D, V, D, x.bn / 2))
         return ZERO_ERR_CUDA;
-    a.k_blocks = (D + BK - 1) / BK;
-    a.splits = 1;
-    a.m_fast = 1;
-    a.rows = T;
-    a.cols = V;
+    x.k_blocks = (D + BK - 1) / BK;
+    x.splits = 1;
+    x.m_fast = 1;
+    x.rows = T;
+    x.cols = V;
     a.token_bytes = target_bytes;
     a.targets = targets;
     a.V = V;
@@ -999,7 +1035,7 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = run_mma<kLse>(a, st);
     if (e == cudaSuccess) {
-        const JoinArgs j{a.part, a.at_target, targets, s.part_ld, T, V, a.n_tiles, target_bytes,
+        const JoinArgs j{a.part, a.at_target, targets, s.part_ld, T, V, x.n_tiles, target_bytes,
                          loss, lse, dev_status};
         e = launch(k_xent_join, dim3((unsigned)((T + 31) / 32)), 1024, 0, st, j);
     }
@@ -1070,7 +1106,9 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         const int64_t n = std::min(g.piece, V - v0);
         const uint16_t* rows = table + v0 * D;
 
-        MmaArgs p = common;                                 // P = f(h E^T)
+        MmaArgs first = common;                             // P = f(h E^T)
+        first.v0 = v0;
+        Product& p = first.x;
         p.m_tiles = tiles(T);
         p.bn = tile_width(n, p.m_tiles, 1, 64);
         p.n_tiles = tiles(n, p.bn);
@@ -1083,10 +1121,10 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         p.m_fast = 1;
         p.rows = T;
         p.cols = n;
-        p.v0 = v0;
-        if ((e = run_mma<kDlogits>(p, st)) != cudaSuccess) break;
+        if ((e = run_mma<kP>(first, st)) != cudaSuccess) break;
 
-        MmaArgs d = common;                                 // dh += P E
+        MmaArgs second = common;
+        Product& d = second.x;                              // dh += P E
         if (!encode(&d.a, P, n, T, g.piece, 128) || !encode(&d.b, rows, D, n, D, 64))
             return ZERO_ERR_CUDA;
         d.out = sums;
@@ -1098,11 +1136,10 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         d.n_tiles = tiles(D, d.bn);
         d.rows = T;
         d.cols = D;
-        d.out_split_rows = g.split_rows;
-        d.add = v0 > 0;
-        if ((e = run_mma<kDh>(d, st)) != cudaSuccess) break;
+        second.out_split_rows = g.split_rows;
+        second.add = v0 > 0;
 
-        MmaArgs w = common;                                 // dE = P^T h
+        Product& w = second.y;                              // dE = P^T h
         if (!encode(&w.a, P, n, T, g.piece, 64) || !encode(&w.b, clean, D, T, D, 64))
             return ZERO_ERR_CUDA;
         w.out = dtable + v0 * D;
@@ -1114,7 +1151,7 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         w.splits = 1;
         w.rows = n;
         w.cols = D;
-        e = run_mma<kDtable>(w, st);
+        e = run_mma<kGrads>(second, st);
     }
     if (e == cudaSuccess) {
         const FinishArgs f{sums, unit, dh, T, g.split_rows, dh_ld, D, g.splits};
