@@ -77,6 +77,14 @@ struct Product {
     int32_t m_tiles, n_tiles, bn;      // tiles of 256 x bn
     int32_t k_blocks, splits;          // blocks of 64 along the summed dimension; its splits
     int32_t m_fast;                    // which tile coordinate runs fastest
+    // Rows of a box of `a` where it is contiguous along the sum, and how many of
+    // the pair's CTAs load one: filling the rest of a mostly empty tile with
+    // zeros took longer than reading it (17 tokens longer than 256), and what
+    // stands in rows past the last goes nowhere.
+    int32_t a_box, a_ctas;
+    // Along the sum, the last stage's steps of 16, and the rows of its boxes
+    // where an operand is contiguous the other way (one stage only, else 64).
+    int32_t last_steps, k_box;
     int64_t rows, cols;                // of the result (of the piece)
     int32_t units() const { return m_tiles * n_tiles * splits; }
 };
@@ -282,7 +290,7 @@ __device__ __forceinline__ uint32_t instruction(int bn)
     return 1u << 4 | 1u << 7 | 1u << 10 | (A_K ? 0u : 1u << 15) | (B_K ? 0u : 1u << 16) |
            (uint32_t)(bn >> 3) << 17 | (uint32_t)(BM >> 4) << 24;
 }
-// One stage's four products.
+// One stage's products.
 template <bool A_K, bool B_K>
 __device__ __forceinline__ void products(uint32_t d, uint32_t at, int bn, bool add)
 {
@@ -292,6 +300,17 @@ __device__ __forceinline__ void products(uint32_t d, uint32_t at, int bn, bool a
 #pragma unroll
     for (int q = 0; q < BK / 16; ++q)
         mma(d, da + q * Layout<A_K>::step, db + q * Layout<B_K>::step, idesc, add || q > 0);
+}
+// The first `steps` of them, where the sum ends in the stage.
+template <bool A_K, bool B_K>
+__device__ __forceinline__ void products_end(uint32_t d, uint32_t at, int bn, bool add, int steps)
+{
+    const uint64_t da = Layout<A_K>::descriptor(at);
+    const uint64_t db = Layout<B_K>::descriptor(at + kStageBytes / 2);
+#pragma unroll 1
+    for (int q = 0; q < steps; ++q)
+        mma(d, da + q * Layout<A_K>::step, db + q * Layout<B_K>::step, instruction<A_K, B_K>(bn),
+            add || q > 0);
 }
 
 // The i-th unit of work of a CTA pair, or -1: x's units by turns, then (for
@@ -603,21 +622,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Unit t = unit_at(p, first ? u : u - a.x_units);
             const int ra = t.m * BM + (int)rank * 128, rb = t.n * p.bn + (int)rank * (p.bn / 2);
             // both CTAs' boxes of a stage (a box always counts in full)
-            const uint32_t stage_tx =
-                2 * (kStageBytes / 2 + (K == kGrads ? kStageBytes / 2 : p.bn / 2 * 128));
-            for (int kb = t.k0; kb < t.k1; ++kb) {
-                if (!(ok = warp_wait(empty + 8 * s, ph ^ 1, a.wait_limit, dead))) break;
-                if (elect()) {
-                    if (leader) mbar_expect(full + 8 * s, stage_tx);
-                    const uint32_t dst = smem + s * kStageBytes, bar = leader_full + 8 * s;
-                    if (first) Layout<true>::load(dst, &p.a, ra, kb * BK, bar);
-                    else Layout<false>::load(dst, &p.a, ra, kb * BK, bar);
-                    Layout<K != kGrads>::load(dst + kStageBytes / 2, &p.b, rb, kb * BK, bar);
+            const uint32_t stage_tx = (first ? p.a_ctas * p.a_box : 4 * p.k_box) * 128 +
+                                      (K == kGrads ? 4 * p.k_box : p.bn) * 128;
+            // (a loop for each way to load `a`: any condition inside it is paid for
+            // by the tensor cores)
+            auto stages = [&](auto load_a) {
+                for (int kb = t.k0; kb < t.k1; ++kb) {
+                    if (!(ok = warp_wait(empty + 8 * s, ph ^ 1, a.wait_limit, dead))) break;
+                    if (elect()) {
+                        if (leader) mbar_expect(full + 8 * s, stage_tx);
+                        const uint32_t dst = smem + s * kStageBytes, bar = leader_full + 8 * s;
+                        load_a(dst, kb * BK, bar);
+                        Layout<K != kGrads>::load(dst + kStageBytes / 2, &p.b, rb, kb * BK, bar);
+                    }
+                    __syncwarp();
+                    ++issued;
+                    if (++s == S) { s = 0; ph ^= 1; }
                 }
-                __syncwarp();
-                ++issued;
-                if (++s == S) { s = 0; ph ^= 1; }
-            }
+            };
+            if (!first)
+                stages([&](uint32_t dst, int k, uint32_t bar) {
+                    Layout<false>::load(dst, &p.a, ra, k, bar);
+                });
+            else if ((int)rank < p.a_ctas)
+                stages([&](uint32_t dst, int k, uint32_t bar) {
+                    Layout<true>::load(dst, &p.a, ra, k, bar);
+                });
+            else
+                stages([](uint32_t, int, uint32_t) {});
         }
         // Before this CTA may leave: the products' last arrivals at its
         // barriers; or, after a wait ran out, the copies that were issued (both
@@ -640,22 +672,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Product& p = first ? a.x : a.y;
             const Unit t = unit_at(p, first ? u : u - a.x_units);
             const int b = i & 1, nk = t.k1 - t.k0, bn = p.bn;
+            // a last stage that the sum ends in
+            const int end = t.k1 == p.k_blocks && p.last_steps < BK / 16 ? nk - 1 : nk;
             if (!(ok = warp_wait(sums_empty + 8 * b, ((i >> 1) & 1) ^ 1, a.wait_limit, dead)))
                 break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             // the next stage is looked at before this one's products are issued
             bool ready = __all_sync(0xFFFFFFFFu, mbar_try(full + 8 * s, ph));
-            for (int k = 0; k < nk; ++k) {
-                if (!ready && !(ok = warp_wait(full + 8 * s, ph, a.wait_limit, dead))) break;
-                const uint32_t at = smem + s * kStageBytes, done = empty + 8 * s;
-                if (++s == S) { s = 0; ph ^= 1; }
-                if (k + 1 < nk) ready = __all_sync(0xFFFFFFFFu, mbar_try(full + 8 * s, ph));
-                if (elect()) {
-                    if (first) products<true, K != kGrads>(tmem + b * BN, at, bn, k > 0);
-                    else products<false, false>(tmem + b * BN, at, bn, k > 0);
-                    mma_commit(done);
+            auto stages = [&](int from, int to, auto issue) {
+                for (int k = from; k < to; ++k) {
+                    if (!ready && !(ok = warp_wait(full + 8 * s, ph, a.wait_limit, dead))) return;
+                    const uint32_t at = smem + s * kStageBytes, done = empty + 8 * s;
+                    if (++s == S) { s = 0; ph ^= 1; }
+                    if (k + 1 < nk) ready = __all_sync(0xFFFFFFFFu, mbar_try(full + 8 * s, ph));
+                    if (elect()) {
+                        issue(at, k > 0);
+                        mma_commit(done);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+            };
+            const uint32_t d = tmem + b * BN;
+            if (first) {
+                stages(0, end, [&](uint32_t at, bool add) {
+                    products<true, K != kGrads>(d, at, bn, add);
+                });
+                if (ok) stages(end, nk, [&](uint32_t at, bool add) {
+                    products_end<true, K != kGrads>(d, at, bn, add, p.last_steps);
+                });
+            } else {
+                stages(0, end, [&](uint32_t at, bool add) {
+                    products<false, false>(d, at, bn, add);
+                });
+                if (ok) stages(end, nk, [&](uint32_t at, bool add) {
+                    products_end<false, false>(d, at, bn, add, p.last_steps);
+                });
             }
             if (ok && elect()) mma_commit(sums_full + 8 * b);
             __syncwarp();
@@ -891,6 +942,16 @@ int tile_width(int64_t n, int64_t m_tiles, int64_t splits, int step)
     return best;
 }
 
+// Where the sum of length `k` and the rows of `a` end.
+void set_boxes(Product& p, int64_t k)
+{
+    p.k_blocks = (int32_t)((k + BK - 1) / BK);
+    p.last_steps = (int32_t)((k - (int64_t)(p.k_blocks - 1) * BK + 15) / 16);
+    p.k_box = p.k_blocks == 1 ? 16 * p.last_steps : BK;
+    p.a_box = (int32_t)std::min<int64_t>(128, up(p.rows, 8));
+    p.a_ctas = p.rows <= 128 ? 1 : 2;
+}
+
 template <Kind K>
 cudaError_t run_mma(MmaArgs& a, cudaStream_t st)
 {
@@ -1017,13 +1078,13 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
     x.m_tiles = tiles(T);
     x.bn = tile_width(V, x.m_tiles, 1, 16);
     x.n_tiles = tiles(V, x.bn);
-    if (!encode(&x.a, h, D, T, h_ld, 128) || !encode(&x.b, table, D, V, D, x.bn / 2))
-        return ZERO_ERR_CUDA;
-    x.k_blocks = (D + BK - 1) / BK;
     x.splits = 1;
     x.m_fast = 1;
     x.rows = T;
     x.cols = V;
+    set_boxes(x, D);
+    if (!encode(&x.a, h, D, T, h_ld, x.a_box) || !encode(&x.b, table, D, V, D, x.bn / 2))
+        return ZERO_ERR_CUDA;
     a.token_bytes = target_bytes;
     a.targets = targets;
     a.V = V;
@@ -1112,45 +1173,45 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         p.m_tiles = tiles(T);
         p.bn = tile_width(n, p.m_tiles, 1, 64);
         p.n_tiles = tiles(n, p.bn);
-        if (!encode(&p.a, h, D, T, h_ld, 128) || !encode(&p.b, rows, D, n, D, p.bn / 2))
-            return ZERO_ERR_CUDA;
         p.out = P;
         p.out_ld = g.piece;
-        p.k_blocks = (D + BK - 1) / BK;
         p.splits = 1;
         p.m_fast = 1;
         p.rows = T;
         p.cols = n;
+        set_boxes(p, D);
+        if (!encode(&p.a, h, D, T, h_ld, p.a_box) || !encode(&p.b, rows, D, n, D, p.bn / 2))
+            return ZERO_ERR_CUDA;
         if ((e = run_mma<kP>(first, st)) != cudaSuccess) break;
 
         MmaArgs second = common;
         Product& d = second.x;                              // dh += P E
-        if (!encode(&d.a, P, n, T, g.piece, 128) || !encode(&d.b, rows, D, n, D, 64))
-            return ZERO_ERR_CUDA;
         d.out = sums;
         d.out_ld = D;
-        d.k_blocks = (int32_t)((n + BK - 1) / BK);
+        d.rows = T;
+        d.cols = D;
+        set_boxes(d, n);
+        if (!encode(&d.a, P, n, T, g.piece, d.a_box) || !encode(&d.b, rows, D, n, D, d.k_box))
+            return ZERO_ERR_CUDA;
         d.splits = std::min(g.splits, d.k_blocks);
         d.m_tiles = tiles(T);
         d.bn = tile_width(D, d.m_tiles, d.splits, 64);
         d.n_tiles = tiles(D, d.bn);
-        d.rows = T;
-        d.cols = D;
         second.out_split_rows = g.split_rows;
         second.add = v0 > 0;
 
         Product& w = second.y;                              // dE = P^T h
-        if (!encode(&w.a, P, n, T, g.piece, 64) || !encode(&w.b, clean, D, T, D, 64))
+        w.rows = n;
+        w.cols = D;
+        set_boxes(w, T);
+        if (!encode(&w.a, P, n, T, g.piece, w.k_box) || !encode(&w.b, clean, D, T, D, w.k_box))
             return ZERO_ERR_CUDA;
         w.out = dtable + v0 * D;
         w.out_ld = D;
         w.m_tiles = tiles(n);
         w.bn = tile_width(D, w.m_tiles, 1, 64);
         w.n_tiles = tiles(D, w.bn);
-        w.k_blocks = (int32_t)((T + BK - 1) / BK);
         w.splits = 1;
-        w.rows = n;
-        w.cols = D;
         e = run_mma<kGrads>(second, st);
     }
     if (e == cudaSuccess) {
