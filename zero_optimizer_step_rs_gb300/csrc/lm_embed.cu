@@ -133,6 +133,11 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
     const int64_t part = (a.T + a.cluster - 1) / a.cluster;
     const int64_t lo = min((int64_t)blockIdx.x * part, a.T), hi = min(lo + part, a.T);
     const bool one_round = part <= kSortRound;
+    // the lists that the first pass scatters into, met before they are written
+    for (int64_t i = lo + tid * 32; i < hi; i += kSortThreads * 32) {
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.key1 + i));
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pos1 + i));
+    }
     uint32_t* mine = warp_bins + warp * bins;
     for (int pass = 0; pass < a.passes; ++pass) {
         const uint32_t* key_in = pass & 1 ? a.key1 : a.key0;
@@ -363,54 +368,57 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_consta
     if (r.n == 0) return;
 
     // places [from, to) of the chunk and the C after it, a batch of rows at a
-    // time: the rows, and what the gradient holds where a run ends, are all
-    // asked for before the first is added
+    // time, all asked for before the first is added; what the gradient holds
+    // where a run ends is brought into L2 meanwhile (registers for it would
+    // halve the resident warps)
     const int from = r.head_long ? 0 : r.skip;
     const int to = r.n + r.more;
-    // bit s: place s is the last of its run (or of what is summed here)
-    uint64_t ends;
+    // bit s: place s is the last of its run (or of what is summed here); and
+    // place s is of a long run
+    uint64_t ends, longs;
     {
         constexpr uint32_t PLACES = C == 32 ? ALL : (1u << (C & 31)) - 1;
         const uint32_t up = __shfl_down_sync(ALL, r.cur, 1), first_next = __shfl_sync(ALL, r.next, 0);
-        const uint32_t a0 =
-            __ballot_sync(ALL, r.cur != (lane == C - 1 ? first_next : up)) & PLACES;
-        ends = a0 | 1ull << (to - 1);
-        // the tail run goes on: its last place is to - 1, past the chunk
-        if (r.more > 0) ends &= ~(((1ull << r.more) - 1) << (C - 1));
+        ends = (__ballot_sync(ALL, r.cur != (lane == C - 1 ? first_next : up)) & PLACES) |
+               1ull << (to - 1);
+        longs = (r.head_long ? (1ull << r.skip) - 1 : 0) |
+                (r.tail_long ? (1ull << C) - (1ull << r.tail) : 0);
     }
     const uint16_t* dy = a.dy + col;
     uint16_t* grad = a.grad + col;
     float acc[8] = {};
     for (int b = from; b < to; b += kBatch) {
-        uint4 x[kBatch], old[ACC ? kBatch : 1];
+        // the batch's places: bit q stands for place b + q
+        const uint32_t in = to - b >= kBatch ? (1u << kBatch) - 1 : (1u << (to - b)) - 1;
+        const uint32_t end = (uint32_t)(ends >> b) & in, part = (uint32_t)(longs >> b);
+        uint4 x[kBatch];
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int s = b + q;
-            const uint32_t t = __shfl_sync(ALL, s < C ? pos_cur : pos_next, s & (C - 1));
+            const uint32_t t = __shfl_sync(ALL, b + q < C ? pos_cur : pos_next, b + q & (C - 1));
             x[q] = make_uint4(0, 0, 0, 0);
-            if (on && s < to) x[q] = ld16_stream(dy + t * a.dy_ld);
-            if constexpr (ACC) {
+            if (on && (in >> q & 1)) x[q] = ld16_stream(dy + t * a.dy_ld);
+        }
+        if constexpr (ACC) {
+            for (uint32_t m = end & ~part; m; m &= m - 1) {
+                const int s = b + __ffs(m) - 1;
                 const uint32_t v = __shfl_sync(ALL, s < C ? r.cur : r.next, s & (C - 1));
-                const bool part = (r.head_long && s < r.skip) || (r.tail_long && s >= r.tail);
-                old[q] = make_uint4(0, 0, 0, 0);
-                if (on && s < to && (ends >> s & 1) && !part)
-                    old[q] = ld16(grad + (int64_t)v * a.D);
+                if (on) asm volatile("prefetch.global.L2 [%0];" ::"l"(grad + (int64_t)v * a.D));
             }
         }
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int s = b + q;
             add8(acc, x[q]);
-            if (s >= to || !(ends >> s & 1)) continue;             // the same for the whole warp
+            if (!(end >> q & 1)) continue;                         // the same for the whole warp
+            const int s = b + q;
             const uint32_t v = __shfl_sync(ALL, s < C ? r.cur : r.next, s & (C - 1));
-            const bool head = r.head_long && s < r.skip, tail = r.tail_long && s >= r.tail;
-            if (on && (head || tail)) {
-                float* part = a.parts + (2 * c + (tail ? 1 : 0)) * a.D + col;
-                *reinterpret_cast<float4*>(part) = make_float4(acc[0], acc[1], acc[2], acc[3]);
-                *reinterpret_cast<float4*>(part + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            if (on && (part >> q & 1)) {
+                float* to_part = a.parts + (2 * c + (s >= r.skip ? 1 : 0)) * a.D + col;
+                *reinterpret_cast<float4*>(to_part) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+                *reinterpret_cast<float4*>(to_part + 4) =
+                    make_float4(acc[4], acc[5], acc[6], acc[7]);
             } else if (on) {
                 float f[8] = {};
-                if constexpr (ACC) bf_unpack8(old[q], f);
+                if constexpr (ACC) bf_unpack8(ld16(grad + (int64_t)v * a.D), f);
 #pragma unroll
                 for (int z = 0; z < 8; ++z) f[z] += acc[z] * a.scale;
                 st16(grad + (int64_t)v * a.D, bf_pack8(f));
@@ -453,8 +461,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const __grid_consta
         const int64_t c = group + (int64_t)k * groups;
         // the first place past the run, by 32 probes at a time
         int64_t lo = (c + 1) * C, hi = a.T;
-        while (lo < hi) {
-            const int64_t gap = (hi - lo + 31) / 32, at = lo + lane * gap;
+        for (int64_t near = 32; lo < hi; near = hi) {          // most are found near the start
+            const int64_t gap = min(near, (hi - lo + 31) / 32), at = lo + lane * gap;
             const uint32_t past =
                 __ballot_sync(0xFFFFFFFFu, at >= hi || a.key[at < hi ? at : hi - 1] > v);
             const int k = past ? __ffs(past) - 1 : 32;         // probes before k are in the run
