@@ -102,6 +102,7 @@ struct SortArgs {
     uint32_t* pos0;
     uint32_t* pos1;
     uint32_t* counts;                // [2][kMaxCluster][kMaxBins], by turns
+    int32_t* long_runs;              // set to 0 for the next launch
     int32_t passes, bits;            // digits of `bits` bits
     int32_t cluster;
     uint4* zero;                     // the gradient to fill, or null
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
         return;
     }
 
+    if (blockIdx.x == 0 && tid == 0) *a.long_runs = 0;
     const int bins = 1 << a.bits;
     const int64_t part = (a.T + a.cluster - 1) / a.cluster;
     const int64_t lo = min((int64_t)blockIdx.x * part, a.T), hi = min(lo + part, a.T);
@@ -295,6 +297,7 @@ struct GradArgs {
     const uint32_t* pos;
     uint16_t* grad;
     float* parts;                            // [2 * chunks][D]: a chunk's head and tail
+    int32_t* long_runs;                      // their number, and then the chunks they start in
     int64_t T, V, dy_ld;
     int32_t D, slices, chunks, accumulate;
     float scale;
@@ -366,6 +369,9 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_consta
     const uint32_t pos_next = lane < C && i0 + C + lane < a.T ? a.pos[i0 + C + lane] : 0;
     const ChunkRuns r = chunk_runs<C>(a.key, a.T, a.V, c, lane);
     if (r.n == 0) return;
+    // (in any order: each run is joined by itself)
+    if (r.tail_long && w % a.slices == 0 && lane == 0)
+        a.long_runs[1 + atomicAdd(a.long_runs, 1)] = (int32_t)c;
 
     // places [from, to) of the chunk and the C after it, a batch of rows at a
     // time, all asked for before the first is added; what the gradient holds
@@ -430,35 +436,21 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_consta
 }
 
 // Joins the parts of each long run: the chunk where the run starts has a tail
-// part, the next ones head parts.  A block looks at 8 chunks (one a warp, a
-// grid's stride apart, since frequent tokens lie together) and then sums the
-// runs it found, its 8 warps a consecutive share of the parts each, and the
-// shares in order.
+// part, the next ones head parts.  A block takes a run and 256 columns: its 8
+// warps add a consecutive share of the parts each, and the shares are added in
+// order.
 template <int C>
 __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const __grid_constant__ GradArgs a)
 {
     pdl_enter();
     constexpr int W = kJoinThreads / 32;
     __shared__ float share[W][kColumns];
-    __shared__ uint32_t run_key[W];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int groups = (a.chunks + W - 1) / W;
-    const int group = blockIdx.x / a.slices;
-    const int col = (int)(blockIdx.x % a.slices) * kColumns + lane * 8;
-    {
-        const int64_t c = group + (int64_t)warp * groups;
-        uint32_t v = (uint32_t)a.V;
-        if (c < a.chunks) {
-            const ChunkRuns r = chunk_runs<C>(a.key, a.T, a.V, c, lane);
-            if (r.tail_long) v = __shfl_sync(0xFFFFFFFFu, r.cur, C - 1);
-        }
-        if (lane == 0) run_key[warp] = v;
-    }
-    __syncthreads();
-    for (int k = 0; k < W; ++k) {
-        const uint32_t v = run_key[k];
-        if (v == (uint32_t)a.V) continue;                      // the same in every warp
-        const int64_t c = group + (int64_t)k * groups;
+    const int64_t items = (int64_t)a.long_runs[0] * a.slices;
+    for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+        const int64_t c = a.long_runs[1 + item / a.slices];
+        const int col = (int)(item % a.slices) * kColumns + lane * 8;
+        const uint32_t v = a.key[c * C + C - 1];
         // the first place past the run, by 32 probes at a time
         int64_t lo = (c + 1) * C, hi = a.T;
         for (int64_t near = 32; lo < hi; near = hi) {          // most are found near the start
@@ -483,7 +475,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const __grid_consta
                 acc[4] += y.x; acc[5] += y.y; acc[6] += y.z; acc[7] += y.w;
             }
         }
-        __syncthreads();
 #pragma unroll
         for (int q = 0; q < 8; ++q) share[warp][q * 32 + lane] = acc[q];
         __syncthreads();
@@ -498,6 +489,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const __grid_consta
             for (int q = 0; q < 8; ++q) f[q] += acc[q] * a.scale;
             st16(p, bf_pack8(f));
         }
+        __syncthreads();
     }
 }
 
@@ -519,15 +511,15 @@ cudaError_t launch_grad(GradArgs a, cudaStream_t st)
     cudaError_t e = launch(a.accumulate ? k_embed_grad<C, true> : k_embed_grad<C, false>, grid,
                            kGradThreads, 0, st, a);
     if (e == cudaSuccess && a.T > C) {
-        constexpr int W = kJoinThreads / 32;
-        const int64_t groups = (a.chunks + W - 1) / W;
-        e = launch(k_embed_join<C>, dim3((unsigned)(groups * a.slices)), kJoinThreads, 0, st, a);
+        // a long run has more than C places, so there are fewer of them than chunks
+        const int64_t blocks = std::min<int64_t>((int64_t)a.chunks * a.slices, 6 * device_sms());
+        e = launch(k_embed_join<C>, dim3((unsigned)blocks), kJoinThreads, 0, st, a);
     }
     return e;
 }
 
 struct GradScratch {
-    int64_t key0, key1, pos0, pos1, counts, parts, bytes;
+    int64_t key0, key1, pos0, pos1, counts, long_runs, parts, bytes;
 };
 
 GradScratch grad_scratch(int64_t T, int32_t D)
@@ -539,8 +531,9 @@ GradScratch grad_scratch(int64_t T, int32_t D)
     s.pos0 = 2 * list;
     s.pos1 = 3 * list;
     s.counts = 4 * list;
-    s.parts = s.counts + 2 * 4 * kMaxCluster * kMaxBins;
     const int C = chunk_places(T, D);
+    s.long_runs = s.counts + 2 * 4 * kMaxCluster * kMaxBins;
+    s.parts = s.long_runs + up(4 * (1 + (T + C - 1) / C), 256);
     s.bytes = s.parts + 8 * ((T + C - 1) / C) * (int64_t)D;
     return s;
 }
@@ -634,6 +627,7 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     s.pos0 = reinterpret_cast<uint32_t*>(base + g.pos0);
     s.pos1 = reinterpret_cast<uint32_t*>(base + g.pos1);
     s.counts = reinterpret_cast<uint32_t*>(base + g.counts);
+    s.long_runs = reinterpret_cast<int32_t*>(base + g.long_runs);
     int key_bits = 1;                                      // keys run to V itself
     while (key_bits < 32 && (V >> key_bits) != 0) ++key_bits;
     s.passes = (key_bits + 8) / 9;                         // digits of at most 9 bits
@@ -662,6 +656,7 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     a.pos = s.passes & 1 ? s.pos1 : s.pos0;
     a.grad = grad;
     a.parts = reinterpret_cast<float*>(base + g.parts);
+    a.long_runs = s.long_runs;
     a.T = T;
     a.V = V;
     a.dy_ld = dy_ld;

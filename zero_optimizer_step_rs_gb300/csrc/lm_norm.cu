@@ -410,6 +410,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_norm_join(const __grid_constan
     const int col = blockIdx.x * kJoinCols + cv * 4;
     float4 s = make_float4(0, 0, 0, 0);
     if (col < a.D)
+#pragma unroll 4
         for (int r = sh; r < a.blocks; r += kJoinShares) {
             const float4 x =
                 __ldcs(reinterpret_cast<const float4*>(a.parts + (int64_t)r * a.D + col));
@@ -433,8 +434,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_norm_join(const __grid_constan
     }
 }
 
+// Blocks of a form of k_norm_grad that fit on an SM, per device (0: not asked yet).
 template <int TPR, int NV>
-std::atomic<uint64_t> grad_smem_set;
+std::atomic<int> grad_per_sm[64];
 
 // The most blocks that k_norm_grad takes: 8 for each of 152 SMs, so 8 fp32 rows
 // of parts per SM.
@@ -595,16 +597,22 @@ extern "C" zero_status zero_norm_grad(const uint16_t* dy, int64_t dy_ld, const u
     a.dsum_ld = dsum_ld;
     a.dx_ld = dx_ld;
     a.D = D;
-    auto run = [&](void (*kernel)(NormGradArgs), int tpr, int smem, std::atomic<uint64_t>& done) {
+    auto run = [&](void (*kernel)(NormGradArgs), int tpr, int smem, std::atomic<int>* per_sm) {
         const int threads = tpr > 128 ? tpr : 128, groups = threads / tpr;
         // as many blocks as are resident at once: a second wave would be a short one
-        cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), smem, done);
-        int per_sm = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) !=
-                cudaSuccess || per_sm < 1)
-            per_sm = 1;
-        a.blocks = (int)std::min<int64_t>(
-            {(T + groups - 1) / groups, (int64_t)grad_blocks(T), (int64_t)per_sm * device_sms()});
+        int dev = 0;
+        cudaGetDevice(&dev);
+        int fit = per_sm[dev & 63].load(std::memory_order_relaxed);
+        cudaError_t e = cudaSuccess;
+        if (fit == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem);
+            if (e == cudaSuccess && fit > 0)
+                per_sm[dev & 63].store(fit, std::memory_order_relaxed);
+        }
+        a.blocks = (int)std::min<int64_t>({(T + groups - 1) / groups, (int64_t)grad_blocks(T),
+                                           (int64_t)std::max(1, fit) * device_sms()});
         if (e == cudaSuccess)
             e = launch(kernel, dim3((unsigned)a.blocks), threads, smem, st, a);
         if (e == cudaSuccess)
@@ -612,7 +620,7 @@ extern "C" zero_status zero_norm_grad(const uint16_t* dy, int64_t dy_ld, const u
                        kJoinThreads, 0, st, a);
         return status_of(e);
     };
-#define GRAD_GO(tpr, nv) run(k_norm_grad<tpr, nv>, tpr, grad_smem<tpr, nv>(), grad_smem_set<tpr, nv>)
+#define GRAD_GO(tpr, nv) run(k_norm_grad<tpr, nv>, tpr, grad_smem<tpr, nv>(), grad_per_sm<tpr, nv>)
     NORM_FORMS(GRAD_GO);
 #undef GRAD_GO
 }
