@@ -1,5 +1,9 @@
 """Build the in-tree C-ABI library libzero_step.so for sm_103a.
 
+The Python module _lm (csrc/lm_binding.cpp, the tensors' checks of the
+language-model operators) is compiled beside it with the host compiler against
+the installed torch's headers.
+
 The translation units (the step's CUDA kernels and entry points, the
 language-model operators' three, and the host-only plan and checkpoint code)
 are compiled in parallel by nvcc and linked into one shared library with the CUDA runtime linked statically, so the library needs no
@@ -8,9 +12,11 @@ called) on a machine without a GPU.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +30,8 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INC
 SOURCES = [os.path.join(CSRC, "zero_step.cu"), os.path.join(CSRC, "plan.cpp"),
            os.path.join(CSRC, "ckpt.cpp"), os.path.join(CSRC, "lm_embed.cu"),
            os.path.join(CSRC, "lm_norm.cu"), os.path.join(CSRC, "lm_xent.cu")]
+EXT = os.path.join(PKG, "_lm.so")
+EXT_SOURCE = os.path.join(CSRC, "lm_binding.cpp")
 HEADERS = [os.path.join(INCLUDE, "zero_step.h")] + sorted(
     os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cuh"))
 
@@ -34,10 +42,10 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(EXT)):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(p) > t for p in SOURCES + HEADERS + [__file__])
+    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
+    return any(os.path.getmtime(p) > t for p in SOURCES + [EXT_SOURCE] + HEADERS + [__file__])
 
 
 def compile_commands():
@@ -51,10 +59,23 @@ def compile_commands():
     return cmds, link
 
 
+def ext_command():
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+    include = [INCLUDE, os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_path("include"), cuda]
+    libs = os.path.join(torch, "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            *(x for i in include for x in ("-I", i)), EXT_SOURCE, "-o", EXT + ".tmp", "-L", libs,
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{libs}"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
     cmds, link = compile_commands()
+    cmds.append(ext_command())
     procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
              for c in cmds]
     failed = []
@@ -69,6 +90,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         raise RuntimeError(f"nvcc failed:\n{msg}")
     subprocess.run(link, check=True)
     os.replace(LIB + ".tmp", LIB)
+    os.replace(EXT + ".tmp", EXT)
     return LIB
 
 
