@@ -518,13 +518,127 @@ cudaError_t launch_grad(GradArgs a, cudaStream_t st)
     return e;
 }
 
+// ------------------------------------------------- the gradient, few tokens --
+// Up to 1024 tokens need no sort: a block takes a token and 1024 columns (256 a
+// warp), looks through all ids for its own, stops unless it is the first to
+// have it, and adds the rows.  One launch instead of three; other blocks fill
+// the rows that no token has with zeros (64 rows a block, after a look at the
+// same ids).  Measured against the sort: 64 x 768 into a tied table 18 -> 3 us,
+// 1023 x 768 into an untied one of 50257 rows 22.6 -> 17.6 us.
+
+constexpr int kFew = 1024;
+constexpr int kFewThreads = 128;
+constexpr int kFewBatch = 8;                 // rows in flight
+constexpr int kFillRows = 64;
+
+struct FewArgs {
+    const uint16_t* dy;
+    const void* tokens;
+    uint16_t* grad;
+    int64_t V, dy_ld;
+    int32_t T, D, slices, token_bytes, accumulate;
+    int32_t fills;                           // blocks that fill with zeros
+    float scale;
+    int32_t* status;
+};
+
+__global__ void __launch_bounds__(kFewThreads) k_embed_few(const __grid_constant__ FewArgs a)
+{
+    pdl_enter();
+    constexpr int W = kFewThreads / 32, EACH = kFew / kFewThreads;
+    __shared__ uint16_t list[kFew];
+    __shared__ uint32_t found[W];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int i0 = tid * EACH;                               // this thread's ids
+    if ((int)blockIdx.x < a.fills) {                         // zeros
+        const int64_t v0 = (int64_t)blockIdx.x * kFillRows;
+        const int n = (int)min((int64_t)kFillRows, a.V - v0);
+        if (tid < 2) found[tid] = 0;
+        __syncthreads();
+        for (int i = tid; i < a.T; i += kFewThreads) {
+            const int64_t r = token_at(a.tokens, a.token_bytes, i) - v0;
+            if (r >= 0 && r < n) atomicOr(&found[r >> 5], 1u << (r & 31));
+        }
+        __syncthreads();
+        const uint32_t lo = found[0], hi = found[1];
+        const int nv = a.D >> 3;
+        for (int r = warp; r < n; r += W) {
+            if ((r < 32 ? lo : hi) >> (r & 31) & 1) continue;
+            uint16_t* row = a.grad + (v0 + r) * a.D;
+            for (int c = lane; c < nv; c += 32) st16_stream(row + c * 8, make_uint4(0, 0, 0, 0));
+        }
+        return;
+    }
+
+    const int block = (int)blockIdx.x - a.fills;
+    const int groups = (a.slices + W - 1) / W, t = block / groups;
+    const int col = (block % groups * W + warp) * kColumns + lane * 8;
+    const int64_t v = token_at(a.tokens, a.token_bytes, t);
+    if (v < 0 || v >= a.V) {
+        if (v >= a.V && a.status && tid == 0) atomicOr(a.status, ZERO_DEV_BAD_TOKEN);
+        return;
+    }
+    uint32_t same = 0;                                       // bit q: id i0 + q is this one
+#pragma unroll
+    for (int q = 0; q < EACH; ++q)
+        if (i0 + q < a.T && token_at(a.tokens, a.token_bytes, i0 + q) == v) same |= 1u << q;
+    const uint32_t before = i0 >= t ? 0 : t - i0 >= EACH ? same : same & ((1u << (t - i0)) - 1);
+    if (__syncthreads_or(before != 0)) return;               // another block's
+    // the places of the id, in order
+    int at = __popc(same);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, at, o);
+        if (lane >= o) at += x;
+    }
+    if (lane == 31) found[warp] = at;
+    at -= __popc(same);
+    __syncthreads();
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        if (k < warp) at += found[k];
+        n += found[k];
+    }
+    for (uint32_t m = same; m; m &= m - 1) list[at++] = (uint16_t)(i0 + __ffs(m) - 1);
+    __syncthreads();
+
+    if (col - lane * 8 >= a.D) return;                       // a warp past the row's end
+    const bool on = col < a.D;
+    float acc[8] = {};
+    // (no load depends on a condition, so that all are asked for at once: the
+    // last row again past the list's end, the first columns past the row's)
+    const uint16_t* dy = a.dy + (on ? col : 0);
+    for (int b = 0; b < n; b += kFewBatch) {
+        uint4 x[kFewBatch];
+#pragma unroll
+        for (int q = 0; q < kFewBatch; ++q)
+            x[q] = ld16(dy + (int64_t)list[min(b + q, n - 1)] * a.dy_ld);
+#pragma unroll
+        for (int q = 0; q < kFewBatch; ++q)
+            if (b + q < n) add8(acc, x[q]);
+    }
+    if (on) {
+        uint16_t* p = a.grad + v * a.D + col;
+        float f[8] = {};
+        if (a.accumulate) bf_unpack8(ld16(p), f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] += acc[q] * a.scale;
+        st16(p, bf_pack8(f));
+    }
+}
+
 struct GradScratch {
     int64_t key0, key1, pos0, pos1, counts, long_runs, parts, bytes;
 };
 
 GradScratch grad_scratch(int64_t T, int32_t D)
 {
-    GradScratch s;
+    GradScratch s{};
+    if (T <= kFew) {
+        s.bytes = 256;
+        return s;
+    }
     const int64_t list = up(4 * T, 256);
     s.key0 = 0;
     s.key1 = list;
@@ -615,6 +729,15 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     sp.add(scratch, g.bytes, true);
     sp.add(dev_status, 4, true);
     LM_CHECK(sp.check());
+
+    if (T <= kFew) {
+        const int32_t fills = accumulate ? 0 : (int32_t)((V + kFillRows - 1) / kFillRows);
+        const FewArgs f{dy, tokens, grad, V, dy_ld, (int32_t)T, D, (int32_t)slices, token_bytes,
+                        accumulate, fills, scale, dev_status};
+        const int64_t groups = (slices + kFewThreads / 32 - 1) / (kFewThreads / 32);
+        return status_of(launch(k_embed_few, dim3((unsigned)(fills + T * groups)), kFewThreads, 0,
+                                st, f));
+    }
 
     uint8_t* base = static_cast<uint8_t*>(scratch);
     SortArgs s{};
