@@ -83,11 +83,12 @@ __global__ void __launch_bounds__(kLookupThreads) k_lookup(const __grid_constant
 
 // ================================================================== sort ==
 // A stable least-significant-digit radix sort of (token, position) by ONE
-// cluster of up to 8 blocks: a block owns a contiguous part of the list, the
-// blocks exchange digit counts and items through global memory (L2), and the
-// cluster barrier orders the passes, so the whole sort is one launch.  Ids
-// that take part in nothing (negative, or past the table) get the key V and
-// end up last.
+// cluster of up to 8 blocks: a block owns a contiguous part of the list, and the
+// cluster barrier orders the passes, so the whole sort is one launch.  Up to
+// 32768 tokens a block's part is one round, and the blocks read each other's
+// digit counts and pass items on in shared memory; above, through global memory
+// (L2).  Ids that take part in nothing (negative, or past the table) get the key
+// V and end up last.
 //
 // The rest of the grid, where there is one, fills the table's gradient with
 // zeros meanwhile; the rows that are met are written by the next launch.
@@ -98,7 +99,8 @@ constexpr int kSortItems = 4;                               // per thread and ro
 constexpr int kSortRound = kSortThreads * kSortItems;       // items of a block per round
 constexpr int kMaxCluster = 8;
 constexpr int kMaxBins = 512;
-constexpr int kSortSmem = kSortWarps * kMaxBins * 4;
+constexpr int kSortBins = kSortWarps * kMaxBins * 4;        // bytes: a warp's place in each digit
+constexpr int kSortSmem = kSortBins + 2 * 4 * kSortRound;   // and one round's ids and places
 
 struct SortArgs {
     const void* tokens;
@@ -108,7 +110,6 @@ struct SortArgs {
     uint32_t* key1;                  // passes the result is in the second
     uint32_t* pos0;
     uint32_t* pos1;
-    uint32_t* counts;                // [2][kMaxCluster][kMaxBins], by turns
     int32_t* long_runs;              // set to 0 for the next launch
     int32_t passes, bits;            // digits of `bits` bits
     int32_t cluster;
@@ -117,16 +118,39 @@ struct SortArgs {
     int32_t* status;
 };
 
+// This address in another block of the cluster.
+__device__ __forceinline__ uint32_t in_block(const void* p, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(r)
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void st_remote(uint32_t addr, uint32_t x)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_remote(uint32_t addr)
+{
+    uint32_t x;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(addr) : "memory");
+    return x;
+}
+
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::
                      : "memory");
 }
 
 __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ SortArgs a)
 {
     extern __shared__ uint32_t warp_bins[];                 // [kSortWarps][bins]
-    __shared__ uint32_t base[kMaxBins], total[kMaxBins], warp_total[kMaxBins / 32];
+    uint32_t* held_key = warp_bins + kSortBins / 4;         // one round: this block's part
+    uint32_t* held_pos = held_key + kSortRound;             // between two passes
+    __shared__ uint32_t base[kMaxBins], total[kMaxBins], counts[kMaxBins];
+    __shared__ uint32_t warp_total[kMaxBins / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if ((int)blockIdx.x >= a.cluster) {                     // whole clusters of fillers
@@ -142,11 +166,6 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
     const int64_t part = (a.T + a.cluster - 1) / a.cluster;
     const int64_t lo = min((int64_t)blockIdx.x * part, a.T), hi = min(lo + part, a.T);
     const bool one_round = part <= kSortRound;
-    // the lists that the first pass scatters into, met before they are written
-    for (int64_t i = lo + tid * 32; i < hi; i += kSortThreads * 32) {
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.key1 + i));
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.pos1 + i));
-    }
     uint32_t* mine = warp_bins + warp * bins;
     for (int pass = 0; pass < a.passes; ++pass) {
         const uint32_t* key_in = pass & 1 ? a.key1 : a.key0;
@@ -155,7 +174,12 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
         uint32_t* pos_out = pass & 1 ? a.pos0 : a.pos1;
         const int shift = pass * a.bits;
         auto load = [&](int64_t i, uint32_t& k, uint32_t& p) {
-            if (pass > 0) {                                 // written by the other blocks
+            if (pass > 0 && one_round) {                    // written by the other blocks
+                k = held_key[i - lo];
+                p = held_pos[i - lo];
+                return;
+            }
+            if (pass > 0) {
                 k = __ldcg(key_in + i);
                 p = __ldcg(pos_in + i);
                 return;
@@ -227,14 +251,13 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
         // digits of all blocks, then the same digit of the blocks before
         uint32_t before = 0, sum = 0;
         if (a.cluster > 1) {
-            uint32_t* counts = a.counts + (pass & 1) * kMaxCluster * kMaxBins;
-            if (tid < bins) __stcg(counts + blockIdx.x * kMaxBins + tid, total[tid]);
+            if (tid < bins) counts[tid] = total[tid];
             cluster_sync();
             if (tid < bins) {
                 uint32_t n[kMaxCluster];
 #pragma unroll
                 for (int q = 0; q < kMaxCluster; ++q)
-                    n[q] = q < a.cluster ? __ldcg(counts + q * kMaxBins + tid) : 0;
+                    n[q] = q < a.cluster ? ld_remote(in_block(&counts[tid], q)) : 0;
 #pragma unroll
                 for (int q = 0; q < kMaxCluster; ++q) {
                     sum += n[q];
@@ -244,6 +267,10 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
         } else if (tid < bins) {
             sum = total[tid];
         }
+        // the others have read this block's counts once all have arrived here:
+        // waited for at the end, before the block leaves or counts again
+        if (pass + 1 == a.passes)
+            asm volatile("barrier.cluster.arrive.release;" ::: "memory");
         if (tid < kMaxBins) {
             uint32_t incl = sum;
 #pragma unroll
@@ -269,8 +296,14 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
                 if (w0 + q * 32 < hi) {
                     const uint32_t d = (k[q] >> shift) & (bins - 1);
                     const uint32_t to = base[d] + mine[d] + rank[q];
-                    __stcg(key_out + to, k[q]);
-                    __stcg(pos_out + to, p[q]);
+                    if (one_round && pass + 1 < a.passes) {
+                        const uint32_t block = to / (uint32_t)part, at = to - block * (uint32_t)part;
+                        st_remote(in_block(held_key + at, block), k[q]);
+                        st_remote(in_block(held_pos + at, block), p[q]);
+                    } else {
+                        __stcg(key_out + to, k[q]);
+                        __stcg(pos_out + to, p[q]);
+                    }
                 }
             }
             if (!one_round) {
@@ -280,6 +313,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort(const __grid_constant__ S
             }
         }
         if (pass + 1 < a.passes) cluster_sync();
+        else asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     }
 }
 
@@ -636,7 +670,7 @@ __global__ void __launch_bounds__(kFewThreads) k_embed_few(const __grid_constant
 }
 
 struct GradScratch {
-    int64_t key0, key1, pos0, pos1, counts, long_runs, parts, bytes;
+    int64_t key0, key1, pos0, pos1, long_runs, parts, bytes;
 };
 
 GradScratch grad_scratch(int64_t T, int32_t D)
@@ -651,9 +685,8 @@ GradScratch grad_scratch(int64_t T, int32_t D)
     s.key1 = list;
     s.pos0 = 2 * list;
     s.pos1 = 3 * list;
-    s.counts = 4 * list;
     const int C = chunk_places(T, D);
-    s.long_runs = s.counts + 2 * 4 * kMaxCluster * kMaxBins;
+    s.long_runs = 4 * list;
     s.parts = s.long_runs + up(4 * (1 + (T + C - 1) / C), 256);
     s.bytes = s.parts + 8 * ((T + C - 1) / C) * (int64_t)D;
     return s;
@@ -756,7 +789,6 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     s.key1 = reinterpret_cast<uint32_t*>(base + g.key1);
     s.pos0 = reinterpret_cast<uint32_t*>(base + g.pos0);
     s.pos1 = reinterpret_cast<uint32_t*>(base + g.pos1);
-    s.counts = reinterpret_cast<uint32_t*>(base + g.counts);
     s.long_runs = reinterpret_cast<int32_t*>(base + g.long_runs);
     int key_bits = 1;                                      // keys run to V itself
     while (key_bits < 32 && (V >> key_bits) != 0) ++key_bits;
@@ -777,7 +809,7 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     cudaError_t e = allow_smem(reinterpret_cast<const void*>(&k_sort), kSortSmem, smem_set);
     if (e == cudaSuccess)
         e = launch_clusters(k_sort, dim3((unsigned)(s.cluster + fillers)), kSortThreads,
-                            kSortWarps * (4 << s.bits), s.cluster, st, s);
+                            kSortSmem, s.cluster, st, s);
     if (e != cudaSuccess) return status_of(e);
 
     GradArgs a{};

@@ -369,12 +369,33 @@ __device__ __forceinline__ Unit unit_at(const Product& p, int u)
 
 // ---------------------------------------------------------- the epilogues --
 
-// A row's target, or -1 where it takes part in nothing.
-__device__ __forceinline__ int64_t target_of(const MmaArgs& a, int64_t row)
+// What an epilogue needs to know of its row; asked for while the tile's
+// products still run (after them it is a good part of a short tile's time).
+struct Row {
+    int64_t y = -1;                    // the target, or -1 where the row takes part in nothing
+    float lse2 = 0.0f;                 // kP: lse in units of log 2
+    float g = 0.0f;                    // kP: dloss / u; kGrads: u
+};
+
+template <Kind K>
+__device__ __forceinline__ Row row_of(const MmaArgs& a, int64_t row, float unit)
 {
-    if (row >= a.x.rows) return -1;
-    const int64_t y = token_at(a.targets, a.token_bytes, row);
-    return y < a.V ? y : -1;
+    Row r;
+    if constexpr (K != kGrads) {
+        if (row >= a.x.rows) return r;
+        r.y = token_at(a.targets, a.token_bytes, row);
+        if (r.y >= a.V) r.y = -1;
+        if constexpr (K == kP) {
+            const float lse = a.lse[row], g = a.dloss[row];
+            if (r.y >= 0) {
+                r.lse2 = lse * kLog2e;
+                r.g = g / unit;
+            }
+        }
+    } else {
+        r.g = unit;
+    }
+    return r;
 }
 
 // The joint (maximum, sum) of two parts of a row; maxima in units of log 2.
@@ -392,12 +413,13 @@ __device__ __forceinline__ void join(float& m, float& s, float2 x)
 // tile's are free again once the first warp has given up the tile's sums, without
 // which the products two tiles on do not start.
 __device__ __forceinline__ bool epilogue_lse(const MmaArgs& a, const Unit& t, uint32_t tmem,
-                                             int64_t row, int half, float2* share, uint32_t ready,
-                                             uint32_t parity, volatile int* dead)
+                                             int64_t row, const Row& info, int half,
+                                             float2* share, uint32_t ready, uint32_t parity,
+                                             volatile int* dead)
 {
     const int64_t c0 = (int64_t)t.n * a.x.bn;
     const int live = (int)min((int64_t)a.x.bn, a.V - c0);
-    const int64_t y = target_of(a, row) - c0;                // of the tile, if in it
+    const int64_t y = info.y - c0;                           // of the tile, if in it
     float top = -INFINITY, sum = 0.0f;
 #pragma unroll 1
     for (int c = half * 128; c < half * 128 + 128; c += 32) {
@@ -478,24 +500,14 @@ __device__ __forceinline__ void write_rows(uint32_t buf, int lane, Store&& store
 // columns at a time through the warp's buffer, 128 columns a warp.
 template <bool P>
 __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Product& p, const Unit& t,
-                                              uint32_t tmem, int64_t row0, int lane, int half,
-                                              uint32_t to)
+                                              uint32_t tmem, int64_t row0, const Row& info,
+                                              int lane, int half, uint32_t to)
 {
     const int64_t c0 = (int64_t)t.n * p.bn;
     if (row0 >= p.rows) return;
-    const int64_t row = row0 + lane;
-    int64_t y = -1;
-    float lse2 = 0.0f, g = 0.0f;
-    bool live = true;
-    if constexpr (P) {
-        y = target_of(a, row);
-        live = y >= 0;
-        lse2 = live ? a.lse[row] * kLog2e : 0.0f;
-        g = live ? a.dloss[row] / *a.unit : 0.0f;
-        y -= a.v0 + c0;
-    } else {
-        g = *a.unit;
-    }
+    const bool live = !P || info.y >= 0;
+    const float lse2 = info.lse2, g = info.g;
+    const int64_t y = info.y - (a.v0 + c0);
 #pragma unroll 1
     for (int c = half * 128; c < min(p.bn, half * 128 + 128); c += 64) {
         if (c0 + c >= p.cols) break;
@@ -735,25 +747,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_mma(const __grid_constant__ Mma
         const int half = (warp - 4) >> 2;                // and half of the columns
         const uint32_t buf = staging + (warp - 4) * kWarpStage;
         float2* share = reinterpret_cast<float2*>(raw + (staging - smem_u32(raw))) + q * 32 + lane;
+        const float unit = K == kLse ? 1.0f : *a.unit;
         for (int i = 0, u; (u = unit_of(a, pair, pairs, i)) >= 0; ++i) {
             const bool first = K != kGrads || u < a.x_units;
             const Product& p = first ? a.x : a.y;
             const Unit t = unit_at(p, first ? u : u - a.x_units);
             const int b = i & 1;
+            const int64_t row0 = (int64_t)t.m * BM + rank * 128 + q * 32;
+            const Row info = row_of<K>(a, row0 + lane, unit);
             if (!warp_wait(sums_full + 8 * b, (i >> 1) & 1, a.wait_limit, dead)) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t from = tmem + b * BN + ((uint32_t)(q * 32) << 16);
-            const int64_t row0 = (int64_t)t.m * BM + rank * 128 + q * 32;
             if constexpr (K == kLse) {
-                if (!epilogue_lse(a, t, from, row0 + lane, half, share + b * 128,
+                if (!epilogue_lse(a, t, from, row0 + lane, info, half, share + b * 128,
                                   shared_full + 8 * (4 * b + q), (i >> 1) & 1, dead))
                     break;
             } else if constexpr (K == kP) {
-                epilogue_bf16<true>(a, p, t, from, row0, lane, half, buf);
+                epilogue_bf16<true>(a, p, t, from, row0, info, lane, half, buf);
             } else if (first) {
                 epilogue_f32(a, t, from, row0, lane, half, buf);
             } else {
-                epilogue_bf16<false>(a, p, t, from, row0, lane, half, buf);
+                epilogue_bf16<false>(a, p, t, from, row0, info, lane, half, buf);
             }
             asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
             __syncwarp();
@@ -872,24 +886,42 @@ struct FinishArgs {
     int32_t D, splits;
 };
 
+// G threads share a vector of 8 columns (many splits: few tokens), each with every
+// G-th split; their sums are added in order.
+template <int G>
 __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishArgs a)
 {
     pdl_enter();
-    const int nv = a.D >> 3;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    constexpr int VECS = 256 / G;
+    __shared__ float share[G > 1 ? G : 1][8][G > 1 ? VECS : 1];
+    const int nv = a.D >> 3, lane = threadIdx.x % VECS, group = threadIdx.x / VECS;
+    const int64_t i = (int64_t)blockIdx.x * VECS + lane;
     const int64_t t = i / nv;
-    if (t >= a.T) return;
     const int c = (int)(i - t * nv) * 8;
+    const bool in = t < a.T;
     const float unit = *a.unit;
     float f[8] = {};
+    if (in) {
 #pragma unroll 4
-    for (int s = 0; s < a.splits; ++s) {
-        const float* p = a.sums + (s * a.split_rows + t) * a.D + c;
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
-        const float4 y = __ldcs(reinterpret_cast<const float4*>(p + 4));
-        f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
-        f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+        for (int s = group; s < a.splits; s += G) {
+            const float* p = a.sums + (s * a.split_rows + t) * a.D + c;
+            const float4 x = __ldcs(reinterpret_cast<const float4*>(p));
+            const float4 y = __ldcs(reinterpret_cast<const float4*>(p + 4));
+            f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+            f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+        }
     }
+    if constexpr (G > 1) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) share[group][q][lane] = f[q];
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int k = 1; k < G; ++k)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) f[q] += share[k][q][lane];
+    }
+    if (!in) return;
 #pragma unroll
     for (int q = 0; q < 8; ++q) f[q] *= unit;
     st16_stream(a.dh + t * a.dh_ld + c, bf_pack8(f));
@@ -1229,7 +1261,11 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
     }
     if (e == cudaSuccess) {
         const FinishArgs f{sums, unit, dh, T, g.split_rows, dh_ld, D, g.splits};
-        e = launch(k_finish, dim3((unsigned)((T * (D / 8) + 255) / 256)), 256, 0, st, f);
+        const int64_t vecs = T * (D / 8);
+        if (g.splits >= 8)
+            e = launch(k_finish<8>, dim3((unsigned)((vecs + 31) / 32)), 256, 0, st, f);
+        else
+            e = launch(k_finish<1>, dim3((unsigned)((vecs + 255) / 256)), 256, 0, st, f);
     }
     return status_of(e);
 }
