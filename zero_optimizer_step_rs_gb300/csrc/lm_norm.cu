@@ -16,10 +16,9 @@
 // from it is made in registers.  All of it is bound by HBM traffic: forward
 // 2+2 bytes an element read and 2+2+1 written, replay 1 and 2, gradient 2+2+1
 // and 2.  Measured, one GB300, 32768 x 2048: forward and replay together 119.7 us
-// (6.77 TB/s, the rate of a copy), gradient 89 us (5.3 TB/s: 73 us for the rows,
-// whose 25 instructions an element fill 63 % of the issue slots, and 6 us for
-// the join of dw).  333 x 768: 5.2 us for forward and replay, 6.2 us for the
-// gradient, bound by their two launches each.
+// (6.77 TB/s, the rate of a copy), gradient 77 us (6.1 TB/s; the rows' 25
+// instructions an element fill 63 % of the issue slots).  333 x 768: 5.1 us for
+// forward and replay, 5.7 us for the gradient, bound by their two launches each.
 #include "lm_common.cuh"
 
 namespace {

@@ -65,7 +65,7 @@ constexpr int kEpilogueWarps = 8;                  // two for each quarter of th
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kStageBytes = 2 * 128 * BK * 2;      // per CTA: 128 rows of each operand
 constexpr int kPieceAlign = 256;
-constexpr uint64_t kWaitLimit = 1000000000;        // ns that a wait may take
+constexpr uint64_t kWaitLimit = 2000000000;        // ns that a wait may take
 constexpr uint64_t kDrainLimit = 200000000;
 constexpr int kWarpStage = 4096;                   // an epilogue warp's output buffer
 constexpr int kStaging = kEpilogueWarps * kWarpStage;
