@@ -12,7 +12,7 @@
 // Measured, one GB300: the lookup of 65536 x 2048 from 128256 rows 54.7 us (6.4 TB/s
 // of the bytes above; the copy rate is 6.77); the gradient of 1000 x 2048 into
 // 128256 rows 75.7 us (7.0 TB/s, mostly zeros written), of 32768 x 2048 added to a
-// tied table 73 us for 230 MB (34 us at the copy rate): 20 us of that are the sort,
+// tied table 72 us for 230 MB (34 us at the copy rate): 18 us of that are the sort,
 // in which 8 SMs wait on latencies one after another, 37 the sums (bound by the
 // instructions around each row's 512 bytes a warp, and by latency), 10 the join.
 //
@@ -338,7 +338,8 @@ struct GradArgs {
     const uint32_t* pos;
     uint16_t* grad;
     float* parts;                            // [2 * chunks][D]: a chunk's head and tail
-    int32_t* long_runs;                      // their number, and then the chunks they start in
+    int32_t* long_runs;                      // their number; from the third word on, the
+                                             // chunk each starts in and its key
     int64_t T, V, dy_ld;
     int32_t D, slices, chunks, accumulate;
     float scale;
@@ -411,8 +412,10 @@ __global__ void __launch_bounds__(kGradThreads) k_embed_grad(const __grid_consta
     const ChunkRuns r = chunk_runs<C>(a.key, a.T, a.V, c, lane);
     if (r.n == 0) return;
     // (in any order: each run is joined by itself)
+    const uint32_t last = __shfl_sync(ALL, r.cur, C - 1);
     if (r.tail_long && w % a.slices == 0 && lane == 0)
-        a.long_runs[1 + atomicAdd(a.long_runs, 1)] = (int32_t)c;
+        reinterpret_cast<uint2*>(a.long_runs)[1 + atomicAdd(a.long_runs, 1)] =
+            make_uint2((uint32_t)c, last);
 
     // places [from, to) of the chunk and the C after it, a batch of rows at a
     // time, all asked for before the first is added; what the gradient holds
@@ -489,9 +492,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_embed_join(const __grid_consta
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t items = (int64_t)a.long_runs[0] * a.slices;
     for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
-        const int64_t c = a.long_runs[1 + item / a.slices];
+        const uint2 run = reinterpret_cast<const uint2*>(a.long_runs)[1 + item / a.slices];
+        const int64_t c = run.x;
         const int col = (int)(item % a.slices) * kColumns + lane * 8;
-        const uint32_t v = a.key[c * C + C - 1];
+        const uint32_t v = run.y;
         // the first place past the run, by 32 probes at a time
         int64_t lo = (c + 1) * C, hi = a.T;
         for (int64_t near = 32; lo < hi; near = hi) {          // most are found near the start
@@ -687,7 +691,7 @@ GradScratch grad_scratch(int64_t T, int32_t D)
     s.pos1 = 3 * list;
     const int C = chunk_places(T, D);
     s.long_runs = 4 * list;
-    s.parts = s.long_runs + up(4 * (1 + (T + C - 1) / C), 256);
+    s.parts = s.long_runs + up(8 * (1 + (T + C - 1) / C), 256);
     s.bytes = s.parts + 8 * ((T + C - 1) / C) * (int64_t)D;
     return s;
 }

@@ -805,9 +805,14 @@ __global__ void __launch_bounds__(1024) k_xent_join(const __grid_constant__ Join
     __shared__ float2 all[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t row = (int64_t)blockIdx.x * 32 + lane;
+    // what the end needs, asked for first
+    const int64_t r = (int64_t)blockIdx.x * 32 + warp;
+    const bool last = lane == 0 && r < a.T;
+    const int64_t y = last ? token_at(a.targets, a.token_bytes, r) : -1;
+    const float at_target = last ? a.at_target[r] : 0.0f;      // meaningless without a target
     float m = -INFINITY, s = 0.0f;
     if (row < a.T) {
-#pragma unroll 4
+#pragma unroll 8
         for (int n = warp; n < a.n_tiles; n += 32) join(m, s, a.part[n * a.part_ld + row]);
     }
     all[lane][warp] = make_float2(m, s);
@@ -817,17 +822,15 @@ __global__ void __launch_bounds__(1024) k_xent_join(const __grid_constant__ Join
     s = x.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-        const float2 y = make_float2(__shfl_down_sync(0xFFFFFFFFu, m, o),
+        const float2 z = make_float2(__shfl_down_sync(0xFFFFFFFFu, m, o),
                                      __shfl_down_sync(0xFFFFFFFFu, s, o));
-        join(m, s, y);
+        join(m, s, z);
     }
-    const int64_t r = (int64_t)blockIdx.x * 32 + warp;
-    if (lane == 0 && r < a.T) {
+    if (last) {
         const float lse = m * kLn2 + logf(s);
         a.lse[r] = lse;
-        const int64_t y = token_at(a.targets, a.token_bytes, r);
         if (y >= a.V && a.status) atomicOr(a.status, ZERO_DEV_BAD_TOKEN);
-        a.loss[r] = y >= 0 && y < a.V ? lse - a.at_target[r] : 0.0f;
+        a.loss[r] = y >= 0 && y < a.V ? lse - at_target : 0.0f;
     }
 }
 
