@@ -614,6 +614,7 @@ zero_status zero_ckpt_load(const zero_plan_t* plan, const char* dir, uint16_t* c
  *   - T = 0 is allowed: outputs with one row per token are not touched, and
  *     the gradients of tables and weights become zero (or keep what they hold,
  *     with accumulate).
+ *   - loss, lse and dloss need 4-byte alignment only.
  *   - scratch: scratch_bytes of device memory, at least what the matching
  *     *_scratch_bytes call returns (-1 for sizes it does not take), 16-byte
  *     aligned, not shared by calls that may overlap in time.  Its contents

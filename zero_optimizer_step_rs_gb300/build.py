@@ -12,6 +12,7 @@ called) on a machine without a GPU.
 """
 from __future__ import annotations
 
+import fcntl
 import importlib.util
 import os
 import subprocess
@@ -74,6 +75,14 @@ def ext_command():
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not _stale():
         return LIB
+    # several processes may find it stale at once: one builds, the others wait
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(os.path.join(BUILD_DIR, ".lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)
+        return _build(verbose) if force or _stale() else LIB
+
+
+def _build(verbose: bool) -> str:
     cmds, link = compile_commands()
     cmds.append(ext_command())
     procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
