@@ -5,19 +5,25 @@
 //   l = h E^T (bf16 products, fp32 sums), lse_t = log sum_v exp(l_tv),
 //   loss_t = lse_t - l_{t, y_t}                       (0 for an ignored token)
 //   P_tv = (exp(l_tv - lse_t) - [v = y_t]) * dloss_t / u   (0 in an ignored row)
-//   dh = u P E,  dE = u P^T h,  u = max_t |dloss_t|
+//   dh = u (P E + e_t E_y),  dE = u P^T h,  u = max_t |dloss_t|
+// with e_t what the rounding of P_ty to bf16 lost.
 //
 // Forward is one matrix product whose epilogue keeps, per row and tile of up to
 // 256 vocabulary rows, a maximum and the sum of exponentials relative to it; a
 // small second kernel joins the tiles.  Backward keeps nothing but lse: for a
 // piece of the vocabulary at a time it makes the logits again, turns them into P
 // in bf16 (an operand of the tensor cores, and the one rounding before the
-// sums), and multiplies P with both operands.  Where all tokens weigh the same,
-// as in a mean, dloss / u is exactly 1, and a row's large entry exp - 1, near -1,
-// loses next to nothing in bf16; with dloss itself in P its rounding would be the
-// whole row's error (0.0026 of the result instead of 0.0018).  The gradient of
-// the table's piece is final and written once; dh is summed over the pieces in
-// fp32 and rounded once at the end.
+// sums), and multiplies P with both operands.  A row's entry at the target,
+// exp - 1, outweighs all others together, so its rounding would be the error of the
+// row of dh (0.0023 of it, where rounding the result takes 0.0017): what it lost is
+// kept as one fp32 number a token, and its product with the target's row of the
+// table is added in fp32 before dh is rounded.  The gradient of the table has P's
+// rounding: a token's terms go to as many rows as the vocabulary has, so adding
+// the lost parts there would take the tokens sorted by target.  Where all tokens
+// weigh the same, as in a mean, dloss / u is exactly 1 and the entry near -1 loses
+// next to nothing (0.0017); with other weights it is off by 0.0022 to 0.0024, two
+// roundings.  The gradient of the table's piece is final and written once; dh is
+// summed over the pieces in fp32 and rounded once at the end.
 //
 // Floor: 2*T*D*V operations forward, 6*T*D*V backward (the logits are needed
 // again), on the tensor cores; with few tokens the table's 2*V*D bytes.
@@ -117,6 +123,7 @@ struct MmaArgs {
     const float* lse;
     const float* dloss;
     const float* unit;                 // u
+    float* lost;                       // kP: e_t, of the rows whose target is in the piece
     float2* part;                      // kLse: [n_tiles][part_ld] (maximum, sum)
     int64_t part_ld;
     float* at_target;                  // kLse: the target's logit
@@ -523,9 +530,15 @@ __device__ __forceinline__ void epilogue_bf16(const MmaArgs& a, const Product& p
                     x[i] = live ? exp2_fast(fmaf(x[i], kLog2e, -lse2)) : 0.0f;
                 }
                 if (here) {
+                    float v = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if (i == at) x[i] -= 1.0f;
+                        if (i == at) {
+                            x[i] -= 1.0f;
+                            v = x[i] * g;
+                        }
+                    const float e = v - bf_lo(bf_pack(v, 0.0f));
+                    a.lost[row0 + lane] = fabsf(e) < INFINITY ? e : 0.0f;
                 }
                 __syncwarp();
             }
@@ -880,13 +893,16 @@ __global__ void __launch_bounds__(256) k_clean(const __grid_constant__ CleanArgs
         st16(a.out + t * a.D + c * 8, live ? ld16(a.h + t * a.h_ld + c * 8) : make_uint4(0, 0, 0, 0));
 }
 
-// dh from its splits' sums, added in order.
+// dh from its splits' sums, added in order, and what the target's entry lost.
 struct FinishArgs {
     const float* sums;
     const float* unit;
+    const float* lost;
+    const uint16_t* table;
+    const void* targets;
     uint16_t* dh;
-    int64_t T, split_rows, dh_ld;
-    int32_t D, splits;
+    int64_t T, V, split_rows, dh_ld;
+    int32_t D, splits, token_bytes;
 };
 
 // G threads share a vector of 8 columns (many splits: few tokens), each with every
@@ -904,6 +920,10 @@ __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishAr
     const bool in = t < a.T;
     const float unit = *a.unit;
     float f[8] = {};
+    const int64_t y = in && group == 0 ? token_at(a.targets, a.token_bytes, t) : -1;
+    const bool live = y >= 0 && y < a.V;
+    const float lost = live ? a.lost[t] : 0.0f;
+    const uint4 row = live ? ld16(a.table + y * a.D + c) : make_uint4(0, 0, 0, 0);
     if (in) {
 #pragma unroll 4
         for (int s = group; s < a.splits; s += G) {
@@ -925,6 +945,12 @@ __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishAr
             for (int q = 0; q < 8; ++q) f[q] += share[k][q][lane];
     }
     if (!in) return;
+    if (lost != 0.0f) {
+        float e[8];
+        bf_unpack8(row, e);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) f[q] = fmaf(lost, e[q], f[q]);
+    }
 #pragma unroll
     for (int q = 0; q < 8; ++q) f[q] *= unit;
     st16_stream(a.dh + t * a.dh_ld + c, bf_pack8(f));
@@ -1043,7 +1069,7 @@ LossScratch loss_scratch(int64_t T, int64_t V)
 
 // The backward pass's plan: the piece, the splits of dh's sum, the scratch.
 struct GradPlan {
-    int64_t piece, p, clean, sums, unit, split_rows, bytes;
+    int64_t piece, p, clean, sums, lost, unit, split_rows, bytes;
     int32_t splits;
 };
 
@@ -1067,7 +1093,8 @@ GradPlan grad_plan(int64_t T, int64_t V, int32_t D, int64_t piece)
     g.clean = up(2 * T * g.piece, 256);
     g.sums = g.clean + up(2 * T * D, 256);
     g.split_rows = T;
-    g.unit = g.sums + up(4 * g.split_rows * D * g.splits, 256);
+    g.lost = g.sums + up(4 * g.split_rows * D * g.splits, 256);
+    g.unit = g.lost + up(4 * T, 256);
     g.bytes = g.unit + 256;
     return g;
 }
@@ -1199,6 +1226,7 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
     float* sums = reinterpret_cast<float*>(base + g.sums);
     const unsigned row_blocks = (unsigned)((T + 7) / 8);
     float* unit = reinterpret_cast<float*>(base + g.unit);
+    float* lost = reinterpret_cast<float*>(base + g.lost);
     const CleanArgs ca{h, clean, dloss, unit, targets, T, V, h_ld, D, target_bytes, dev_status};
     cudaError_t e = launch(k_clean, dim3(row_blocks), 256, 0, st, ca);
 
@@ -1209,6 +1237,7 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
     common.lse = lse;
     common.dloss = dloss;
     common.unit = unit;
+    common.lost = lost;
     common.status = dev_status;
     common.wait_limit = flags & ZERO_FLAG_DEBUG_EXPIRE_WAITS ? 0 : kWaitLimit;
     for (int64_t v0 = 0; v0 < V && e == cudaSuccess; v0 += g.piece) {
@@ -1263,7 +1292,8 @@ extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uin
         e = run_mma<kGrads>(second, st);
     }
     if (e == cudaSuccess) {
-        const FinishArgs f{sums, unit, dh, T, g.split_rows, dh_ld, D, g.splits};
+        const FinishArgs f{sums, unit,         lost,  table, targets,  dh,          T,
+                           V,    g.split_rows, dh_ld, D,     g.splits, target_bytes};
         const int64_t vecs = T * (D / 8);
         if (g.splits >= 8)
             e = launch(k_finish<8>, dim3((unsigned)((vecs + 31) / 32)), 256, 0, st, f);
