@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import lm_ref as R
-from tests.test_gpu_lm_xent import backward
+from tests.test_gpu_lm_xent import backward, forward
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +32,25 @@ def test_gradients_lose_no_more_than_their_own_rounding(T, V, D, weights):
         return ((x.to(torch.bfloat16).to(R.F) - x).norm() / x.norm()).item()
     R.norm_close(dh, want_h, 1.1 * rounding(want_h), "dh")
     R.norm_close(dt, want_t, 1.1 * 2 ** 0.5 * rounding(want_t), "dtable")
+
+
+@pytest.mark.parametrize("T,V", [(64, 200), (300, 5003)])
+def test_a_small_loss_at_large_logits(T, V):
+    """Whole numbers, so that every logit is exact, of magnitude 300 and more; the
+    target is the largest logit or one of the next.  The loss then has the errors
+    of the exponentials (2^-22 each), of their sums and joins and of one
+    logarithm: below 2^-19 together, and two roundings of itself; none of the
+    logits' own magnitude."""
+    g = R.gen(V)
+    h = torch.randint(-8, 9, (T, 64), generator=g, device="cuda").to(torch.bfloat16)
+    table = torch.randint(-8, 9, (V, 64), generator=g, device="cuda").to(torch.bfloat16)
+    logits = h.to(R.F) @ table.to(R.F).T
+    top = logits.topk(3, 1)
+    assert float(top.values[:, 0].median()) > 300
+    t = top.indices.gather(1, (torch.arange(T, device="cuda") % 3)[:, None])[:, 0]
+    loss, lse = forward(h, table, t)
+    want_lse = torch.logsumexp(logits, 1)
+    want = want_lse - logits.gather(1, t[:, None])[:, 0]
+    assert int((want < 1).sum()) > T // 4
+    R.within(loss, want, 2.0 ** -19 + 2 * R.U32 * want, "loss")
+    R.within(lse, want_lse, 2.0 ** -19 + 2 * R.U32 * want_lse.abs(), "lse")

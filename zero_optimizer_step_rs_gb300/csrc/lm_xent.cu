@@ -64,7 +64,10 @@ namespace {
 using namespace lm;
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+// 1 / kLog2e (the fp32 number, not log2 e), in two parts: maxima are kept as x * kLog2e,
+// and the fp32 constant alone would be off by 1e-5 at logits of some hundreds
+constexpr float kUnLog2e = (float)(1.0 / (double)kLog2e);
+constexpr float kUnLog2eRest = (float)(1.0 / (double)kLog2e - (double)kUnLog2e);
 
 constexpr int BM = 256, BN = 256, BK = 64;         // a CTA pair's largest tile, a stage's depth
 constexpr int kEpilogueWarps = 8;                  // two for each quarter of the tensor memory
@@ -840,10 +843,13 @@ __global__ void __launch_bounds__(1024) k_xent_join(const __grid_constant__ Join
         join(m, s, z);
     }
     if (last) {
-        const float lse = m * kLn2 + logf(s);
-        a.lse[r] = lse;
+        // log s plus the distance from the target's logit to the maximum: the
+        // difference of lse and the logit would carry lse's rounding (3e-5 at 500)
+        const float log_s = logf(s);
+        const float rest = fabsf(m) < INFINITY ? fmaf(m, kUnLog2eRest, log_s) : log_s;
+        a.lse[r] = fmaf(m, kUnLog2e, rest);
         if (y >= a.V && a.status) atomicOr(a.status, ZERO_DEV_BAD_TOKEN);
-        a.loss[r] = y >= 0 && y < a.V ? lse - at_target : 0.0f;
+        a.loss[r] = y >= 0 && y < a.V ? fmaf(m, kUnLog2e, -at_target) + rest : 0.0f;
     }
 }
 
