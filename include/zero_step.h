@@ -708,7 +708,8 @@ int64_t zero_xent_grad_scratch_bytes(int64_t T, int64_t V, int32_t D, int64_t pi
  * P = bf16((exp(logit - lse) - [v == target]) * dloss / u),
  * zero in the rows of no token whatever h and dloss hold there,
  *   dh = bf16(u (P table + e table[target])),  dtable = bf16(u P^T h)   (every row written)
- * where e[t], kept in fp32, is what the rounding of P[t, target] lost.
+ * where e[t], kept in fp32, is what the rounding of P[t, target] lost; rows of dh
+ * of no token are zeros whatever the table holds.
  * The vocabulary is taken `piece` rows at a time (a multiple of 256; 0: chosen
  * so that P takes at most 512 MiB); a larger piece needs more scratch.
  */

@@ -54,3 +54,18 @@ def test_a_small_loss_at_large_logits(T, V):
     assert int((want < 1).sum()) > T // 4
     R.within(loss, want, 2.0 ** -19 + 2 * R.U32 * want, "loss")
     R.within(lse, want_lse, 2.0 ** -19 + 2 * R.U32 * want_lse.abs(), "lse")
+
+
+@pytest.mark.parametrize("T", [17, 300])
+def test_ignored_rows_have_no_gradient_beside_a_table_that_is_not_finite(T):
+    g = R.gen(T)
+    h, table = R.bf16(g, (T, 64)), R.bf16(g, (1000, 64), 0.1)
+    t = torch.randint(0, 1000, (T,), generator=g, device="cuda")
+    t[::4] = -1
+    t[1] = 1000                                          # past the table: no token either
+    table[7, 3], table[500] = float("inf"), float("nan")
+    _, lse = forward(h, table, t)
+    dh, _ = backward(h, table, t, lse, torch.ones(T, device="cuda"))
+    gone = (t < 0) | (t >= 1000)
+    assert not dh[gone].any()                            # a NaN would count as true
+    assert bool(torch.isnan(dh[~gone]).all())

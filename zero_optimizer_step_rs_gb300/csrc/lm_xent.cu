@@ -900,6 +900,8 @@ __global__ void __launch_bounds__(256) k_clean(const __grid_constant__ CleanArgs
 }
 
 // dh from its splits' sums, added in order, and what the target's entry lost.
+// Rows of no token are zeros whatever the sums hold: their P is zero, but zero
+// times an Inf or a NaN of the table is not.
 struct FinishArgs {
     const float* sums;
     const float* unit;
@@ -926,10 +928,10 @@ __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishAr
     const bool in = t < a.T;
     const float unit = *a.unit;
     float f[8] = {};
-    const int64_t y = in && group == 0 ? token_at(a.targets, a.token_bytes, t) : -1;
-    const bool live = y >= 0 && y < a.V;
+    const int64_t target = in && group == 0 ? token_at(a.targets, a.token_bytes, t) : -1;
+    const bool live = target >= 0 && target < a.V;
     const float lost = live ? a.lost[t] : 0.0f;
-    const uint4 row = live ? ld16(a.table + y * a.D + c) : make_uint4(0, 0, 0, 0);
+    const uint4 row = live ? ld16(a.table + target * a.D + c) : make_uint4(0, 0, 0, 0);
     if (in) {
 #pragma unroll 4
         for (int s = group; s < a.splits; s += G) {
@@ -958,7 +960,7 @@ __global__ void __launch_bounds__(256) k_finish(const __grid_constant__ FinishAr
         for (int q = 0; q < 8; ++q) f[q] = fmaf(lost, e[q], f[q]);
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) f[q] *= unit;
+    for (int q = 0; q < 8; ++q) f[q] = live ? f[q] * unit : 0.0f;
     st16_stream(a.dh + t * a.dh_ld + c, bf_pack8(f));
 }
 
