@@ -12,11 +12,15 @@
 // one place that finds and loads the library.  Every function takes its arguments
 // by position, None for those left out, and returns the status code; a tensor of
 // the wrong type raises TypeError, of the wrong shape, stride or device
-// ValueError.
+// ValueError.  All of a call's tensors lie on one device, which is the current
+// one while the entry point runs: a kernel is launched on the current device, and
+// every device's default stream has the same null handle.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -51,7 +55,38 @@ const at::Tensor& tensor(PyObject* o, const char* name)
     return THPVariable_Unpack(o);
 }
 
-const at::Tensor& typed(PyObject* o, at::ScalarType type, const char* name)
+// The device that a call's tensors lie on: the first one's, which is made the
+// current one until the call ends, and which the others are held to.
+class Call {
+public:
+    void on_device(const at::Tensor& t, const char* name)
+    {
+        if (!t.is_cuda()) {
+            PyErr_Format(PyExc_ValueError, "%s: must be a CUDA tensor", name);
+            raise_set();
+        }
+        const c10::DeviceIndex d = t.get_device();
+        if (d == device_) return;
+        if (device_ >= 0) {
+            PyErr_Format(PyExc_ValueError, "%s: tensors on different devices, cuda:%d and cuda:%d",
+                         name, (int)device_, (int)d);
+            raise_set();
+        }
+        device_ = d;
+    }
+    // Once every tensor has been seen.
+    void make_current()
+    {
+        if (device_ != c10::cuda::current_device()) guard_.set_index(device_);
+    }
+    c10::DeviceIndex device() const { return device_; }
+
+private:
+    c10::DeviceIndex device_ = -1;
+    c10::cuda::OptionalCUDAGuard guard_;
+};
+
+const at::Tensor& typed(Call& c, PyObject* o, at::ScalarType type, const char* name)
 {
     const at::Tensor& t = tensor(o, name);
     if (t.scalar_type() != type) {
@@ -63,10 +98,7 @@ const at::Tensor& typed(PyObject* o, at::ScalarType type, const char* name)
                      c10::toString(t.scalar_type()));
         raise_set();
     }
-    if (!t.is_cuda()) {
-        PyErr_Format(PyExc_ValueError, "%s: must be a CUDA tensor", name);
-        raise_set();
-    }
+    c.on_device(t, name);
     return t;
 }
 
@@ -83,9 +115,9 @@ struct Rows {
     int64_t ld = 0;
 };
 
-Rows rows(PyObject* o, int64_t T, int64_t D, const char* name)
+Rows rows(Call& c, PyObject* o, int64_t T, int64_t D, const char* name)
 {
-    const at::Tensor& t = typed(o, at::kBFloat16, name);
+    const at::Tensor& t = typed(c, o, at::kBFloat16, name);
     if (t.dim() != 2 || t.size(0) != T || t.size(1) != D) wrong_shape(name, T, D);
     if (t.stride(1) != 1 && D > 1) {
         PyErr_Format(PyExc_ValueError, "%s: columns must be contiguous", name);
@@ -94,16 +126,16 @@ Rows rows(PyObject* o, int64_t T, int64_t D, const char* name)
     return {static_cast<uint16_t*>(t.data_ptr()), T > 1 ? t.stride(0) : D};
 }
 
-Rows rows_or_none(PyObject* o, int64_t T, int64_t D, const char* name)
+Rows rows_or_none(Call& c, PyObject* o, int64_t T, int64_t D, const char* name)
 {
-    return o == Py_None ? Rows{} : rows(o, T, D, name);
+    return o == Py_None ? Rows{} : rows(c, o, T, D, name);
 }
 
 // A contiguous tensor of that shape: a matrix, or a vector (b < 0).
 template <typename E>
-E* dense(PyObject* o, at::ScalarType type, int64_t a, int64_t b, const char* name)
+E* dense(Call& c, PyObject* o, at::ScalarType type, int64_t a, int64_t b, const char* name)
 {
-    const at::Tensor& t = typed(o, type, name);
+    const at::Tensor& t = typed(c, o, type, name);
     const bool fits = b < 0 ? t.dim() == 1 && t.size(0) == a
                             : t.dim() == 2 && t.size(0) == a && t.size(1) == b;
     if (!fits) wrong_shape(name, a, b);
@@ -133,7 +165,7 @@ struct Ids {
     int64_t n;
 };
 
-Ids ids(PyObject* o, const char* name)
+Ids ids(Call& c, PyObject* o, const char* name)
 {
     const at::Tensor& t = tensor(o, name);
     const bool wide = t.scalar_type() == at::kLong;
@@ -142,10 +174,7 @@ Ids ids(PyObject* o, const char* name)
                      c10::toString(t.scalar_type()));
         raise_set();
     }
-    if (!t.is_cuda()) {
-        PyErr_Format(PyExc_ValueError, "%s: must be a CUDA tensor", name);
-        raise_set();
-    }
+    c.on_device(t, name);
     if (t.dim() != 1 || !t.is_contiguous()) {
         PyErr_Format(PyExc_ValueError, "%s: expected a contiguous vector", name);
         raise_set();
@@ -158,20 +187,21 @@ struct Scratch {
     int64_t bytes;
 };
 
-Scratch scratch(PyObject* o)
+Scratch scratch(Call& c, PyObject* o)
 {
     const at::Tensor& t = tensor(o, "scratch");
-    if (!t.is_cuda() || !t.is_contiguous()) {
-        PyErr_SetString(PyExc_ValueError, "scratch: must be a contiguous CUDA tensor");
+    c.on_device(t, "scratch");
+    if (!t.is_contiguous()) {
+        PyErr_SetString(PyExc_ValueError, "scratch: must be contiguous");
         raise_set();
     }
     return {t.data_ptr(), (int64_t)t.nbytes()};
 }
 
-int32_t* status(PyObject* o)
+int32_t* status(Call& c, PyObject* o)
 {
     if (o == Py_None) return nullptr;
-    const at::Tensor& t = typed(o, at::kInt, "dev_status");
+    const at::Tensor& t = typed(c, o, at::kInt, "dev_status");
     if (t.numel() < 1) {
         PyErr_SetString(PyExc_ValueError, "dev_status: need 1 element");
         raise_set();
@@ -179,11 +209,12 @@ int32_t* status(PyObject* o)
     return static_cast<int32_t*>(t.data_ptr());
 }
 
-// None: the current stream of the device of `of`; else the stream's address.
-void* stream(PyObject* o, PyObject* of)
+// The last of a call's arguments.  None: the current stream of the tensors' device;
+// else the stream's address.
+void* stream(Call& c, PyObject* o)
 {
-    if (o == Py_None)
-        return c10::cuda::getCurrentCUDAStream(THPVariable_Unpack(of).get_device()).stream();
+    c.make_current();
+    if (o == Py_None) return c10::cuda::getCurrentCUDAStream(c.device()).stream();
     void* s = PyLong_AsVoidPtr(o);
     if (!s && PyErr_Occurred()) raise_set();
     return s;
@@ -219,7 +250,8 @@ PyObject* guarded(Py_ssize_t n, bool bound, F&& f)
             PyErr_SetString(PyExc_RuntimeError, "the library's entry points are not bound");
             return nullptr;
         }
-        return PyLong_FromLong((long)f());
+        Call c;
+        return PyLong_FromLong((long)f(c));
     } catch (const Raised&) {
         return nullptr;
     } catch (const std::exception& e) {
@@ -231,31 +263,33 @@ PyObject* guarded(Py_ssize_t n, bool bound, F&& f)
 // table, tokens, out, scale, dev_status, stream
 PyObject* py_embed(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<6>(n, lib.embed, [&] {
+    return guarded<6>(n, lib.embed, [&](Call& c) {
         int64_t V, D;
         sizes(a[0], V, D, "table");
-        const Ids t = ids(a[1], "tokens");
-        const Rows out = rows(a[2], t.n, D, "out");
-        const auto* table = dense<uint16_t>(a[0], at::kBFloat16, V, D, "table");
+        const Ids t = ids(c, a[1], "tokens");
+        const Rows out = rows(c, a[2], t.n, D, "out");
+        const auto* table = dense<uint16_t>(c, a[0], at::kBFloat16, V, D, "table");
+        int32_t* word = status(c, a[4]);
         return lib.embed(table, V, width(D), t.p, t.bytes, t.n, real(a[3]), out.p, out.ld,
-                         status(a[4]), stream(a[5], a[0]));
+                         word, stream(c, a[5]));
     });
 }
 
 // dy, tokens, grad, scratch, scale, accumulate, dev_status, stream
 PyObject* py_embed_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<8>(n, lib.embed_grad, [&] {
+    return guarded<8>(n, lib.embed_grad, [&](Call& c) {
         int64_t V, D;
         sizes(a[2], V, D, "grad");
-        const Ids t = ids(a[1], "tokens");
-        const Rows dy = rows(a[0], t.n, D, "dy");
-        auto* grad = dense<uint16_t>(a[2], at::kBFloat16, V, D, "grad");
-        const Scratch s = scratch(a[3]);
+        const Ids t = ids(c, a[1], "tokens");
+        const Rows dy = rows(c, a[0], t.n, D, "dy");
+        auto* grad = dense<uint16_t>(c, a[2], at::kBFloat16, V, D, "grad");
+        const Scratch s = scratch(c, a[3]);
+        int32_t* word = status(c, a[6]);
         const int add = PyObject_IsTrue(a[5]);
         if (add < 0) raise_set();
         return lib.embed_grad(dy.p, dy.ld, t.p, t.bytes, t.n, real(a[4]), V, width(D), grad, add,
-                              s.p, s.bytes, status(a[6]), stream(a[7], a[2]));
+                              s.p, s.bytes, word, stream(c, a[7]));
     });
 }
 
@@ -264,22 +298,22 @@ int64_t blocks(int64_t D) { return (D + ZERO_NORM_BLOCK - 1) / ZERO_NORM_BLOCK; 
 // x, weight, y, codes, scales, rstd, residual, sum_out, eps, stream
 PyObject* py_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<10>(n, lib.norm, [&] {
+    return guarded<10>(n, lib.norm, [&](Call& c) {
         int64_t T, D;
         sizes(a[0], T, D, "x");
-        const Rows x = rows(a[0], T, D, "x");
-        const auto* w = dense<uint16_t>(a[1], at::kBFloat16, D, -1, "weight");
-        const Rows y = rows(a[2], T, D, "y");
+        const Rows x = rows(c, a[0], T, D, "x");
+        const auto* w = dense<uint16_t>(c, a[1], at::kBFloat16, D, -1, "weight");
+        const Rows y = rows(c, a[2], T, D, "y");
         auto* codes =
-            a[3] == Py_None ? nullptr : dense<int8_t>(a[3], at::kChar, T, D, "codes");
+            a[3] == Py_None ? nullptr : dense<int8_t>(c, a[3], at::kChar, T, D, "codes");
         auto* scales = a[4] == Py_None
                            ? nullptr
-                           : dense<float>(a[4], at::kFloat, T, blocks(D), "scales");
-        auto* rstd = dense<float>(a[5], at::kFloat, T, -1, "rstd");
-        const Rows res = rows_or_none(a[6], T, D, "residual");
-        const Rows sum = rows_or_none(a[7], T, D, "sum_out");
+                           : dense<float>(c, a[4], at::kFloat, T, blocks(D), "scales");
+        auto* rstd = dense<float>(c, a[5], at::kFloat, T, -1, "rstd");
+        const Rows res = rows_or_none(c, a[6], T, D, "residual");
+        const Rows sum = rows_or_none(c, a[7], T, D, "sum_out");
         return lib.norm(x.p, x.ld, res.p, res.ld, w, T, width(D), real(a[8]), y.p, y.ld, sum.p,
-                        sum.ld, codes, scales, rstd, stream(a[9], a[0]));
+                        sum.ld, codes, scales, rstd, stream(c, a[9]));
     });
 }
 
@@ -291,77 +325,79 @@ struct Checkpoint {
     const uint16_t* w;
 };
 
-Checkpoint checkpoint(PyObject* codes, PyObject* scales, PyObject* rstd, PyObject* weight)
+Checkpoint checkpoint(Call& c, PyObject* codes, PyObject* scales, PyObject* rstd, PyObject* weight)
 {
-    Checkpoint c;
-    sizes(codes, c.T, c.D, "codes");
-    c.codes = dense<int8_t>(codes, at::kChar, c.T, c.D, "codes");
-    c.scales = dense<float>(scales, at::kFloat, c.T, blocks(c.D), "scales");
-    c.rstd = dense<float>(rstd, at::kFloat, c.T, -1, "rstd");
-    c.w = dense<uint16_t>(weight, at::kBFloat16, c.D, -1, "weight");
-    return c;
+    Checkpoint k;
+    sizes(codes, k.T, k.D, "codes");
+    k.codes = dense<int8_t>(c, codes, at::kChar, k.T, k.D, "codes");
+    k.scales = dense<float>(c, scales, at::kFloat, k.T, blocks(k.D), "scales");
+    k.rstd = dense<float>(c, rstd, at::kFloat, k.T, -1, "rstd");
+    k.w = dense<uint16_t>(c, weight, at::kBFloat16, k.D, -1, "weight");
+    return k;
 }
 
 // codes, scales, rstd, weight, y, stream
 PyObject* py_norm_replay(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<6>(n, lib.norm_replay, [&] {
-        const Checkpoint c = checkpoint(a[0], a[1], a[2], a[3]);
-        const Rows y = rows(a[4], c.T, c.D, "y");
-        return lib.norm_replay(c.codes, c.scales, c.rstd, c.w, c.T, width(c.D), y.p, y.ld,
-                               stream(a[5], a[4]));
+    return guarded<6>(n, lib.norm_replay, [&](Call& c) {
+        const Checkpoint k = checkpoint(c, a[0], a[1], a[2], a[3]);
+        const Rows y = rows(c, a[4], k.T, k.D, "y");
+        return lib.norm_replay(k.codes, k.scales, k.rstd, k.w, k.T, width(k.D), y.p, y.ld,
+                               stream(c, a[5]));
     });
 }
 
 // dy, codes, scales, rstd, weight, dx, dweight, scratch, dsum, stream
 PyObject* py_norm_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<10>(n, lib.norm_grad, [&] {
-        const Checkpoint c = checkpoint(a[1], a[2], a[3], a[4]);
-        const Rows dy = rows(a[0], c.T, c.D, "dy");
-        const Rows dx = rows(a[5], c.T, c.D, "dx");
-        auto* dw = dense<uint16_t>(a[6], at::kBFloat16, c.D, -1, "dweight");
-        const Scratch s = scratch(a[7]);
-        const Rows dsum = rows_or_none(a[8], c.T, c.D, "dsum");
-        return lib.norm_grad(dy.p, dy.ld, dsum.p, dsum.ld, c.codes, c.scales, c.rstd, c.w, c.T,
-                             width(c.D), dx.p, dx.ld, dw, s.p, s.bytes, stream(a[9], a[5]));
+    return guarded<10>(n, lib.norm_grad, [&](Call& c) {
+        const Checkpoint k = checkpoint(c, a[1], a[2], a[3], a[4]);
+        const Rows dy = rows(c, a[0], k.T, k.D, "dy");
+        const Rows dx = rows(c, a[5], k.T, k.D, "dx");
+        auto* dw = dense<uint16_t>(c, a[6], at::kBFloat16, k.D, -1, "dweight");
+        const Scratch s = scratch(c, a[7]);
+        const Rows dsum = rows_or_none(c, a[8], k.T, k.D, "dsum");
+        return lib.norm_grad(dy.p, dy.ld, dsum.p, dsum.ld, k.codes, k.scales, k.rstd, k.w, k.T,
+                             width(k.D), dx.p, dx.ld, dw, s.p, s.bytes, stream(c, a[9]));
     });
 }
 
 // h, table, targets, loss, lse, scratch, flags, dev_status, stream
 PyObject* py_xent(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<9>(n, lib.xent, [&] {
+    return guarded<9>(n, lib.xent, [&](Call& c) {
         int64_t V, D;
         sizes(a[1], V, D, "table");
-        const Ids t = ids(a[2], "targets");
-        const Rows h = rows(a[0], t.n, D, "h");
-        const auto* table = dense<uint16_t>(a[1], at::kBFloat16, V, D, "table");
-        auto* loss = dense<float>(a[3], at::kFloat, t.n, -1, "loss");
-        auto* lse = dense<float>(a[4], at::kFloat, t.n, -1, "lse");
-        const Scratch s = scratch(a[5]);
+        const Ids t = ids(c, a[2], "targets");
+        const Rows h = rows(c, a[0], t.n, D, "h");
+        const auto* table = dense<uint16_t>(c, a[1], at::kBFloat16, V, D, "table");
+        auto* loss = dense<float>(c, a[3], at::kFloat, t.n, -1, "loss");
+        auto* lse = dense<float>(c, a[4], at::kFloat, t.n, -1, "lse");
+        const Scratch s = scratch(c, a[5]);
+        int32_t* word = status(c, a[7]);
         return lib.xent(h.p, h.ld, table, V, width(D), t.p, t.bytes, t.n, loss, lse, s.p, s.bytes,
-                        (int32_t)whole(a[6]), status(a[7]), stream(a[8], a[1]));
+                        (int32_t)whole(a[6]), word, stream(c, a[8]));
     });
 }
 
 // h, table, targets, lse, dloss, dh, dtable, scratch, piece, flags, dev_status, stream
 PyObject* py_xent_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<12>(n, lib.xent_grad, [&] {
+    return guarded<12>(n, lib.xent_grad, [&](Call& c) {
         int64_t V, D;
         sizes(a[1], V, D, "table");
-        const Ids t = ids(a[2], "targets");
-        const Rows h = rows(a[0], t.n, D, "h");
-        const auto* table = dense<uint16_t>(a[1], at::kBFloat16, V, D, "table");
-        const auto* lse = dense<float>(a[3], at::kFloat, t.n, -1, "lse");
-        const auto* dloss = dense<float>(a[4], at::kFloat, t.n, -1, "dloss");
-        const Rows dh = rows(a[5], t.n, D, "dh");
-        auto* dtable = dense<uint16_t>(a[6], at::kBFloat16, V, D, "dtable");
-        const Scratch s = scratch(a[7]);
+        const Ids t = ids(c, a[2], "targets");
+        const Rows h = rows(c, a[0], t.n, D, "h");
+        const auto* table = dense<uint16_t>(c, a[1], at::kBFloat16, V, D, "table");
+        const auto* lse = dense<float>(c, a[3], at::kFloat, t.n, -1, "lse");
+        const auto* dloss = dense<float>(c, a[4], at::kFloat, t.n, -1, "dloss");
+        const Rows dh = rows(c, a[5], t.n, D, "dh");
+        auto* dtable = dense<uint16_t>(c, a[6], at::kBFloat16, V, D, "dtable");
+        const Scratch s = scratch(c, a[7]);
+        int32_t* word = status(c, a[10]);
         return lib.xent_grad(h.p, h.ld, table, V, width(D), t.p, t.bytes, t.n, lse, dloss, dh.p,
                              dh.ld, dtable, whole(a[8]), s.p, s.bytes, (int32_t)whole(a[9]),
-                             status(a[10]), stream(a[11], a[1]));
+                             word, stream(c, a[11]));
     });
 }
 

@@ -3,7 +3,8 @@
 As in binding.py the caller owns every buffer, outputs and scratch among them,
 status codes become ZeroError, and there is no fallback path; work goes to the
 current torch stream of the tensors' device unless `stream` (a torch stream or
-its address) says otherwise.  Shapes, types, strides and devices are checked by
+its address) says otherwise; that device (the same for all of a call's tensors) need
+not be the current one.  Shapes, types, strides and devices are checked by
 the extension module _lm (csrc/lm_binding.cpp; TypeError, ValueError), alignment,
 sizes and overlaps by the library.
 
