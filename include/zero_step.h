@@ -618,7 +618,8 @@ zero_status zero_ckpt_load(const zero_plan_t* plan, const char* dir, uint16_t* c
  *   - scratch: scratch_bytes of device memory, at least what the matching
  *     *_scratch_bytes call returns (-1 for sizes it does not take), 16-byte
  *     aligned, not shared by calls that may overlap in time.  Its contents
- *     need no preparation.
+ *     need no preparation.  What is enough for T tokens is enough for fewer (with
+ *     the same V, D and piece).
  * ---------------------------------------------------------------------- */
 
 #define ZERO_NORM_BLOCK 128        /* elements of a row that share a scale of the checkpoint */

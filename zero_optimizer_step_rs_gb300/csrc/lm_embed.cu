@@ -699,6 +699,15 @@ GradScratch grad_scratch(int64_t T, int32_t D)
     return s;
 }
 
+// What grad_scratch() asks for at any number of tokens up to T: fewer tokens
+// may have more chunks, of 8 places.
+int64_t grad_bytes(int64_t T, int32_t D)
+{
+    const int64_t slices = (D + kColumns - 1) / kColumns;
+    const int64_t last8 = (kFewWarps - 1) / slices * 32;       // tokens with such chunks
+    return std::max(T > last8 ? grad_scratch(last8, D).bytes : 0, grad_scratch(T, D).bytes);
+}
+
 }  // namespace
 
 extern "C" zero_status zero_embed(const uint16_t* table, int64_t V, int32_t D, const void* tokens,
@@ -742,7 +751,7 @@ extern "C" zero_status zero_embed(const uint16_t* table, int64_t V, int32_t D, c
 extern "C" int64_t zero_embed_grad_scratch_bytes(int64_t T, int64_t V, int32_t D)
 {
     if (check_sizes(T, V, D) != ZERO_OK) return -1;
-    return grad_scratch(T, D).bytes;
+    return grad_bytes(T, D);
 }
 
 extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const void* tokens,

@@ -74,6 +74,7 @@ constexpr int kEpilogueWarps = 8;                  // two for each quarter of th
 constexpr int kThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kStageBytes = 2 * 128 * BK * 2;      // per CTA: 128 rows of each operand
 constexpr int kPieceAlign = 256;
+constexpr int64_t kMostP = 1ll << 28;              // elements of a piece's P, unless asked for
 constexpr uint64_t kWaitLimit = 2000000000;        // ns that a wait may take
 constexpr uint64_t kDrainLimit = 200000000;
 constexpr int kWarpStage = 4096;                   // an epilogue warp's output buffer
@@ -1086,7 +1087,7 @@ GradPlan grad_plan(int64_t T, int64_t V, int32_t D, int64_t piece)
     GradPlan g;
     if (piece == 0) {
         // P of a piece is at most 512 MiB; equal pieces
-        const int64_t most = std::max<int64_t>(kPieceAlign, (1ll << 28) / std::max<int64_t>(T, 1) /
+        const int64_t most = std::max<int64_t>(kPieceAlign, kMostP / std::max<int64_t>(T, 1) /
                                                                 kPieceAlign * kPieceAlign);
         const int64_t n = (V + most - 1) / most;
         piece = (V + n - 1) / n;
@@ -1105,6 +1106,21 @@ GradPlan grad_plan(int64_t T, int64_t V, int32_t D, int64_t piece)
     g.unit = g.lost + up(4 * T, 256);
     g.bytes = g.unit + 256;
     return g;
+}
+
+// What grad_plan() asks for at any number of tokens up to T: fewer tokens may
+// take a larger piece, and split the sum of dh more often.
+int64_t grad_bytes(int64_t T, int64_t V, int32_t D, int64_t piece)
+{
+    const int64_t all = up(V, kPieceAlign), longest = piece ? std::min(piece, all) : all;
+    int64_t p = T * longest;                             // elements of P
+    if (piece == 0) p = std::min(p, std::max<int64_t>(kMostP, T * kPieceAlign));
+    // t tokens are split at most pairs / (tiles(t) tiles(D)) times
+    const int64_t pairs = device_sms() / 2, d = tiles(D);
+    const int64_t most = std::max<int64_t>(
+        1, std::min<int64_t>(pairs / d, (std::min(V, longest) + BK - 1) / BK));
+    const int64_t rows = std::max(T, std::min(T * most, BM * (pairs / d)));
+    return up(2 * p, 256) + up(2 * T * D, 256) + up(4 * rows * D, 256) + up(4 * T, 256) + 256;
 }
 
 zero_status check_xent(int64_t T, int64_t V, int32_t D, int32_t target_bytes, int32_t flags,
@@ -1189,7 +1205,7 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
 extern "C" int64_t zero_xent_grad_scratch_bytes(int64_t T, int64_t V, int32_t D, int64_t piece)
 {
     if (check_sizes(T, V, D) != ZERO_OK || piece < 0 || piece % kPieceAlign != 0) return -1;
-    return grad_plan(T, V, D, piece).bytes;
+    return grad_bytes(T, V, D, piece);
 }
 
 extern "C" zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uint16_t* table,
