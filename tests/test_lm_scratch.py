@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import zero_optimizer_step_rs_gb300 as z
+from zero_optimizer_step_rs_gb300 import binding as B
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -37,6 +38,27 @@ def never_falls():
 
 def test_a_size_never_falls_as_tokens_are_added():
     never_falls()
+
+
+@pytest.mark.parametrize("T,V,D", [((1 << 31) - 1024, 1000, 65536), (1 << 25, 1 << 26, 64),
+                                   (1, (1 << 31) - 1024, 65536)])
+def test_sizes_that_a_call_refuses_have_no_scratch_size(T, V, D):
+    """Sizes within each limit whose product is past what a launch counts: -1,
+    where the call says that it does not take them (before it looks at a buffer)."""
+    L = B.lib()
+    word = 1 << 40
+    sizes_and_calls = [
+        (L.zero_embed_grad_scratch_bytes(T, V, D), lambda: L.zero_embed_grad(
+            word, D, word, 8, T, 1.0, V, D, word, 0, None, 0, None, None)),
+        (L.zero_xent_scratch_bytes(T, V, D), lambda: L.zero_xent(
+            word, D, word, V, D, word, 8, T, word, word, None, 0, 0, None, None)),
+        (L.zero_xent_grad_scratch_bytes(T, V, D, 0), lambda: L.zero_xent_grad(
+            word, D, word, V, D, word, 8, T, word, word, word, D, word, 0, None, 0, 0, None, None)),
+    ]
+    for size, call in sizes_and_calls:
+        # (without scratch a call that takes the sizes stops at the missing buffer)
+        assert call() == (B.ZERO_ERR_SIZE if size == -1 else B.ZERO_ERR_NULL)
+    assert -1 in (size for size, _ in sizes_and_calls)
 
 
 @pytest.mark.gpu

@@ -708,6 +708,14 @@ int64_t grad_bytes(int64_t T, int32_t D)
     return std::max(T > last8 ? grad_scratch(last8, D).bytes : 0, grad_scratch(T, D).bytes);
 }
 
+zero_status check_grad(int64_t T, int64_t V, int32_t D)
+{
+    LM_CHECK(check_sizes(T, V, D));
+    // a launch's warps
+    const int64_t slices = (D + kColumns - 1) / kColumns;
+    return (T + 31) / 32 * slices > INT32_MAX ? ZERO_ERR_SIZE : ZERO_OK;
+}
+
 }  // namespace
 
 extern "C" zero_status zero_embed(const uint16_t* table, int64_t V, int32_t D, const void* tokens,
@@ -750,7 +758,7 @@ extern "C" zero_status zero_embed(const uint16_t* table, int64_t V, int32_t D, c
 
 extern "C" int64_t zero_embed_grad_scratch_bytes(int64_t T, int64_t V, int32_t D)
 {
-    if (check_sizes(T, V, D) != ZERO_OK) return -1;
+    if (check_grad(T, V, D) != ZERO_OK) return -1;
     return grad_bytes(T, D);
 }
 
@@ -760,7 +768,7 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
                                        void* scratch, int64_t scratch_bytes, int32_t* dev_status,
                                        void* stream)
 {
-    LM_CHECK(check_sizes(T, V, D));
+    LM_CHECK(check_grad(T, V, D));
     LM_CHECK(check_ld(dy_ld, D));
     if (token_bytes != 4 && token_bytes != 8) return ZERO_ERR_INVALID_ARG;
     if (accumulate != 0 && accumulate != 1) return ZERO_ERR_INVALID_ARG;
@@ -775,7 +783,6 @@ extern "C" zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const 
     LM_CHECK(check_ptr(scratch));
     LM_CHECK(check_status(dev_status));
     const int64_t slices = (D + kColumns - 1) / kColumns;
-    if ((T + 31) / 32 * slices > INT32_MAX) return ZERO_ERR_SIZE;  // a launch's warps
     const GradScratch g = grad_scratch(T, D);
     if (scratch_bytes < g.bytes) return ZERO_ERR_SIZE;
     Spans sp;

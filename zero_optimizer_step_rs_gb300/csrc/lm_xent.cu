@@ -1123,17 +1123,23 @@ int64_t grad_bytes(int64_t T, int64_t V, int32_t D, int64_t piece)
     return up(2 * p, 256) + up(2 * T * D, 256) + up(4 * rows * D, 256) + up(4 * T, 256) + 256;
 }
 
-zero_status check_xent(int64_t T, int64_t V, int32_t D, int32_t target_bytes, int32_t flags,
-                       const int32_t* dev_status)
+zero_status check_units(int64_t T, int64_t V, int32_t D)
 {
     LM_CHECK(check_sizes(T, V, D));
-    if (target_bytes != 4 && target_bytes != 8) return ZERO_ERR_INVALID_ARG;
-    if (flags & ~ZERO_FLAG_DEBUG_EXPIRE_WAITS) return ZERO_ERR_INVALID_ARG;
-    if (flags && !dev_status) return ZERO_ERR_NULL;
     // the units of a launch are counted in 32 bits
     const int64_t t = tiles(T, 128), v = tiles(V, 128), d = tiles(D, 128);
     if (t * v > INT32_MAX / 2 || v * d > INT32_MAX / 2 || t * d > INT32_MAX / 2)
         return ZERO_ERR_SIZE;
+    return ZERO_OK;
+}
+
+zero_status check_xent(int64_t T, int64_t V, int32_t D, int32_t target_bytes, int32_t flags,
+                       const int32_t* dev_status)
+{
+    LM_CHECK(check_units(T, V, D));
+    if (target_bytes != 4 && target_bytes != 8) return ZERO_ERR_INVALID_ARG;
+    if (flags & ~ZERO_FLAG_DEBUG_EXPIRE_WAITS) return ZERO_ERR_INVALID_ARG;
+    if (flags && !dev_status) return ZERO_ERR_NULL;
     return check_status(dev_status);
 }
 
@@ -1141,7 +1147,7 @@ zero_status check_xent(int64_t T, int64_t V, int32_t D, int32_t target_bytes, in
 
 extern "C" int64_t zero_xent_scratch_bytes(int64_t T, int64_t V, int32_t D)
 {
-    if (check_sizes(T, V, D) != ZERO_OK) return -1;
+    if (check_units(T, V, D) != ZERO_OK) return -1;
     return loss_scratch(T, V).bytes;
 }
 
@@ -1204,7 +1210,7 @@ extern "C" zero_status zero_xent(const uint16_t* h, int64_t h_ld, const uint16_t
 
 extern "C" int64_t zero_xent_grad_scratch_bytes(int64_t T, int64_t V, int32_t D, int64_t piece)
 {
-    if (check_sizes(T, V, D) != ZERO_OK || piece < 0 || piece % kPieceAlign != 0) return -1;
+    if (check_units(T, V, D) != ZERO_OK || piece < 0 || piece % kPieceAlign != 0) return -1;
     return grad_bytes(T, V, D, piece);
 }
 
