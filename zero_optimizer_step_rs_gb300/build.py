@@ -1,14 +1,17 @@
 """Build the in-tree C-ABI library libzero_step.so for sm_103a.
 
-The Python module _lm (csrc/lm_binding.cpp, the tensors' checks of the
-language-model operators) is compiled beside it with the host compiler against
-the installed torch's headers.
-
 The translation units (the step's CUDA kernels and entry points, the
 language-model operators' three, and the host-only plan and checkpoint code)
-are compiled in parallel by nvcc and linked into one shared library with the CUDA runtime linked statically, so the library needs no
-libcudart at load time and can be loaded (and its host-only entry points
-called) on a machine without a GPU.
+are compiled in parallel by nvcc and linked into one shared library with the
+CUDA runtime linked statically, so the library needs no libcudart at load time
+and can be loaded (and its host-only entry points called) on a machine without
+a GPU.
+
+The Python module _lm (csrc/lm_binding.cpp, the tensors' checks of the
+language-model operators) is compiled beside it with the host compiler against
+the installed torch's headers.  The library needs neither: without a torch that
+has CUDA the module is left out, and if it fails to compile the library is in
+place all the same.
 """
 from __future__ import annotations
 
@@ -42,11 +45,32 @@ def nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(EXT)):
+def torch_dir():
+    """Where a torch with CUDA is installed, or None."""
+    spec = importlib.util.find_spec("torch")
+    for d in (spec and spec.submodule_search_locations) or ():
+        if os.path.exists(os.path.join(d, "lib", "libc10_cuda.so")):
+            return d
+    return None
+
+
+def _older(built, sources) -> bool:
+    if not os.path.exists(built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return any(os.path.getmtime(p) > t for p in SOURCES + [EXT_SOURCE] + HEADERS + [__file__])
+    t = os.path.getmtime(built)
+    return any(os.path.getmtime(p) > t for p in [*sources, *HEADERS, __file__])
+
+
+def _lib_stale() -> bool:
+    return _older(LIB, SOURCES)
+
+
+def _ext_stale() -> bool:
+    return torch_dir() is not None and _older(EXT, [EXT_SOURCE])
+
+
+def _stale() -> bool:
+    return _lib_stale() or _ext_stale()
 
 
 def compile_commands():
@@ -61,7 +85,7 @@ def compile_commands():
 
 
 def ext_command():
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    torch = torch_dir()
     cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
     include = [INCLUDE, os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
@@ -79,28 +103,33 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     with open(os.path.join(BUILD_DIR, ".lock"), "w") as lock:
         fcntl.flock(lock, fcntl.LOCK_EX)
-        return _build(verbose) if force or _stale() else LIB
+        lib, ext = force or _lib_stale(), _ext_stale() or (force and torch_dir() is not None)
+        if torch_dir() is None:
+            print("no torch with CUDA here: the module _lm of the language-model operators is "
+                  "left out", file=sys.stderr)
+        _build(lib, ext, verbose)
+    return LIB
 
 
-def _build(verbose: bool) -> str:
-    cmds, link = compile_commands()
-    cmds.append(ext_command())
+def _build(lib: bool, ext: bool, verbose: bool) -> None:
+    cmds, link = compile_commands() if lib else ([], None)
+    ext_cmds = [ext_command()] if ext else []
     procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
-             for c in cmds]
-    failed = []
-    for c, p in zip(cmds, procs):
+             for c in cmds + ext_cmds]
+    failed = {}
+    for i, (c, p) in enumerate(zip(cmds + ext_cmds, procs)):
         out, _ = p.communicate()
         if verbose and out:
             sys.stdout.write(out)
         if p.returncode != 0:
-            failed.append((c, out))
+            failed[i] = f"$ {' '.join(c)}\n{out}"
+    if lib and not any(i < len(cmds) for i in failed):
+        subprocess.run(link, check=True)
+        os.replace(LIB + ".tmp", LIB)
     if failed:
-        msg = "\n".join(f"$ {' '.join(c)}\n{o}" for c, o in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
-    subprocess.run(link, check=True)
-    os.replace(LIB + ".tmp", LIB)
-    os.replace(EXT + ".tmp", EXT)
-    return LIB
+        raise RuntimeError("the build failed:\n" + "\n".join(failed.values()))
+    if ext:
+        os.replace(EXT + ".tmp", EXT)
 
 
 if __name__ == "__main__":
