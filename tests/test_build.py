@@ -49,3 +49,17 @@ def test_a_module_that_does_not_compile_leaves_the_library(small, monkeypatch):
     with pytest.raises(RuntimeError, match="#error no"):
         build.build()
     assert os.path.exists(build.LIB) and not os.path.exists(build.EXT)
+
+
+def test_the_module_is_built_again_for_another_torch(monkeypatch, tmp_path):
+    """The one that stands here, as build() leaves it, is fresh for the installed
+    torch and stale for another version of it, or the same one elsewhere."""
+    build.build()
+    if build.torch_dir() is None:
+        pytest.skip("no torch with CUDA here")
+    assert not build._stale()
+    (tmp_path / "lib").mkdir()
+    (tmp_path / "lib" / "libc10_cuda.so").write_text("")
+    (tmp_path / "version.py").write_text("__version__ = '0.0'\n")
+    installed(monkeypatch, tmp_path)
+    assert build._stale()

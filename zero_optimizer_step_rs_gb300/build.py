@@ -18,6 +18,7 @@ from __future__ import annotations
 import fcntl
 import importlib.util
 import os
+import runpy
 import subprocess
 import sys
 import sysconfig
@@ -65,8 +66,19 @@ def _lib_stale() -> bool:
     return _older(LIB, SOURCES)
 
 
+def _ext_for() -> str:
+    """What the module is tied to: the torch and the Python it was built against."""
+    version = runpy.run_path(os.path.join(torch_dir(), "version.py"))["__version__"]
+    return f"{torch_dir()} {version} {sysconfig.get_config_var('EXT_SUFFIX')}\n"
+
+
 def _ext_stale() -> bool:
-    return torch_dir() is not None and _older(EXT, [EXT_SOURCE])
+    if torch_dir() is None:
+        return False
+    if _older(EXT, [EXT_SOURCE]) or not os.path.exists(EXT + ".for"):
+        return True
+    with open(EXT + ".for") as f:
+        return f.read() != _ext_for()
 
 
 def _stale() -> bool:
@@ -130,6 +142,8 @@ def _build(lib: bool, ext: bool, verbose: bool) -> None:
         raise RuntimeError("the build failed:\n" + "\n".join(failed.values()))
     if ext:
         os.replace(EXT + ".tmp", EXT)
+        with open(EXT + ".for", "w") as f:
+            f.write(_ext_for())
 
 
 if __name__ == "__main__":
