@@ -32,10 +32,12 @@ def lm():
     return lm._lm
 
 
+def on(spec, device):
+    return torch.empty(spec[0], dtype=spec[1], device=device) if isinstance(spec, tuple) else spec
+
+
 @pytest.mark.parametrize("name", CALLS)
 def test_tensors_on_two_gpus_are_refused(lm, name):
-    def on(spec, device):
-        return torch.empty(spec[0], dtype=spec[1], device=device) if isinstance(spec, tuple) else spec
     tensors = [i for i, x in enumerate(CALLS[name]) if isinstance(x, tuple)]
     assert len(tensors) >= 4
     for other in tensors:
@@ -43,3 +45,13 @@ def test_tensors_on_two_gpus_are_refused(lm, name):
             args = [on(x, "cuda:1" if i == other else "cuda:0") for i, x in enumerate(CALLS[name])]
         with pytest.raises(ValueError, match="different devices"):
             getattr(lm, name)(*args)
+
+
+@pytest.mark.parametrize("name,at", [("xent", 6), ("xent_grad", 9)])
+@pytest.mark.parametrize("flags", [1 << 32, -(1 << 33), 1 << 80])
+def test_flags_past_32_bits_are_refused(lm, name, at, flags):
+    with FakeTensorMode():
+        args = [on(x, "cuda:0") for x in CALLS[name]]
+    args[at] = flags
+    with pytest.raises(OverflowError):
+        getattr(lm, name)(*args)

@@ -227,6 +227,16 @@ int64_t whole(PyObject* o)
     return v;
 }
 
+int32_t flags(PyObject* o)
+{
+    const int64_t v = whole(o);
+    if (v < INT32_MIN || v > INT32_MAX) {
+        PyErr_SetString(PyExc_OverflowError, "flags: more than 32 bits");
+        raise_set();
+    }
+    return (int32_t)v;
+}
+
 float real(PyObject* o)
 {
     const double v = PyFloat_AsDouble(o);
@@ -375,8 +385,9 @@ PyObject* py_xent(PyObject*, PyObject* const* a, Py_ssize_t n)
         auto* lse = dense<float>(c, a[4], at::kFloat, t.n, -1, "lse");
         const Scratch s = scratch(c, a[5]);
         int32_t* word = status(c, a[7]);
-        return lib.xent(h.p, h.ld, table, V, width(D), t.p, t.bytes, t.n, loss, lse, s.p, s.bytes,
-                        (int32_t)whole(a[6]), word, stream(c, a[8]));
+        const int32_t f = flags(a[6]);
+        return lib.xent(h.p, h.ld, table, V, width(D), t.p, t.bytes, t.n, loss, lse, s.p, s.bytes, f,
+                        word, stream(c, a[8]));
     });
 }
 
@@ -395,9 +406,9 @@ PyObject* py_xent_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
         auto* dtable = dense<uint16_t>(c, a[6], at::kBFloat16, V, D, "dtable");
         const Scratch s = scratch(c, a[7]);
         int32_t* word = status(c, a[10]);
+        const int32_t f = flags(a[9]);
         return lib.xent_grad(h.p, h.ld, table, V, width(D), t.p, t.bytes, t.n, lse, dloss, dh.p,
-                             dh.ld, dtable, whole(a[8]), s.p, s.bytes, (int32_t)whole(a[9]),
-                             word, stream(c, a[11]));
+                             dh.ld, dtable, whole(a[8]), s.p, s.bytes, f, word, stream(c, a[11]));
     });
 }
 
