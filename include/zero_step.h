@@ -639,8 +639,9 @@ int64_t zero_embed_grad_scratch_bytes(int64_t T, int64_t V, int32_t D);
  * Its gradient: grad[v, :] = bf16(scale * sum of dy[t, :] over the t with
  * tokens[t] == v), every row of the table being written; with accumulate = 1,
  * bf16(grad[v, :] + that) for the rows that are met, the others untouched (a
- * tied table's gradient, after zero_xent_grad).  The tokens are sorted first,
- * and each row's terms are added in ascending t.
+ * tied table's gradient, after zero_xent_grad).  A row's terms are taken in
+ * ascending t, those of a row with many of them as a sum of partial sums, cut at
+ * places that the sizes and the ids alone decide.
  */
 zero_status zero_embed_grad(const uint16_t* dy, int64_t dy_ld, const void* tokens,
                             int32_t token_bytes, int64_t T, float scale, int64_t V, int32_t D,

@@ -17,9 +17,11 @@
 // instructions around each row's 512 bytes a warp, and by latency), 10 the join.
 //
 // The gradient's sums have one fixed order, so a step can be repeated bit for
-// bit: the tokens are sorted by (id, position) and each row's terms are
-// added in that order, in pieces that depend on the tokens alone.  No
-// atomics touch a sum.
+// bit.  More than 1024 tokens are sorted by (id, position); a row's terms are
+// added in that order, and a row with more terms than a chunk has places is the
+// sum of its chunks' sums, in pieces that depend on the sizes and the tokens
+// alone.  Up to 1024 tokens are not sorted: a block looks for its id's places and
+// adds them in order.  No atomics touch a sum.
 #include "lm_common.cuh"
 
 namespace {

@@ -29,9 +29,10 @@
 // again), on the tensor cores; with few tokens the table's 2*V*D bytes.
 // Measured, one GB300: 8192 x 128256 x 2048 forward 2.05 ms in a short burst
 // (2.1 PFLOP/s, tensor pipe 98 % busy at the 1.75 GHz that the power limit
-// leaves) and 2.3 ms sustained; backward 7.1 and 7.7 ms (1.82 and 1.69).  17 x
-// 50257 x 768 forward 23 us for the table's 77 MB (11.4 us at the copy rate): two
-// launches, a pipeline to fill, and three rounds of tiles for 76 CTA pairs.
+// leaves) and 2.3 ms sustained; backward 7.1 and 7.6 to 7.7 ms (1.82 and 1.67 to
+// 1.69).  17 x 50257 x 768 forward 25 us for the table's 77 MB (11.4 us at the copy
+// rate): two launches, a pipeline to fill, and three rounds of tiles for 76 CTA
+// pairs; backward 72 us (23).
 //
 // The product kernel (k_mma): a pair of CTAs (cta_group::2) owns a 256 x 256
 // tile of fp32 sums in tensor memory, 128 rows in each CTA, two tiles deep, so

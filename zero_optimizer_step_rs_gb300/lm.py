@@ -60,8 +60,8 @@ def zero_embed_grad_scratch_bytes(T: int, V: int, D: int) -> int:
 
 def zero_embed_grad(dy, tokens, grad, scratch, scale: float = 1.0, accumulate: bool = False,
                     dev_status=None, stream=None) -> None:
-    """grad[v] = scale * sum of dy[t] over tokens[t] == v, in ascending t;
-    with accumulate, added to what the rows met hold."""
+    """grad[v] = scale * sum of dy[t] over tokens[t] == v, in an order fixed by
+    the sizes and the ids; with accumulate, added to what the rows met hold."""
     code = _lm.embed_grad(dy, tokens, grad, scratch, scale, accumulate, dev_status,
                           _address(stream))
     if code:
