@@ -99,6 +99,7 @@ typedef enum {
  * context as suspect (finish or reset it) rather than continue training. */
 #define ZERO_DEV_DRAIN_FAILED 8
 #define ZERO_DEV_BAD_TOKEN 16      /* a token id or target at or past the table's rows */
+#define ZERO_DEV_BAD_OFFSETS 32    /* sequence offsets that fall, or lie outside [0, T] */
 
 /* Flags for zero_step / zero_rs_avg. */
 #define ZERO_FLAG_CHECK_FINITE 1   /* set ZERO_DEV_NONFINITE when g is non-finite */
@@ -720,6 +721,174 @@ zero_status zero_xent_grad(const uint16_t* h, int64_t h_ld, const uint16_t* tabl
                            const float* lse, const float* dloss, uint16_t* dh, int64_t dh_ld,
                            uint16_t* dtable, int64_t piece, void* scratch, int64_t scratch_bytes,
                            int32_t flags, int32_t* dev_status, void* stream);
+
+/*
+ * Layer norm with the residual's addition.
+ *   s = x + residual (fp32; residual may be NULL), mean[t] = mean(s),
+ *   rstd[t] = 1/sqrt(mean((s - mean)^2) + eps)
+ *   y = bf16((s - mean) * rstd * weight + bias);  sum = bf16(s) (may be NULL)
+ * weight and bias: D bf16 each, or NULL for ones and zeros.  mean, rstd: T floats,
+ * 4-byte aligned.  The statistics are of the fp32 sum; the variance is a sum of squared
+ * distances, not a difference of two sums.
+ */
+zero_status zero_layer_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual,
+                            int64_t residual_ld, const uint16_t* weight, const uint16_t* bias,
+                            int64_t T, int32_t D, float eps, uint16_t* y, int64_t y_ld,
+                            uint16_t* sum, int64_t sum_ld, float* mean, float* rstd,
+                            void* stream);
+
+int64_t zero_layer_norm_grad_scratch_bytes(int64_t T, int32_t D);
+
+/*
+ * Its gradients.  x: what the forward call normalised (its x, or its `sum` where
+ * there was a residual); with xhat = (x - mean) * rstd and u = dy * weight,
+ *   dx = bf16(rstd * (u - mean(u) - xhat * mean(u * xhat)) + dsum),
+ *   dweight = bf16(sum over t of dy * xhat),  dbias = bf16(sum over t of dy).
+ * dsum: the gradient that reaches `sum` by itself (may be NULL).  dx is the
+ * gradient of x and of the residual alike.  weight may be NULL (ones); dweight and
+ * dbias may be NULL (not wanted; scratch may be NULL where both are).
+ */
+zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld, const uint16_t* dsum,
+                                 int64_t dsum_ld, const uint16_t* x, int64_t x_ld,
+                                 const float* mean, const float* rstd, const uint16_t* weight,
+                                 int64_t T, int32_t D, uint16_t* dx, int64_t dx_ld,
+                                 uint16_t* dweight, uint16_t* dbias, void* scratch,
+                                 int64_t scratch_bytes, void* stream);
+
+/* ----------------------------------------------------------------------
+ * Losses of sequences from their tokens' losses: training on preferences and on
+ * rewards.  nll[t] is zero_xent's loss (minus the log probability of token t) under the
+ * model that is trained, ref_nll and old_nll the same under a reference model
+ * and under the model that wrote the tokens; the gradient dnll[t] is zero_xent_grad's
+ * dloss.
+ *
+ * The T tokens are sequences packed one behind the other: sequence s holds the
+ * tokens offsets[s] <= t < offsets[s + 1], offsets being S + 1 integers of
+ * offset_bytes (4 or 8) that do not fall, from 0 or more to T or less; a sequence may
+ * be empty.  Offsets that fall or lie outside set ZERO_DEV_BAD_OFFSETS and leave the
+ * outputs unspecified (nothing outside of them is touched).  Tokens before the
+ * first sequence and behind the last one are not read for a result and their dnll
+ * is not written.  A token with a negative target takes part in nothing, whatever
+ * its losses hold (NaN and Inf included), and its dnll is 0.
+ * S and P below 2^30, T below 2^31 - 1024.  Arrays of 4-byte elements need 4-byte
+ * alignment only, ids and offsets their own size.  Sums over a sequence have fp32 terms
+ * and partial sums of at most 256 tokens, joined in 64 bits.  S = 0 is allowed.
+ * average = 1 divides a sequence's sum by the number of its tokens that count
+ * (0 where none does).
+ * ---------------------------------------------------------------------- */
+
+#define ZERO_PREF_SIGMOID 0        /* (1-e) softplus(-z) + e softplus(z), e = smoothing */
+#define ZERO_PREF_HINGE 1          /* max(0, 1 - z) */
+#define ZERO_PREF_IPO 2            /* (d - margin - 1/(2 beta))^2 */
+
+int64_t zero_preference_scratch_bytes(int64_t T, int64_t P);
+
+/*
+ * The loss of P pairs of sequences, of which 2p is the chosen and 2p + 1 the rejected one:
+ *   ratios[s] = sum over its tokens of (ref_nll - nll), or with average their mean
+ *   (ref_nll NULL: of -nll alone),  counts[s] = the number of them,
+ *   d = ratios[2p] - ratios[2p + 1],  z = beta d - margin,  loss[p] by `kind`,
+ *   slope[p] = the derivative of loss[p] by d, which the gradient takes.
+ * beta > 0; 0 <= smoothing < 0.5, 0 for the other kinds than ZERO_PREF_SIGMOID.
+ * loss, slope: P floats; ratios: 2P floats; counts: 2P int32.
+ */
+zero_status zero_preference(const float* nll, const float* ref_nll, const void* targets,
+                            int32_t target_bytes, int64_t T, const void* offsets,
+                            int32_t offset_bytes, int64_t P, int32_t kind, double beta,
+                            double smoothing, double margin, int32_t average, float* loss,
+                            float* slope, float* ratios, int32_t* counts, void* scratch,
+                            int64_t scratch_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Its gradient: dnll[t] = -dloss[p] slope[p] for the chosen sequence's tokens and
+ * +dloss[p] slope[p] for the rejected one's, divided by counts[s] with average.
+ */
+zero_status zero_preference_grad(const void* targets, int32_t target_bytes, int64_t T,
+                                 const void* offsets, int32_t offset_bytes, int64_t P,
+                                 int32_t average, const float* slope, const int32_t* counts,
+                                 const float* dloss, float* dnll, int32_t* dev_status,
+                                 void* stream);
+
+int64_t zero_policy_scratch_bytes(int64_t T, int64_t S);
+
+/*
+ * Clipped policy loss with a KL term.  For each token, with the advantage A =
+ * advantages[s] or, with per_token = 1, advantages[t]:
+ *   r = exp(old_nll - nll)  (old_nll NULL: r = 1, the tokens being this model's own),
+ *   k = exp(nll - ref_nll) - (nll - ref_nll) - 1,
+ *   term = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl_coef k
+ * (-0 where A is 0).  loss[s] is the sum of the terms of its tokens, kl[s] that of
+ * k, or with average the means; clipped[s] counts the tokens whose bounded r is the
+ * smaller one (decided on the exact difference of the two losses), counts[s] those that
+ * count.  ref_nll may be NULL where kl_coef is 0; kl is then 0.
+ * 0 <= clip_low <= 1, clip_high and kl_coef at least 0 and finite.
+ * loss, kl: S floats; clipped, counts: S int32.
+ */
+zero_status zero_policy(const float* nll, const float* old_nll, const float* ref_nll,
+                        const float* advantages, int32_t per_token, const void* targets,
+                        int32_t target_bytes, int64_t T, const void* offsets, int32_t offset_bytes,
+                        int64_t S, double clip_low, double clip_high, double kl_coef,
+                        int32_t average, float* loss, float* kl, int32_t* clipped, int32_t* counts,
+                        void* scratch, int64_t scratch_bytes, int32_t* dev_status, void* stream);
+
+/*
+ * Its gradient, from the same arguments, zero_policy's counts and the upstream
+ * gradient dloss[s] of each sequence's loss:
+ *   dnll[t] = dloss[s] (r A, or 0 where the token is clipped, + kl_coef (exp(nll - ref_nll) - 1)),
+ * divided by counts[s] with average.
+ */
+zero_status zero_policy_grad(const float* nll, const float* old_nll, const float* ref_nll,
+                             const float* advantages, int32_t per_token, const void* targets,
+                             int32_t target_bytes, int64_t T, const void* offsets,
+                             int32_t offset_bytes, int64_t S, double clip_low, double clip_high,
+                             double kl_coef, int32_t average, const int32_t* counts,
+                             const float* dloss, float* dnll, int32_t* dev_status, void* stream);
+
+/* ----------------------------------------------------------------------
+ * The norm of gradients that lie in many tensors, and clipping: for gradients that
+ * do not come from zero_step_clipped's reduce-scatter (summed in fp32 elsewhere, or of
+ * tensors that are no part of a plan).
+ * ---------------------------------------------------------------------- */
+
+#define ZERO_TYPE_BF16 0
+#define ZERO_TYPE_FP16 1
+#define ZERO_TYPE_FP32 2
+#define ZERO_MAX_TENSORS 65536
+
+/* A contiguous tensor on the device, aligned to its elements only (tensors of a flat
+ * buffer without padding are); numel = 0 is allowed, data may then be NULL. */
+typedef struct {
+    void* data;
+    int64_t numel;
+    int32_t type;                  /* ZERO_TYPE_* */
+} zero_tensor;
+
+int64_t zero_grad_norm_scratch_bytes(int32_t count);
+
+/*
+ * norms[i] = the 2-norm of tensor i (may be NULL), norm[0] = that of all of them.  A
+ * thread's squares are added in fp32, the threads' and blocks' sums in 64 bits, in an order
+ * that the sizes alone decide; a part whose sum of squares overflows or vanishes in
+ * fp32 is taken again relative to its largest value, so that every finite
+ * input has the norm that fp32 can hold.  A norm that is not finite sets
+ * ZERO_DEV_NONFINITE.  `tensors` is a host array that is read during the call; count at most
+ * ZERO_MAX_TENSORS, 0 gives norm 0; at most 2^40 elements a tensor and 2^43 together.
+ */
+zero_status zero_grad_norm(const zero_tensor* tensors, int32_t count, float* norm, float* norms,
+                           void* scratch, int64_t scratch_bytes, int32_t* dev_status,
+                           void* stream);
+
+/*
+ * outs[i] = coef * tensors[i], with coef = max_norm / (norm[0] + 1e-6) computed in double where
+ * that is below 1, else the tensor itself, as zero_step_clipped does (a norm
+ * that is NaN clips nothing, one that is Inf multiplies by 0).  norm: zero_grad_norm's, on the device.
+ * outs: as many tensors of the same sizes, each of its tensor's type or
+ * bf16, written once rounded; they overlap nothing.  outs NULL scales the tensors in
+ * place (they overlap nothing then), and where nothing is to clip none is read or written.
+ * max_norm > 0 and finite.
+ */
+zero_status zero_grad_clip(const zero_tensor* tensors, const zero_tensor* outs, int32_t count,
+                           const float* norm, float max_norm, void* stream);
 
 #ifdef __cplusplus
 }

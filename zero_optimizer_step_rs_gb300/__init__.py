@@ -19,11 +19,18 @@ from .binding import (  # noqa: F401
     ZERO_VARIANT_STAGED, ZERO_VARIANT_FUSED_TMA, ZERO_DEV_TIMEOUT, ZERO_FLAG_DEBUG_EXPIRE_WAITS,
 )
 from .binding import ZERO_DEV_BAD_TOKEN, ZERO_NORM_BLOCK, ZERO_NORM_MAX_WIDTH  # noqa: F401
+from .binding import (  # noqa: F401
+    ZERO_DEV_BAD_OFFSETS, ZERO_MAX_TENSORS, ZERO_PREF_HINGE, ZERO_PREF_IPO, ZERO_PREF_SIGMOID,
+)
 
 # the operators of lm.py, which needs torch at import; the steps above do not
 _LM = ("zero_embed", "zero_embed_grad", "zero_embed_grad_scratch_bytes", "zero_norm",
        "zero_norm_grad", "zero_norm_grad_scratch_bytes", "zero_norm_replay", "zero_xent",
-       "zero_xent_grad", "zero_xent_grad_scratch_bytes", "zero_xent_scratch_bytes")
+       "zero_xent_grad", "zero_xent_grad_scratch_bytes", "zero_xent_scratch_bytes",
+       "zero_layer_norm", "zero_layer_norm_grad", "zero_layer_norm_grad_scratch_bytes",
+       "zero_preference", "zero_preference_grad", "zero_preference_scratch_bytes", "zero_policy",
+       "zero_policy_grad", "zero_policy_scratch_bytes", "zero_grad_norm",
+       "zero_grad_norm_scratch_bytes", "zero_grad_clip")
 
 
 def __getattr__(name):

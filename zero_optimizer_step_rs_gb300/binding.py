@@ -36,8 +36,16 @@ ZERO_VARIANT_FUSED_TMA = 2
 ZERO_DEV_TIMEOUT = 2
 ZERO_DEV_DRAIN_FAILED = 8
 ZERO_DEV_BAD_TOKEN = 16
+ZERO_DEV_BAD_OFFSETS = 32
 ZERO_NORM_BLOCK = 128
 ZERO_NORM_MAX_WIDTH = 16384
+ZERO_PREF_SIGMOID = 0
+ZERO_PREF_HINGE = 1
+ZERO_PREF_IPO = 2
+ZERO_TYPE_BF16 = 0
+ZERO_TYPE_FP16 = 1
+ZERO_TYPE_FP32 = 2
+ZERO_MAX_TENSORS = 65536
 ZERO_FLAG_DEBUG_EXPIRE_WAITS = 1 << 30
 ZERO_COMP_FP16 = 1
 ZERO_COMP_INT8 = 2
@@ -57,7 +65,11 @@ EXPORTED = ("zero_abi_version", "zero_status_string", "zero_plan_create", "zero_
             "zero3_gather_units", "zero_embed", "zero_embed_grad",
             "zero_embed_grad_scratch_bytes", "zero_norm", "zero_norm_replay", "zero_norm_grad",
             "zero_norm_grad_scratch_bytes", "zero_xent", "zero_xent_scratch_bytes",
-            "zero_xent_grad", "zero_xent_grad_scratch_bytes")
+            "zero_xent_grad", "zero_xent_grad_scratch_bytes", "zero_layer_norm",
+            "zero_layer_norm_grad", "zero_layer_norm_grad_scratch_bytes", "zero_preference",
+            "zero_preference_scratch_bytes", "zero_preference_grad", "zero_policy",
+            "zero_policy_scratch_bytes", "zero_policy_grad", "zero_grad_norm",
+            "zero_grad_norm_scratch_bytes", "zero_grad_clip")
 
 
 class ZeroError(RuntimeError):
@@ -78,6 +90,10 @@ class zero_plan_t(ctypes.Structure):
 
 class zero_gather_unit(ctypes.Structure):
     _fields_ = [("lo", ctypes.c_int64), ("hi", ctypes.c_int64), ("out", ctypes.c_void_p)]
+
+
+class zero_tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("type", ctypes.c_int32)]
 
 
 class zero_adamw_hparams(ctypes.Structure):
@@ -181,10 +197,30 @@ def lib():
         L.zero_xent_grad_scratch_bytes.argtypes = [i64, i64, i32, i64]
         L.zero_xent_grad.argtypes = [vp, i64, vp, i64, i32, vp, i32, i64, vp, vp, vp, i64, vp, i64,
                                      vp, i64, i32, vp, vp]
+        f64 = ctypes.c_double
+        L.zero_layer_norm.argtypes = [vp, i64, vp, i64, vp, vp, i64, i32, f32, vp, i64, vp, i64,
+                                      vp, vp, vp]
+        L.zero_layer_norm_grad_scratch_bytes.argtypes = [i64, i32]
+        L.zero_layer_norm_grad.argtypes = [vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, i32, vp,
+                                           i64, vp, vp, vp, i64, vp]
+        L.zero_preference_scratch_bytes.argtypes = [i64, i64]
+        L.zero_preference.argtypes = [vp, vp, vp, i32, i64, vp, i32, i64, i32, f64, f64, f64, i32,
+                                      vp, vp, vp, vp, vp, i64, vp, vp]
+        L.zero_preference_grad.argtypes = [vp, i32, i64, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp]
+        L.zero_policy_scratch_bytes.argtypes = [i64, i64]
+        policy = [vp, vp, vp, vp, i32, vp, i32, i64, vp, i32, i64, f64, f64, f64, i32]
+        L.zero_policy.argtypes = policy + [vp, vp, vp, vp, vp, i64, vp, vp]
+        L.zero_policy_grad.argtypes = policy + [vp, vp, vp, vp, vp]
+        L.zero_grad_norm_scratch_bytes.argtypes = [i32]
+        L.zero_grad_norm.argtypes = [vp, i32, vp, vp, vp, i64, vp, vp]
+        L.zero_grad_clip.argtypes = [vp, vp, i32, vp, f32, vp]
         for name in ("zero_embed", "zero_embed_grad", "zero_norm", "zero_norm_replay",
-                     "zero_norm_grad", "zero_xent", "zero_xent_grad"):
+                     "zero_norm_grad", "zero_xent", "zero_xent_grad", "zero_layer_norm",
+                     "zero_layer_norm_grad", "zero_preference", "zero_preference_grad",
+                     "zero_policy", "zero_policy_grad", "zero_grad_norm", "zero_grad_clip"):
             getattr(L, name).restype = ctypes.c_int
-        for name in ("zero_embed_grad", "zero_norm_grad", "zero_xent", "zero_xent_grad"):
+        for name in ("zero_embed_grad", "zero_norm_grad", "zero_xent", "zero_xent_grad",
+                     "zero_layer_norm_grad", "zero_preference", "zero_policy", "zero_grad_norm"):
             getattr(L, name + "_scratch_bytes").restype = i64
         _lib = L
     return _lib

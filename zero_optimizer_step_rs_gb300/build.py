@@ -1,7 +1,7 @@
 """Build the in-tree C-ABI library libzero_step.so for sm_103a.
 
 The translation units (the step's CUDA kernels and entry points, the
-language-model operators' three, and the host-only plan and checkpoint code)
+language-model operators' six, and the host-only plan and checkpoint code)
 are compiled in parallel by nvcc and linked into one shared library with the
 CUDA runtime linked statically, so the library needs no libcudart at load time
 and can be loaded (and its host-only entry points called) on a machine without
@@ -34,7 +34,9 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 SOURCES = [os.path.join(CSRC, "zero_step.cu"), os.path.join(CSRC, "plan.cpp"),
            os.path.join(CSRC, "ckpt.cpp"), os.path.join(CSRC, "lm_embed.cu"),
-           os.path.join(CSRC, "lm_norm.cu"), os.path.join(CSRC, "lm_xent.cu")]
+           os.path.join(CSRC, "lm_norm.cu"), os.path.join(CSRC, "lm_xent.cu"),
+           os.path.join(CSRC, "lm_layer_norm.cu"), os.path.join(CSRC, "lm_loss.cu"),
+           os.path.join(CSRC, "lm_clip.cu")]
 EXT = os.path.join(PKG, "_lm.so")
 EXT_SOURCE = os.path.join(CSRC, "lm_binding.cpp")
 HEADERS = [os.path.join(INCLUDE, "zero_step.h")] + sorted(
