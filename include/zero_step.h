@@ -765,8 +765,8 @@ zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld, const uint16
  * The T tokens are sequences packed one behind the other: sequence s holds the
  * tokens offsets[s] <= t < offsets[s + 1], offsets being S + 1 integers of
  * offset_bytes (4 or 8) that do not fall, from 0 or more to T or less; a sequence may
- * be empty.  Offsets that fall or lie outside set ZERO_DEV_BAD_OFFSETS and leave the
- * outputs unspecified (nothing outside of them is touched).  Tokens before the
+ * be empty.  Offsets that fall or lie outside set ZERO_DEV_BAD_OFFSETS in the forward call's
+ * dev_status (optional) and leave the outputs unspecified (nothing outside of them is touched).  Tokens before the
  * first sequence and behind the last one are not read for a result and their dnll
  * is not written.  A token with a negative target takes part in nothing, whatever
  * its losses hold (NaN and Inf included), and its dnll is 0.
@@ -806,8 +806,7 @@ zero_status zero_preference(const float* nll, const float* ref_nll, const void* 
 zero_status zero_preference_grad(const void* targets, int32_t target_bytes, int64_t T,
                                  const void* offsets, int32_t offset_bytes, int64_t P,
                                  int32_t average, const float* slope, const int32_t* counts,
-                                 const float* dloss, float* dnll, int32_t* dev_status,
-                                 void* stream);
+                                 const float* dloss, float* dnll, void* stream);
 
 int64_t zero_policy_scratch_bytes(int64_t T, int64_t S);
 
@@ -842,7 +841,7 @@ zero_status zero_policy_grad(const float* nll, const float* old_nll, const float
                              int32_t target_bytes, int64_t T, const void* offsets,
                              int32_t offset_bytes, int64_t S, double clip_low, double clip_high,
                              double kl_coef, int32_t average, const int32_t* counts,
-                             const float* dloss, float* dnll, int32_t* dev_status, void* stream);
+                             const float* dloss, float* dnll, void* stream);
 
 /* ----------------------------------------------------------------------
  * The norm of gradients that lie in many tensors, and clipping: for gradients that

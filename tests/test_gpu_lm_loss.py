@@ -1,6 +1,6 @@
 """Losses of packed sequences and their gradients on the GPU against 64-bit forms.
 
-A tile's sum has 8 terms of a lane and 5 halvings, the tiles are joined in 64 bits: off by 13
+A tile's sum has at most 8 terms of a lane and 5 halvings, the tiles are joined in 64 bits: off by 13
 U32 of the terms' magnitudes, and the result by one rounding (16 U32 are allowed for
 both).  expf and expm1f are taken to be off by 4 U32 of their values, and an argument of
 magnitude |c| that was rounded moves exp(c) by U32 |c| of it."""
@@ -37,7 +37,14 @@ CASES = {
     "one long": (10, [50_000, 3], 5),
     "two long": (0, [3, 40_001, 0, 70_000], 0),
     "ragged": (0, [(k * 7919) % 1500 for k in range(64)], 31),
-    "around what one block takes": (0, [2000] * 4 + [191, 1], 0),
+    "what one block takes": (0, [2000, 47, 0, 1], 0),
+    "more than one block takes": (0, [2000, 47, 1, 1], 0),
+    "sequences for more than one block": (3, [7] * 130, 0),
+    "tiles of 64": (0, [64, 63, 1, 65, 128, 127], 2000),
+    "around where tiles grow": (0, [60_000, 5535], 0),
+    "where tiles grow": (0, [60_000, 5536], 0),
+    "past where tiles grow": (1, [60_000, 100, 5437, 0], 0),
+    "many short in large tiles": (5, [1, 0, 3, 200, 7] * 400, 3),
 }
 
 
@@ -123,7 +130,7 @@ def preference(c, kind=0, smoothing=0.0, margin=0.0, beta=0.1, average=False, re
     dnll = fresh(c.T)
     if dloss is not None:
         z.zero_preference_grad(c.targets, c.offsets, slope, counts, dloss, dnll, average=average,
-                               dev_status=status, stream=stream)
+                               stream=stream)
     return loss, slope, ratios, counts, dnll
 
 
@@ -239,12 +246,12 @@ def policy(c, old=True, ref=True, per_token=False, low=0.2, high=0.28, kl_coef=0
            dloss=None, status=None, stream=None):
     adv = c.per_token if per_token else c.advantages
     how = dict(per_token=per_token, clip_low=low, clip_high=high, kl_coef=kl_coef, average=average,
-               dev_status=status, stream=stream)
+               stream=stream)
     args = (c.nll, c.old if old else None, c.ref if ref else None, adv, c.targets, c.offsets)
     loss, kl = fresh(c.S), fresh(c.S)
     clipped, counts = fresh(c.S, torch.int32), fresh(c.S, torch.int32)
     z.zero_policy(*args, loss, kl, clipped, counts,
-                  scratch_of(z.zero_policy_scratch_bytes, c.T, c.S), **how)
+                  scratch_of(z.zero_policy_scratch_bytes, c.T, c.S), dev_status=status, **how)
     dnll = fresh(c.T)
     if dloss is not None:
         z.zero_policy_grad(*args, counts, dloss, dnll, **how)
@@ -404,9 +411,10 @@ def test_bad_offsets_are_reported(bad, dtype):
     c.advantages = torch.ones(4, device="cuda")
     c.offsets = torch.tensor([min(b, 2 ** 31 - 1) for b in bad] if dtype == torch.int32 else bad,
                              dtype=dtype, device="cuda")
+    dloss = {preference: torch.ones(2, device="cuda"), policy: torch.ones(4, device="cuda")}
     for call in (preference, policy):
         status = torch.zeros(1, dtype=torch.int32, device="cuda")
-        call(c, status=status)
+        call(c, status=status, dloss=dloss[call])
         assert status.item() == z.ZERO_DEV_BAD_OFFSETS
         call(c)                                             # nobody asks
 

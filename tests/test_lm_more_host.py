@@ -33,7 +33,7 @@ PREF = Call("zero_preference", dict(
     counts=at(7), scratch=at(8), size=BIG, status=None, stream=None))
 PREF_GRAD = Call("zero_preference_grad", dict(
     targets=at(0), width=4, T=50, offsets=at(1), offset_width=4, P=3, average=0, slope=at(2),
-    counts=at(3), dloss=at(4), dnll=at(5), status=None, stream=None))
+    counts=at(3), dloss=at(4), dnll=at(5), stream=None))
 POLICY = Call("zero_policy", dict(
     nll=at(0), old_nll=at(1), ref_nll=at(2), advantages=at(3), per_token=0, targets=at(4), width=8,
     T=50, offsets=at(5), offset_width=4, S=3, clip_low=0.2, clip_high=0.2, kl_coef=0.1, average=1,
@@ -42,7 +42,7 @@ POLICY = Call("zero_policy", dict(
 POLICY_GRAD = Call("zero_policy_grad", dict(
     nll=at(0), old_nll=at(1), ref_nll=at(2), advantages=at(3), per_token=1, targets=at(4), width=8,
     T=50, offsets=at(5), offset_width=8, S=3, clip_low=0.2, clip_high=0.2, kl_coef=0.1, average=0,
-    counts=at(6), dloss=at(7), dnll=at(8), status=None, stream=None))
+    counts=at(6), dloss=at(7), dnll=at(8), stream=None))
 NORMS, LOSSES = (LN, LN_GRAD), (PREF, PREF_GRAD, POLICY, POLICY_GRAD)
 ALL = NORMS + LOSSES
 OPTIONAL = {"res", "sum", "dsum", "weight", "bias", "dweight", "dbias", "old_nll"}
@@ -284,11 +284,11 @@ CALLS = {
     "layer_norm_grad": (M, M, PER, PER, ROW, M, ROW, ROW, SCRATCH, M, None),
     "preference": (PER, PER, IDS, OFF, PAIR, PAIR, SEQ, COUNT, SCRATCH, 0, 0.1, 0.0, 0.0, True,
                    WORD, None),
-    "preference_grad": (IDS, OFF, PAIR, COUNT, PAIR, PER, True, WORD, None),
+    "preference_grad": (IDS, OFF, PAIR, COUNT, PAIR, PER, True, None),
     "policy": (PER, PER, PER, SEQ, IDS, OFF, SEQ, SEQ, COUNT, COUNT, SCRATCH, False, 0.2, 0.2, 0.1,
                True, WORD, None),
     "policy_grad": (PER, PER, PER, SEQ, IDS, OFF, COUNT, SEQ, PER, False, 0.2, 0.2, 0.1, True,
-                    WORD, None),
+                    None),
 }
 
 

@@ -206,11 +206,11 @@ def lib():
         L.zero_preference_scratch_bytes.argtypes = [i64, i64]
         L.zero_preference.argtypes = [vp, vp, vp, i32, i64, vp, i32, i64, i32, f64, f64, f64, i32,
                                       vp, vp, vp, vp, vp, i64, vp, vp]
-        L.zero_preference_grad.argtypes = [vp, i32, i64, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp]
+        L.zero_preference_grad.argtypes = [vp, i32, i64, vp, i32, i64, i32, vp, vp, vp, vp, vp]
         L.zero_policy_scratch_bytes.argtypes = [i64, i64]
         policy = [vp, vp, vp, vp, i32, vp, i32, i64, vp, i32, i64, f64, f64, f64, i32]
         L.zero_policy.argtypes = policy + [vp, vp, vp, vp, vp, i64, vp, vp]
-        L.zero_policy_grad.argtypes = policy + [vp, vp, vp, vp, vp]
+        L.zero_policy_grad.argtypes = policy + [vp, vp, vp, vp]
         L.zero_grad_norm_scratch_bytes.argtypes = [i32]
         L.zero_grad_norm.argtypes = [vp, i32, vp, vp, vp, i64, vp, vp]
         L.zero_grad_clip.argtypes = [vp, vp, i32, vp, f32, vp]

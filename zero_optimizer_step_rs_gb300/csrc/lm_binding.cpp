@@ -531,20 +531,19 @@ PyObject* py_preference(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
-// targets, offsets, slope, counts, dloss, dnll, average, dev_status, stream
+// targets, offsets, slope, counts, dloss, dnll, average, stream
 PyObject* py_preference_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<9>(n, lib.preference_grad, [&](Call& c) {
+    return guarded<8>(n, lib.preference_grad, [&](Call& c) {
         const Ids t = ids(c, a[0], "targets"), f = offsets(c, a[1]);
         const int64_t P = pairs(f);
         const auto* slope = dense<float>(c, a[2], at::kFloat, P, -1, "slope");
         const auto* counts = dense<int32_t>(c, a[3], at::kInt, 2 * P, -1, "counts");
         const auto* dloss = dense<float>(c, a[4], at::kFloat, P, -1, "dloss");
         auto* dnll = dense<float>(c, a[5], at::kFloat, t.n, -1, "dnll");
-        int32_t* word = status(c, a[7]);
         const int32_t average = truth(a[6]);
         return lib.preference_grad(t.p, t.bytes, t.n, f.p, f.bytes, P, average, slope, counts,
-                                   dloss, dnll, word, stream(c, a[8]));
+                                   dloss, dnll, stream(c, a[7]));
     });
 }
 
@@ -591,19 +590,18 @@ PyObject* py_policy(PyObject*, PyObject* const* a, Py_ssize_t n)
 }
 
 // nll, old_nll, ref_nll, advantages, targets, offsets, counts, dloss, dnll, per_token,
-// clip_low, clip_high, kl_coef, average, dev_status, stream
+// clip_low, clip_high, kl_coef, average, stream
 PyObject* py_policy_grad(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return guarded<16>(n, lib.policy_grad, [&](Call& c) {
+    return guarded<15>(n, lib.policy_grad, [&](Call& c) {
         const Policy p = policy(c, a, a[9]);
         const auto* counts = dense<int32_t>(c, a[6], at::kInt, p.S, -1, "counts");
         const auto* dloss = dense<float>(c, a[7], at::kFloat, p.S, -1, "dloss");
         auto* dnll = dense<float>(c, a[8], at::kFloat, p.t.n, -1, "dnll");
-        int32_t* word = status(c, a[14]);
         const int32_t average = truth(a[13]);
         return lib.policy_grad(p.nll, p.old, p.ref, p.adv, p.per_token, p.t.p, p.t.bytes, p.t.n,
                                p.f.p, p.f.bytes, p.S, real64(a[10]), real64(a[11]), real64(a[12]),
-                               average, counts, dloss, dnll, word, stream(c, a[15]));
+                               average, counts, dloss, dnll, stream(c, a[14]));
     });
 }
 

@@ -293,10 +293,23 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant
                            : type == ZERO_TYPE_FP16
                                ? sum_squares<ZERO_TYPE_FP16>(p, numel, head, lo, hi)
                                : sum_squares<ZERO_TYPE_FP32>(p, numel, head, lo, hi);
+        if (stop == end) pdl_let_in();
         if (threadIdx.x == 0) a.parts[blockIdx.x + i] = sum;
         tile = stop;
         while (i + 1 < a.count && a.e[i + 1].tile <= tile) ++i;
     }
+}
+
+// The root of a sum of squares, rounded to fp32.  A 64-bit root takes about 2 us here; the
+// sum's fraction in [1, 4) rounded to fp32 is off by 2^-24 of itself, half of which is
+// left in the root, beside the root's own rounding.
+__device__ __forceinline__ float root(double s)
+{
+    if (!(s > 0.0) || s > 1.7e308) return (float)s;      // 0, Inf, NaN
+    // (squares of fp32 values, the smallest 2^-298: no subnormal number)
+    const int power = ((int)(__double2hiint(s) >> 20) - 1023) & ~1;
+    const float f = (float)__hiloint2double(__double2hiint(s) - power * (1 << 20), __double2loint(s));
+    return ldexpf(sqrtf(f), power / 2);
 }
 
 // The tensors' sums of squares and that of all of them, in order.
@@ -316,7 +329,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_grad_norm_join(const __grid_co
         s = warp_sum64(s);
         if (lane == 0) {
             sums[i] = s;
-            if (a.norms) a.norms[i] = (float)sqrt(s);
+            if (a.norms) a.norms[i] = root(s);
         }
     }
     __syncthreads();
@@ -330,7 +343,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_grad_norm_join(const __grid_co
         *a.total = s;
         return;
     }
-    const float norm = (float)sqrt(s);
+    const float norm = root(s);
     a.norm[0] = norm;
     if (a.status && !(norm <= 3.402823466e38f)) atomicOr(a.status, ZERO_DEV_NONFINITE);
 }

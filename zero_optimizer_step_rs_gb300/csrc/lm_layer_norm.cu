@@ -40,7 +40,7 @@ constexpr uint32_t kOnes = 0x3F803F80u;              // two bf16 ones
 // which cancels nothing and needs one barrier where two passes over the row would
 // need two.
 template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128)
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, 1)
     k_layer_norm(const __grid_constant__ LayerNormArgs a)
 {
     constexpr int THREADS = TPR > 128 ? TPR : 128;
@@ -100,11 +100,11 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128)
             parts[threadIdx.x >> 5] = make_float4(s, mean, m2, (float)held);
         __syncthreads();
         float total = 0.0f;
-#pragma unroll
+#pragma unroll 8
         for (int k = 0; k < TPR / 32; ++k) total += parts[k].x;
         mean = total / (float)a.D;
         m2 = 0.0f;
-#pragma unroll
+#pragma unroll 8
         for (int k = 0; k < TPR / 32; ++k) {
             const float4 p = parts[k];
             const float d = p.y - mean;
@@ -159,31 +159,96 @@ __device__ __forceinline__ float2 row_sums(float x, float y, float2 (*slots)[32]
         const int warp = threadIdx.x >> 5;
         if ((threadIdx.x & 31) == 0) slots[slot][warp] = make_float2(x, y);
         __syncthreads();
-        x = y = 0.0f;
+        if constexpr (TPR > 256) {
+            const int lane = threadIdx.x & 31;
+            const float2 p = lane < TPR / 32 ? slots[slot][lane] : make_float2(0.0f, 0.0f);
+            x = warp_sum(p.x);
+            y = warp_sum(p.y);
+        } else {
+            x = y = 0.0f;
 #pragma unroll
-        for (int k = 0; k < TPR / 32; ++k) {
-            const float2 p = slots[slot][k];
-            x += p.x;
-            y += p.y;
+            for (int k = 0; k < TPR / 32; ++k) {
+                const float2 p = slots[slot][k];
+                x += p.x;
+                y += p.y;
+            }
         }
     }
     return make_float2(x, y);
 }
 
-// A row's threads walk over many rows and keep the sums of dw and db in
-// registers; a block's row groups are added in order at its end.
+// A copy of 16 bytes from global memory into the thread's own place in shared memory,
+// which only that thread reads: no barrier, only its own wait.
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// Rows that a thread has asked for ahead of the one it works on, plus that one.
 template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128)
+__host__ __device__ constexpr int grad_stages() { return TPR * NV <= 512 ? 3 : 2; }
+template <int TPR, int NV>
+__host__ __device__ constexpr int grad_smem()
+{
+    return grad_stages<TPR, NV>() * NV * (TPR > 128 ? TPR : 128) * 48;
+}
+
+// A row's threads walk over many rows and keep the sums of dw and db in
+// registers; a block's row groups are added in order at its end.  The rows ahead wait in
+// shared memory, where a thread finds its own vectors: with a barrier in the middle of each
+// row a block would otherwise have nothing in flight for half of the time.
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 128 ? 512 / TPR : 4)
     k_layer_norm_grad(const __grid_constant__ LayerNormGradArgs a)
 {
     constexpr int THREADS = TPR > 128 ? TPR : 128;
     constexpr int GROUPS = THREADS / TPR;
+    constexpr int S = grad_stages<TPR, NV>();
+    constexpr int N = NV * THREADS * 16, STAGE = 3 * N;      // a stage: dy, x, dsum
     pdl_enter();
+    extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 slots[2][32];
     const int group = threadIdx.x / TPR, lane = threadIdx.x % TPR;
     const int nv = a.D >> 3;
     const int64_t step = (int64_t)gridDim.x * GROUPS;
+    const int64_t first = (int64_t)blockIdx.x * GROUPS + group;
     const float inv = 1.0f / (float)a.D;
+
+    // where the row to ask for next lies; a thread past the row's end asks for
+    // nothing and keeps the zeros that its places start with
+    const uint16_t* p_d = a.dy + first * a.dy_ld + lane * 8;
+    const uint16_t* p_x = a.x + first * a.x_ld + lane * 8;
+    const uint16_t* p_s = a.dsum ? a.dsum + first * a.dsum_ld + lane * 8 : nullptr;
+    const int64_t d_step = step * a.dy_ld, x_step = step * a.x_ld, s_step = step * a.dsum_ld;
+    const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16;
+    auto ask = [&](bool in, uint32_t stage) {
+        if (in) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (lane + k * TPR >= nv) break;
+                const uint32_t at = mine + stage + k * THREADS * 16;
+                copy_async(at, p_d + k * TPR * 8);
+                copy_async(at + N, p_x + k * TPR * 8);
+                if (p_s) copy_async(at + 2 * N, p_s + k * TPR * 8);
+            }
+        }
+        p_d += d_step;
+        p_x += x_step;
+        if (p_s) p_s += s_step;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = threadIdx.x; i < S * STAGE / 16; i += THREADS)
+        reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+
     uint4 w4[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -191,31 +256,43 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128)
         if (a.w && lane + k * TPR < nv) w4[k] = ld16(a.w + (lane + k * TPR) * 8);
     }
     float dw[NV][8] = {}, db[NV][8] = {};
+    uint32_t stage = 0;                                   // offset of the row at hand
     int slot = 0;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) ask(first + s * step < a.T, s * STAGE);
+    float mean_next = 0.0f, rstd_next = 0.0f;
+    if (first < a.T) {
+        mean_next = a.mean[first];
+        rstd_next = a.rstd[first];
+    }
+    uint16_t* p_o = a.dx + first * a.dx_ld + lane * 8;
     // (barriers: where a row has more than a warp, the block has one row at a time)
-    for (int64_t t = (int64_t)blockIdx.x * GROUPS + group; t < a.T; t += step) {
-        const float mean = a.mean[t], rstd = a.rstd[t];
-        float u[NV][8], xh[NV][8], s1 = 0.0f, s2 = 0.0f;
+    for (int64_t t = first; t < a.T; t += step, p_o += step * a.dx_ld) {
+        const float mean = mean_next, rstd = rstd_next;
+        if (t + step < a.T) {
+            mean_next = a.mean[t + step];
+            rstd_next = a.rstd[t + step];
+        }
+        ask(t + (S - 1) * step < a.T,
+            stage == 0 ? (S - 1) * STAGE : stage - STAGE);
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
+        // xhat and dy * w are made twice, from what shared memory holds: keeping them
+        // would cost 16 registers a vector
+        const uint32_t here = mine + stage;
+        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR;
-            uint4 p = make_uint4(0, 0, 0, 0), q4 = p;
-            if (c < nv) {
-                p = ld16_stream(a.dy + t * a.dy_ld + c * 8);
-                q4 = ld16_stream(a.x + t * a.x_ld + c * 8);
-            }
-            float w[8];
-            bf_unpack8(p, u[k]);
-            bf_unpack8(q4, xh[k]);
+            float w[8], x[8], d[8];
             bf_unpack8(w4[k], w);
+            bf_unpack8(ld_shared(here + k * THREADS * 16), d);
+            bf_unpack8(ld_shared(here + k * THREADS * 16 + N), x);
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                xh[k][q] = (xh[k][q] - mean) * rstd;
-                db[k][q] += u[k][q];
-                dw[k][q] = fmaf(u[k][q], xh[k][q], dw[k][q]);
-                u[k][q] *= w[q];
-                s1 += u[k][q];
-                s2 = fmaf(u[k][q], xh[k][q], s2);
+                const float xh = (x[q] - mean) * rstd, u = d[q] * w[q];
+                db[k][q] += d[q];
+                dw[k][q] = fmaf(d[q], xh, dw[k][q]);
+                s1 += u;
+                s2 = fmaf(u, xh, s2);
             }
         }
         const float2 all = row_sums<TPR>(s1, s2, slots, slot);
@@ -223,16 +300,23 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128)
         const float c1 = all.x * inv, c2 = all.y * inv;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR;
-            if (c >= nv) break;
-            float s[8] = {};
-            if (a.dsum) bf_unpack8(ld16_stream(a.dsum + t * a.dsum_ld + c * 8), s);
+            if (lane + k * TPR >= nv) break;
+            float s[8] = {}, w[8], x[8], d[8];
+            bf_unpack8(w4[k], w);
+            bf_unpack8(ld_shared(here + k * THREADS * 16), d);
+            bf_unpack8(ld_shared(here + k * THREADS * 16 + N), x);
+            if (p_s) bf_unpack8(ld_shared(here + k * THREADS * 16 + 2 * N), s);
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                s[q] = fmaf(rstd, fmaf(-xh[k][q], c2, u[k][q] - c1), s[q]);
-            st16_stream(a.dx + t * a.dx_ld + c * 8, bf_pack8(s));
+            for (int q = 0; q < 8; ++q) {
+                const float xh = (x[q] - mean) * rstd;
+                s[q] = fmaf(rstd, fmaf(-xh, c2, fmaf(d[q], w[q], -c1)), s[q]);
+            }
+            st16_stream(p_o + k * TPR * 8, bf_pack8(s));
         }
+        stage = stage == (S - 1) * STAGE ? 0 : stage + STAGE;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    pdl_let_in();
     if (!a.parts) return;
     float* part = a.parts + (int64_t)blockIdx.x * 2 * a.D;
     if constexpr (GROUPS == 1) {
@@ -459,7 +543,7 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
     a.x_ld = x_ld;
     a.dx_ld = dx_ld;
     a.D = D;
-    auto run = [&](void (*kernel)(LayerNormGradArgs), int tpr, std::atomic<int>* per_sm) {
+    auto run = [&](void (*kernel)(LayerNormGradArgs), int tpr, int smem, std::atomic<int>* per_sm) {
         const int threads = tpr > 128 ? tpr : 128, groups = threads / tpr;
         // as many blocks as are resident at once: a second wave would be a short one
         int dev = 0;
@@ -467,19 +551,22 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
         int fit = per_sm[dev & 63].load(std::memory_order_relaxed);
         cudaError_t e = cudaSuccess;
         if (fit == 0) {
-            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, 0);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e == cudaSuccess)
+                e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem);
             if (e == cudaSuccess && fit > 0)
                 per_sm[dev & 63].store(fit, std::memory_order_relaxed);
         }
         a.blocks = (int)std::min<int64_t>({(T + groups - 1) / groups, (int64_t)grad_blocks(T),
                                            (int64_t)std::max(1, fit) * device_sms()});
-        if (e == cudaSuccess) e = launch(kernel, dim3((unsigned)a.blocks), threads, 0, st, a);
+        if (e == cudaSuccess) e = launch(kernel, dim3((unsigned)a.blocks), threads, smem, st, a);
         if (e == cudaSuccess && wanted)
             e = launch(k_layer_norm_join, dim3((unsigned)((2 * D + kJoinCols - 1) / kJoinCols)),
                        kJoinThreads, 0, st, a);
         return status_of(e);
     };
-#define GRAD_GO(tpr, nv) run(k_layer_norm_grad<tpr, nv>, tpr, grad_per_sm<tpr, nv>)
+#define GRAD_GO(tpr, nv) \
+    run(k_layer_norm_grad<tpr, nv>, tpr, grad_smem<tpr, nv>(), grad_per_sm<tpr, nv>)
     LAYER_NORM_FORMS(GRAD_GO);
 #undef GRAD_GO
 }

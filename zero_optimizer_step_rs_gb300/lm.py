@@ -193,10 +193,10 @@ def zero_preference(nll, ref_nll, targets, offsets, loss, slope, ratios, counts,
 
 
 def zero_preference_grad(targets, offsets, slope, counts, dloss, dnll, average: bool = False,
-                         dev_status=None, stream=None) -> None:
+                         stream=None) -> None:
     """dnll [T] from zero_preference's slope and counts (and its `average`) and the
     upstream gradient dloss [P] of each pair's loss."""
-    code = _lm.preference_grad(targets, offsets, slope, counts, dloss, dnll, average, dev_status,
+    code = _lm.preference_grad(targets, offsets, slope, counts, dloss, dnll, average,
                                _address(stream))
     if code:
         raise ZeroError(code, "zero_preference_grad")
@@ -224,12 +224,11 @@ def zero_policy(nll, old_nll, ref_nll, advantages, targets, offsets, loss, kl, c
 
 def zero_policy_grad(nll, old_nll, ref_nll, advantages, targets, offsets, counts, dloss, dnll,
                      per_token: bool = False, clip_low: float = 0.2, clip_high: float = 0.2,
-                     kl_coef: float = 0.0, average: bool = True, dev_status=None,
-                     stream=None) -> None:
+                     kl_coef: float = 0.0, average: bool = True, stream=None) -> None:
     """dnll [T] from zero_policy's arguments and counts, and the upstream gradient
     dloss [S] of each sequence's loss."""
     code = _lm.policy_grad(nll, old_nll, ref_nll, advantages, targets, offsets, counts, dloss,
-                           dnll, per_token, clip_low, clip_high, kl_coef, average, dev_status,
+                           dnll, per_token, clip_low, clip_high, kl_coef, average,
                            _address(stream))
     if code:
         raise ZeroError(code, "zero_policy_grad")
