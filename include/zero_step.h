@@ -772,7 +772,7 @@ zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld, const uint16
  * its losses hold (NaN and Inf included), and its dnll is 0.
  * S and P below 2^30, T below 2^31 - 1024.  Arrays of 4-byte elements need 4-byte
  * alignment only, ids and offsets their own size.  Sums over a sequence have fp32 terms
- * and partial sums of at most 256 tokens, joined in 64 bits.  S = 0 is allowed.
+ * and partial sums of at most 256 tokens, which are joined without loss (as two fp32 numbers).  S = 0 is allowed.
  * average = 1 divides a sequence's sum by the number of its tokens that count
  * (0 where none does).
  * ---------------------------------------------------------------------- */

@@ -24,7 +24,7 @@ using namespace lm;
 constexpr int kThreads = 256;
 constexpr int kTile = 8192;                          // elements
 constexpr int kMaxBlocks = 1216;                     // 8 for each of 152 SMs
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 128;
 constexpr int kNoVectors = 255;                      // a head: input and output never have one together
 constexpr int64_t kMaxNumel = 1ll << 40, kMaxTotal = 1ll << 43;
 
@@ -50,8 +50,10 @@ struct ClipArgs {
     int32_t* status;
     int64_t tiles;
     int32_t count, per_block;
+    int32_t slots;                                   // that the blocks fill
     int32_t first, last;                             // of the call's launches
     int32_t in_place;
+    int32_t last_full;                               // the last tensor that is not empty
     float max_norm;
     Entry e[N];
 };
@@ -184,18 +186,18 @@ __device__ __forceinline__ double warp_sum64(double x)
     return x;
 }
 
-// A thread's sum in 32 bits over the block's threads in 64; in every thread.
-__device__ __forceinline__ double block_sum(float x)
+// The sum over the block's threads, in every thread.
+__device__ __forceinline__ float block_sum(float x)
 {
-    __shared__ double slots[kThreads / 32];
-    const double w = warp_sum64((double)x);
+    __shared__ float slots[kThreads / 32];
+    x = warp_sum(x);
     __syncthreads();                                 // the slots may be in use still
-    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = w;
+    if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = x;
     __syncthreads();
-    double s = 0.0;
+    x = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) s += slots[k];
-    return s;
+    for (int k = 0; k < kThreads / 32; ++k) x += slots[k];
+    return x;
 }
 
 __device__ __forceinline__ uint32_t block_max(uint32_t x)
@@ -240,7 +242,7 @@ __device__ __noinline__ double scaled_sum(const void* p, int64_t numel, int head
         });
         s += part;
     }
-    return ldexp(block_sum(s), 2 * power);
+    return ldexp((double)block_sum(s), 2 * power);
 }
 
 template <int TYPE>
@@ -255,9 +257,9 @@ __device__ __forceinline__ double sum_squares(const void* p, int64_t numel, int 
         for_elements<TYPE>(p, numel, head, t, [&](float x) { part = fmaf(x, x, part); });
         s += part;
     }
-    const double sum = block_sum(s);
+    s = block_sum(s);
     // (each of the sum's terms was off by at most 2^-150: under 2^-24 of it from here up)
-    if (sum >= 0x1p-80 && sum <= 0x1p120) return sum;
+    if (s >= 0x1p-80f && s <= 0x1p120f) return (double)s;
     return scaled_sum<TYPE>(p, numel, head, lo, hi);
 }
 
@@ -282,6 +284,9 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant
     int64_t tile = (int64_t)blockIdx.x * a.per_block;
     const int64_t end = min(tile + a.per_block, a.tiles);
     int i = tensor_of(a, tile);
+    // Slots that no pair has, beside empty tensors and where a block and a tensor end together,
+    // become 0 by the block that comes after them: the sum of all slots is that of all tensors.
+    int slot = blockIdx.x == 0 ? 0 : (int)blockIdx.x + tensor_of(a, tile - 1);
     while (tile < end) {
         const int64_t first = a.e[i].tile, numel = a.e[i].numel;
         const void* p = a.e[i].p;
@@ -294,7 +299,10 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant
                                ? sum_squares<ZERO_TYPE_FP16>(p, numel, head, lo, hi)
                                : sum_squares<ZERO_TYPE_FP32>(p, numel, head, lo, hi);
         if (stop == end) pdl_let_in();
-        if (threadIdx.x == 0) a.parts[blockIdx.x + i] = sum;
+        if (threadIdx.x == 0) {
+            for (; slot < (int)blockIdx.x + i; ++slot) a.parts[slot] = 0.0;
+            a.parts[slot++] = sum;
+        }
         tile = stop;
         while (i + 1 < a.count && a.e[i + 1].tile <= tile) ++i;
     }
@@ -312,33 +320,37 @@ __device__ __forceinline__ float root(double s)
     return ldexpf(sqrtf(f), power / 2);
 }
 
-// The tensors' sums of squares and that of all of them, in order.
+// The tensors' norms, a warp each, and by the last block that of all of them.
 template <int N>
 __global__ void __launch_bounds__(kJoinThreads) k_grad_norm_join(const __grid_constant__ ClipArgs<N> a)
 {
     pdl_enter();
-    __shared__ double sums[N];
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < a.count; i += kJoinThreads / 32) {
-        const int64_t from = a.e[i].tile, to = i + 1 < a.count ? (int64_t)a.e[i + 1].tile : a.tiles;
+    if (blockIdx.x + 1 < gridDim.x) {
+        const int i = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+        if (i >= a.count) return;
+        const int from = a.e[i].tile, to = i + 1 < a.count ? a.e[i + 1].tile : (int)a.tiles;
         double s = 0.0;
         if (from < to) {
-            const int64_t first = from / a.per_block, last = (to - 1) / a.per_block;
-            for (int64_t b = first + lane; b <= last; b += 32) s += a.parts[b + i];
+            const int first = from / a.per_block, last = (to - 1) / a.per_block;
+#pragma unroll 4
+            for (int b = first + lane; b <= last; b += 32) s += a.parts[b + i];
         }
         s = warp_sum64(s);
-        if (lane == 0) {
-            sums[i] = s;
-            if (a.norms) a.norms[i] = root(s);
-        }
+        if (lane == 0) a.norms[i] = root(s);
+        return;
     }
-    __syncthreads();
-    if (threadIdx.x >= 32) return;
+    __shared__ double sums[kJoinThreads / 32];
     double s = 0.0;
-    for (int i = lane; i < a.count; i += 32) s += sums[i];
+#pragma unroll 4
+    for (int k = threadIdx.x; k < a.slots; k += kJoinThreads) s += a.parts[k];
     s = warp_sum64(s);
-    if (lane) return;
-    if (!a.first) s += *a.total;
+    if (lane == 0) sums[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x) return;
+    s = a.first ? 0.0 : *a.total;
+#pragma unroll
+    for (int k = 0; k < kJoinThreads / 32; ++k) s += sums[k];
     if (!a.last) {
         *a.total = s;
         return;
@@ -396,10 +408,15 @@ template <int N>
 __global__ void __launch_bounds__(kThreads, 4) k_grad_clip(const __grid_constant__ ClipArgs<N> a)
 {
     pdl_enter();
-    const double coef64 = (double)a.max_norm / ((double)*a.norm_in + 1e-6);
-    const bool clip = coef64 < 1.0;
-    const float coef = clip ? (float)coef64 : 1.0f;
-    if (!clip && a.in_place) return;
+    // (one warp: the eight of a block take 64-bit operations in turn)
+    __shared__ float the_coef;
+    if (threadIdx.x < 32) {
+        const double coef = (double)a.max_norm / ((double)*a.norm_in + 1e-6);
+        the_coef = coef < 1.0 ? (float)coef : 1.0f;      // a norm that is NaN clips nothing
+    }
+    __syncthreads();
+    const float coef = the_coef;
+    if (coef == 1.0f && a.in_place) return;
     const int64_t begin = (int64_t)blockIdx.x * a.per_block;
     int64_t tile = min(begin + a.per_block, a.tiles) - 1;
     // backwards: the end of a block's run is what the norm's pass has read last
@@ -513,6 +530,7 @@ cudaError_t for_launches(const zero_tensor* t, const zero_tensor* outs, int32_t 
     for (int32_t at = 0; at < count; at += N) {
         a.count = std::min(count - at, N);
         a.tiles = 0;
+        a.last_full = 0;
         for (int32_t i = 0; i < a.count; ++i) {
             const zero_tensor& x = t[at + i];
             Entry& e = a.e[i];
@@ -525,6 +543,7 @@ cudaError_t for_launches(const zero_tensor* t, const zero_tensor* outs, int32_t 
             e.head = x.numel ? head_of(x, outs ? &outs[at + i] : nullptr) : 0;
             e.pad = 0;
             const int64_t before = e.head == kNoVectors ? 0 : e.head;
+            if (x.numel) a.last_full = i;
             if (x.numel) a.tiles += std::max<int64_t>(1, (x.numel - before + kTile - 1) / kTile);
         }
         a.per_block = (int32_t)std::max<int64_t>(1, (a.tiles + kMaxBlocks - 1) / kMaxBlocks);
@@ -547,8 +566,12 @@ cudaError_t norm_launches(const zero_tensor* t, int32_t count, float* norm, floa
         a.first = at == 0;
         a.last = at + N >= count;
         cudaError_t e = cudaSuccess;
+        // (what ends with empty tensors leaves their slots to nobody: they are not summed)
+        a.slots = blocks ? (int32_t)blocks + a.last_full : 0;
+        const unsigned join = norms ? (unsigned)((a.count + kJoinThreads / 32 - 1) / (kJoinThreads / 32)) : 0;
         if (blocks) e = launch(k_grad_norm<N>, dim3(blocks), kThreads, 0, st, a);
-        if (e == cudaSuccess) e = launch(k_grad_norm_join<N>, dim3(1), kJoinThreads, 0, st, a);
+        if (e == cudaSuccess)
+            e = launch(k_grad_norm_join<N>, dim3(join + 1), kJoinThreads, 0, st, a);
         return e;
     });
 }

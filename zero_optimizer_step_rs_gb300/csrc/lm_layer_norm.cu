@@ -352,44 +352,53 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 1
 }
 
 // dw and db = the blocks' parts, added in an order that depends on their number only:
-// 32 of the 2 D columns a block, 128 shares of the rows, then the shares in a tree.
+// 32 of the 2 D columns a block, 128 shares of the rows; four shares lie in a warp's
+// lanes, the 32 warps' sums are added by the first one.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinCols = 32;
 constexpr int kJoinShares = kJoinThreads / (kJoinCols / 4);
+
+__device__ __forceinline__ float4 add4(const float4& p, const float4& q)
+{
+    return make_float4(p.x + q.x, p.y + q.y, p.z + q.z, p.w + q.w);
+}
+// Over the lanes that have the same columns.
+__device__ __forceinline__ float4 share_sum(float4 s)
+{
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1)
+        s = add4(s, make_float4(__shfl_xor_sync(0xFFFFFFFFu, s.x, o),
+                                __shfl_xor_sync(0xFFFFFFFFu, s.y, o),
+                                __shfl_xor_sync(0xFFFFFFFFu, s.z, o),
+                                __shfl_xor_sync(0xFFFFFFFFu, s.w, o)));
+    return s;
+}
 
 __global__ void __launch_bounds__(kJoinThreads)
     k_layer_norm_join(const __grid_constant__ LayerNormGradArgs a)
 {
     pdl_enter();
-    __shared__ float4 share[kJoinShares][kJoinCols / 4];
+    __shared__ float4 sums[kJoinThreads / 32][kJoinCols / 4];
     const int cv = threadIdx.x % (kJoinCols / 4), sh = threadIdx.x / (kJoinCols / 4);
     const int col = blockIdx.x * kJoinCols + cv * 4;
     float4 s = make_float4(0, 0, 0, 0);
     if (col < 2 * a.D)
 #pragma unroll 4
-        for (int r = sh; r < a.blocks; r += kJoinShares) {
-            const float4 x =
-                __ldcs(reinterpret_cast<const float4*>(a.parts + (int64_t)r * 2 * a.D + col));
-            s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
-        }
-    share[sh][cv] = s;
+        for (int r = sh; r < a.blocks; r += kJoinShares)
+            s = add4(s, __ldcs(reinterpret_cast<const float4*>(a.parts + (int64_t)r * 2 * a.D + col)));
+    s = share_sum(s);
+    if ((threadIdx.x & 31) < kJoinCols / 4) sums[threadIdx.x >> 5][cv] = s;
     __syncthreads();
+    if (threadIdx.x >= 32) return;
+    s = make_float4(0, 0, 0, 0);
 #pragma unroll
-    for (int o = kJoinShares / 2; o > 0; o >>= 1) {
-        if (sh < o) {
-            float4 p = share[sh][cv];
-            const float4 q = share[sh + o][cv];
-            p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
-            share[sh][cv] = p;
-        }
-        __syncthreads();
-    }
+    for (int k = 0; k < 8; ++k) s = add4(s, sums[sh * 8 + k][cv]);
+    s = share_sum(s);
     if (sh == 0 && col < 2 * a.D) {
-        const float4 p = share[0][cv];
         uint16_t* to = col < a.D ? a.dw : a.db;            // 4 columns never straddle the two
         if (to)
             *reinterpret_cast<uint2*>(to + (col < a.D ? col : col - a.D)) =
-                make_uint2(bf_pack(p.x, p.y), bf_pack(p.z, p.w));
+                make_uint2(bf_pack(s.x, s.y), bf_pack(s.z, s.w));
     }
 }
 

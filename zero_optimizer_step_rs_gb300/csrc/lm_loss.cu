@@ -8,8 +8,8 @@
 // sequences' lengths are.  A tile meets the sequences s0, s0 + 1, ...; going
 // along the tokens either the tile or the sequence steps on, so that tile + s is a
 // slot of its own for every pair that meets, the slots of a sequence lie one behind
-// the other, and no slot needs clearing.  The sequence's slots are then joined in 64
-// bits, in order of the lanes: no atomics, the same bits in every call.
+// the other, and no slot needs clearing.  The sequence's slots are then joined, with what
+// the additions round away kept beside the sum: no atomics, the same bits in every call.
 #include "lm_common.cuh"
 
 #include <math.h>
@@ -18,14 +18,17 @@ namespace {
 
 using namespace lm;
 
-// Tokens of a lane: a warp with 8 takes 1500 instructions one after the other, which is 7 us
-// of a call of few tokens; one with 2 does less work per instruction (the search for its
-// sequences, the sums' halvings), which costs where there are many.
-constexpr int kFewItems = 2, kManyItems = 8;
-constexpr int64_t kFew = 1 << 16;                    // tokens from which on a lane takes 8
+// Tokens of a lane.  A warp with 8 of the policy's takes 1500 instructions one after the other,
+// which is 7 us of a call of few tokens; with 1 it does less work per instruction (the
+// search for its sequences, the sums' halvings), which costs where there are many: 2^20 tokens
+// of the policy 16.4 us with 4 and 17.4 with 8, of preferences 12.0 and 10.3; 30000 of the policy
+// 6.8 us with 1 and 7.5 with 2.
+constexpr int kFewItems = 1;
+constexpr int many_items(int kind) { return kind == 0 ? 8 : 4; }
+constexpr int64_t kFew = 1 << 16;                    // tokens from which on a lane takes several
 constexpr int kThreads = 128;
-constexpr int kAloneThreads = 1024;                  // of the one block that does it all
-constexpr int64_t kAloneResults = 64;
+constexpr int kWideThreads = 512;                    // of a block that joins one result's parts
+constexpr int64_t kWideTiles = 128;                  // parts a result from which on it does
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
 template <int ITEMS>
@@ -89,45 +92,29 @@ __device__ __forceinline__ int64_t offsets_up_to(const LossArgs& a, int64_t t, i
     return lo;
 }
 
-// exp(d) - d - 1 and exp(d) - 1.  Near 0 these cancel, so there they are the
-// exponential's series from its third term on; at |d| <= 1 the first term left out, d^13 / 13!,
-// is under 2^-30 of the sum.
-struct Drift {
-    float k, e;
-};
-__device__ __forceinline__ Drift drift(float d)
+// exp(d) - d - 1 for |d| <= 1, where the three cancel: the exponential's series from its
+// third term on.  The first term left out, d^13 / 13!, is under 2^-30 of the sum.
+__device__ __forceinline__ float drift_series(float d)
 {
-    if (fabsf(d) <= 1.0f) {
-        float p = 1.0f / 479001600.0f;
-        p = fmaf(p, d, 1.0f / 39916800.0f);
-        p = fmaf(p, d, 1.0f / 3628800.0f);
-        p = fmaf(p, d, 1.0f / 362880.0f);
-        p = fmaf(p, d, 1.0f / 40320.0f);
-        p = fmaf(p, d, 1.0f / 5040.0f);
-        p = fmaf(p, d, 1.0f / 720.0f);
-        p = fmaf(p, d, 1.0f / 120.0f);
-        p = fmaf(p, d, 1.0f / 24.0f);
-        p = fmaf(p, d, 1.0f / 6.0f);
-        p = fmaf(p, d, 0.5f);
-        const float k = p * d * d;
-        return {k, d + k};
-    }
-    const float e = expf(d) - 1.0f;
-    return {e - d, e};
+    float p = 1.0f / 479001600.0f;
+    p = fmaf(p, d, 1.0f / 39916800.0f);
+    p = fmaf(p, d, 1.0f / 3628800.0f);
+    p = fmaf(p, d, 1.0f / 362880.0f);
+    p = fmaf(p, d, 1.0f / 40320.0f);
+    p = fmaf(p, d, 1.0f / 5040.0f);
+    p = fmaf(p, d, 1.0f / 720.0f);
+    p = fmaf(p, d, 1.0f / 120.0f);
+    p = fmaf(p, d, 1.0f / 24.0f);
+    p = fmaf(p, d, 1.0f / 6.0f);
+    p = fmaf(p, d, 0.5f);
+    return p * d * d;
 }
 
-// Where old - nll, as exact numbers, lies beside the bounds' logarithms: bit 0 above the
-// upper, bit 1 below the lower one.  Rounding keeps the order, so only a difference that
-// rounds to the same fp32 value as the logarithm needs what both roundings lost: the
-// difference's by Knuth's two-sum.  (In 64 bits, and be it for those few tokens alone, the
-// comparisons took 6 of 12 us of a call: the compiler makes them for all.)
-__device__ __forceinline__ unsigned beyond(const LossArgs& a, float old, float nll, float change)
+// What old - nll lost in its rounding (Knuth's two-sum).
+__device__ __forceinline__ float lost(float old, float nll, float change)
 {
     const float back = __fsub_rn(change, old);
-    const float lost = __fsub_rn(__fsub_rn(old, __fsub_rn(change, back)), __fadd_rn(nll, back));
-    const bool high = change > a.edge_hi || (change == a.edge_hi && lost > a.rest_hi);
-    const bool low = change < a.edge_lo || (change == a.edge_lo && lost < a.rest_lo);
-    return (unsigned)high | (unsigned)low << 1;
+    return __fsub_rn(__fsub_rn(old, __fsub_rn(change, back)), __fadd_rn(nll, back));
 }
 
 // A lane's tokens of a tile: t = base + 32 j + lane.
@@ -137,28 +124,99 @@ struct Tokens {
     unsigned live;                                   // bit j: token j counts
 };
 
-template <Kind K, bool GRAD, int ITEMS>
-__device__ __forceinline__ void load_tokens(const LossArgs& a, int64_t base, int lane,
-                                            Tokens<ITEMS>& x)
+// FULL: the whole tile lies below T.
+template <Kind K, bool GRAD, int ITEMS, bool FULL>
+__device__ __forceinline__ void load_some(const LossArgs& a, int64_t base, int lane,
+                                          Tokens<ITEMS>& x)
 {
+    const int64_t at = base + lane;
+    const int n = FULL ? kTile<ITEMS> : (int)(a.T - base) - lane;    // tokens from `at` on
     int64_t id[ITEMS];
+    if (a.target_bytes == 8) {
+        const auto* p = static_cast<const long long*>(a.targets) + at;
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-        const int64_t t = base + j * 32 + lane;
-        const bool in = t < a.T;
-        id[j] = in ? token_at(a.targets, a.target_bytes, t) : -1;
-        if (K == kPolicy || !GRAD) {
-            x.nll[j] = in ? a.nll[t] : 0.0f;
-            x.ref[j] = in && a.ref ? a.ref[t] : 0.0f;
-        }
-        if (K == kPolicy) {
-            x.old[j] = in && a.old ? a.old[t] : x.nll[j];
-            x.adv[j] = in && a.per_token ? a.adv[t] : 0.0f;
-        }
+        for (int j = 0; j < ITEMS; ++j) id[j] = FULL || j * 32 < n ? p[j * 32] : -1;
+    } else {
+        const auto* p = static_cast<const int*>(a.targets) + at;
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) id[j] = FULL || j * 32 < n ? p[j * 32] : -1;
+    }
+    const auto values = [&](float (&v)[ITEMS], const float* p) {
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) v[j] = p && (FULL || j * 32 < n) ? p[at + j * 32] : 0.0f;
+    };
+    if (K == kPolicy || !GRAD) {
+        values(x.nll, a.nll);
+        values(x.ref, a.ref);
+    }
+    if (K == kPolicy) {
+        values(x.old, a.old);
+        values(x.adv, a.per_token ? a.adv : nullptr);
     }
     x.live = 0;
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) x.live |= (id[j] >= 0 ? 1u : 0u) << j;
+}
+
+template <Kind K, bool GRAD, int ITEMS>
+__device__ __forceinline__ void load_tokens(const LossArgs& a, int64_t base, int lane,
+                                            Tokens<ITEMS>& x)
+{
+    if (base + kTile<ITEMS> <= a.T) load_some<K, GRAD, ITEMS, true>(a, base, lane, x);
+    else load_some<K, GRAD, ITEMS, false>(a, base, lane, x);
+}
+
+// The policy's tokens by themselves: the ratios r, exp(d) - d - 1 or (GRAD) exp(d) - 1 of
+// d = nll - ref, and for each token two bits: r above the upper bound, r below the lower one.
+//
+// The bounds are compared as logarithms, old - nll with log(bound), and as exact numbers:
+// rounding keeps the order, so only a difference that rounds to the same fp32 value as the logarithm
+// needs what both roundings lost.  Such tokens, and those with |d| > 1, are few: the warp
+// looks for them once and takes them by themselves.  (Made for every token these took a third of
+// the time; the comparison in 64 bits, half.)
+template <bool GRAD, int ITEMS>
+__device__ __forceinline__ unsigned policy_terms(const LossArgs& a, const Tokens<ITEMS>& x,
+                                                 float (&r)[ITEMS], float (&kk)[ITEMS])
+{
+    unsigned side = 0;
+    bool tie = false, far = false;
+    const bool drifts = GRAD ? a.kl_coef != 0.0f : a.ref != nullptr;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        const float change = a.old ? x.old[j] - x.nll[j] : 0.0f;
+        r[j] = expf(change);
+        side |= (unsigned)(change > a.edge_hi) << 2 * j | (unsigned)(change < a.edge_lo) << (2 * j + 1);
+        tie |= change == a.edge_hi || change == a.edge_lo;
+        kk[j] = 0.0f;
+        if (drifts) {
+            const float d = x.nll[j] - x.ref[j], k = drift_series(d);
+            kk[j] = GRAD ? d + k : k;
+            far |= !(fabsf(d) <= 1.0f);
+        }
+    }
+    if (__any_sync(kAll, tie) && a.old) {
+#pragma unroll
+        for (int j = 0; j < ITEMS; ++j) {
+            const float change = x.old[j] - x.nll[j], rest = lost(x.old[j], x.nll[j], change);
+            if (change == a.edge_hi && rest > a.rest_hi) side |= 1u << 2 * j;
+            if (change == a.edge_lo && rest < a.rest_lo) side |= 2u << 2 * j;
+        }
+    }
+    if (__any_sync(kAll, far)) {
+#pragma unroll 1
+        for (int j = 0; j < ITEMS; ++j) {
+            float d = 0.0f;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                if (i == j) d = x.nll[i] - x.ref[i];
+            if (!__any_sync(kAll, !(fabsf(d) <= 1.0f))) continue;
+            const float e = expf(d) - 1.0f, k = GRAD ? e : e - d;
+#pragma unroll
+            for (int i = 0; i < ITEMS; ++i)
+                if (i == j && !(fabsf(d) <= 1.0f)) kk[i] = k;
+        }
+    }
+    return side;
 }
 
 // Calls f(s, lo, hi, of(s)) for every sequence from s0 on that the tile at base meets, with the
@@ -194,17 +252,12 @@ __device__ __forceinline__ void tile_parts(const LossArgs& a, int64_t tile, int 
     load_tokens<K, false, ITEMS>(a, base, lane, x);
     const int64_t s0 = offsets_up_to(a, base, lane) - 1;     // while the tokens are on their way
     float v[ITEMS], kk[ITEMS];
-    unsigned side = 0;                               // beyond(), two bits a token
+    unsigned side = 0;
+    if (K == kPolicy) {
+        side = policy_terms<false>(a, x, v, kk);
+    } else {
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-        if (K == kPreference) {
-            v[j] = x.ref[j] - x.nll[j];
-        } else {
-            const float change = x.old[j] - x.nll[j];
-            v[j] = expf(change);
-            kk[j] = a.ref ? drift(x.nll[j] - x.ref[j]).k : 0.0f;
-            side |= beyond(a, x.old[j], x.nll[j], change) << 2 * j;
-        }
+        for (int j = 0; j < ITEMS; ++j) v[j] = x.ref[j] - x.nll[j];
     }
     const auto about = [&](int64_t s) {
         return make_float2(K == kPolicy && !a.per_token ? a.adv[s] : 0.0f, 0.0f);
@@ -238,49 +291,88 @@ __device__ __forceinline__ void tile_parts(const LossArgs& a, int64_t tile, int 
     });
 }
 
+// A sum in two parts, of which the second holds what the roundings lost (up to its own).
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair plus(Pair x, float y)
+{
+    const float s = x.hi + y, back = s - x.hi;
+    return {s, x.lo + ((x.hi - (s - back)) + (y - back))};
+}
+__device__ __forceinline__ Pair warp_pair(Pair x)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float hi = __shfl_xor_sync(kAll, x.hi, o), lo = __shfl_xor_sync(kAll, x.lo, o);
+        // both lanes of a pair add the same two numbers in the same order
+        const bool upper = threadIdx.x & o;
+        x = plus(Pair{upper ? hi : x.hi, x.lo + lo}, upper ? x.hi : hi);
+    }
+    return x;
+}
+__device__ __forceinline__ double whole(Pair x)
+{
+    // (Inf and NaN have no rest)
+    return fabsf(x.hi) <= 3.0e38f ? (double)x.hi + (double)x.lo : (double)x.hi;
+}
+// x / n for a count n: the quotient, and that of what it leaves.
+__device__ __forceinline__ Pair share(Pair x, int32_t n)
+{
+    if (n <= 1 || !(fabsf(x.hi) <= 3.0e38f)) return n > 1 ? Pair{x.hi / (float)n, 0.0f} : x;
+    const float d = (float)n, more = (float)(n - (int32_t)d);
+    const float q = x.hi / d;
+    return {q, (fmaf(-q, more, fmaf(-q, d, x.hi)) + x.lo) / d};
+}
+
 struct Sums {
-    double a, k;
+    Pair a, k;
     int32_t count, clipped;
 };
 
-// x / n for a count n.  A 64-bit division takes 1 us of a call that takes 2; the quotient of
-// the high parts and one of what it leaves are as good as 48 bits.
-__device__ __forceinline__ double over(double x, int32_t n)
-{
-    if (n <= 1) return x;
-    const float d = (float)n, hi = (float)x;
-    if (n >= 1 << 24 || !(fabsf(hi) <= 3.0e38f)) return x / (double)n;
-    const float q = hi / d, lo = (float)(x - (double)hi);
-    return (double)q + (double)((fmaf(-q, d, hi) + lo) / d);
-}
-
-// The parts of sequence s = [from, to) over a warp's lanes, joined in every lane.
+// The parts of sequence s = [from, to), each of n threads taking every n-th; joined over the
+// warp's lanes.
 template <Kind K, int ITEMS>
 __device__ __forceinline__ Sums join_parts(const LossArgs& a, int64_t s, int64_t from, int64_t to,
-                                           int lane)
+                                           int thread, int n)
 {
-    Sums r{0.0, 0.0, 0, 0};
+    Sums r{{0.0f, 0.0f}, {0.0f, 0.0f}, 0, 0};
     if (from < 0 || to < from || to > a.T) {
-        if (lane == 0 && a.status) atomicOr(a.status, ZERO_DEV_BAD_OFFSETS);
+        if (thread == 0 && a.status) atomicOr(a.status, ZERO_DEV_BAD_OFFSETS);
         return r;
     }
     if (from == to) return r;
     const int64_t first = from / kTile<ITEMS>, last = (to - 1) / kTile<ITEMS>;
-#pragma unroll 4
-    for (int64_t i = first + lane; i <= last; i += 32) {
+#pragma unroll 8
+    for (int64_t i = first + thread; i <= last; i += n) {
         const Part p = a.parts[i + s];
-        r.a += p.a;
-        if (K == kPolicy) r.k += p.k;
+        r.a = plus(r.a, p.a);
+        if (K == kPolicy) r.k = plus(r.k, p.k);
         r.count += p.count;
         r.clipped += p.clipped;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        r.a += __shfl_xor_sync(kAll, r.a, o);
-        if (K == kPolicy) r.k += __shfl_xor_sync(kAll, r.k, o);
-    }
+    r.a = warp_pair(r.a);
+    if (K == kPolicy) r.k = warp_pair(r.k);
     r.count = __reduce_add_sync(kAll, r.count);
     if (K == kPolicy) r.clipped = __reduce_add_sync(kAll, r.clipped);
+    return r;
+}
+
+// The same over the warps of a block that has one result.
+__device__ __forceinline__ Sums join_warps(Sums r)
+{
+    __shared__ Sums all[kWideThreads / 32];
+    __syncthreads();                                 // (a pair's two sequences use it in turn)
+    if ((threadIdx.x & 31) == 0) all[threadIdx.x >> 5] = r;
+    __syncthreads();
+    r = all[0];
+    for (int w = 1; w < kWideThreads / 32; ++w) {
+        const Sums x = all[w];
+        r.a = plus(Pair{r.a.hi, r.a.lo + x.a.lo}, x.a.hi);
+        r.k = plus(Pair{r.k.hi, r.k.lo + x.k.lo}, x.k.hi);
+        r.count += x.count;
+        r.clipped += x.clipped;
+    }
     return r;
 }
 
@@ -289,41 +381,48 @@ __device__ __forceinline__ float softplus(float x)
     return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
-// Pair p's loss from its two sequences, or sequence p's.  `ready` is called once between the
-// offsets' loads and the parts'.
-template <Kind K, int ITEMS, typename Ready>
-__device__ __forceinline__ void finish(const LossArgs& a, int64_t p, int lane, Ready&& ready)
+// Pair p's loss from its two sequences, or sequence p's, by a warp or (WIDE) a block.  Waits
+// for the parts once the offsets are there.
+template <Kind K, int ITEMS, bool WIDE>
+__device__ __forceinline__ void finish(const LossArgs& a, int64_t p)
 {
+    const int thread = WIDE ? threadIdx.x : threadIdx.x & 31, n = WIDE ? kWideThreads : 32;
     if (K == kPolicy) {
         const int64_t from = raw_offset(a, p), to = raw_offset(a, p + 1);
-        ready();
-        Sums r = join_parts<K, ITEMS>(a, p, from, to, lane);
-        if (lane) return;
+        pdl_enter();
+        Sums r = join_parts<K, ITEMS>(a, p, from, to, thread, n);
+        if (WIDE) r = join_warps(r);
+        if (thread) return;
         if (a.average) {
-            r.a = over(r.a, r.count);
-            r.k = over(r.k, r.count);
+            r.a = share(r.a, r.count);
+            r.k = share(r.k, r.count);
         }
-        a.loss[p] = (float)r.a;
-        a.kl[p] = (float)r.k;
+        a.loss[p] = (float)whole(r.a);
+        a.kl[p] = (float)whole(r.k);
         a.counts[p] = r.count;
         a.clipped[p] = r.clipped;
         return;
     }
     const int64_t from = raw_offset(a, 2 * p), mid = raw_offset(a, 2 * p + 1),
                   to = raw_offset(a, 2 * p + 2);
-    ready();
-    Sums c = join_parts<K, ITEMS>(a, 2 * p, from, mid, lane);
-    Sums r = join_parts<K, ITEMS>(a, 2 * p + 1, mid, to, lane);
-    if (lane) return;
-    if (a.average) {
-        c.a = over(c.a, c.count);
-        r.a = over(r.a, r.count);
+    pdl_enter();
+    Sums c = join_parts<K, ITEMS>(a, 2 * p, from, mid, thread, n);
+    Sums r = join_parts<K, ITEMS>(a, 2 * p + 1, mid, to, thread, n);
+    if (WIDE) {
+        c = join_warps(c);
+        r = join_warps(r);
     }
-    a.ratios[2 * p] = (float)c.a;
-    a.ratios[2 * p + 1] = (float)r.a;
+    if (thread) return;
+    if (a.average) {
+        c.a = share(c.a, c.count);
+        r.a = share(r.a, r.count);
+    }
+    const double chosen = whole(c.a), rejected = whole(r.a);
+    a.ratios[2 * p] = (float)chosen;
+    a.ratios[2 * p + 1] = (float)rejected;
     a.counts[2 * p] = c.count;
     a.counts[2 * p + 1] = r.count;
-    const double d = c.a - r.a;
+    const double d = chosen - rejected;
     float loss, slope;
     if (a.kind == ZERO_PREF_IPO) {
         const double e = d - a.margin;                     // (margin + 1/(2 beta))
@@ -359,27 +458,16 @@ __global__ void __launch_bounds__(kThreads) k_loss_parts(const __grid_constant__
 
 // Its blocks come in beside those of k_loss_parts, which have waited for what was before them:
 // the offsets may be read before the parts are there.
-template <Kind K, int ITEMS>
-__global__ void __launch_bounds__(kThreads) k_loss_join(const __grid_constant__ LossArgs a)
+template <Kind K, int ITEMS, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? kWideThreads : kThreads)
+    k_loss_join(const __grid_constant__ LossArgs a)
 {
-    const int64_t p = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int64_t p =
+        WIDE ? blockIdx.x : (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (p < (K == kPreference ? a.S / 2 : a.S))
-        finish<K, ITEMS>(a, p, threadIdx.x & 31, [] { pdl_enter(); });
+        finish<K, ITEMS, WIDE>(a, p);
     else
         pdl_enter();
-}
-
-// Few tokens: one block does both, in one launch.
-template <Kind K>
-__global__ void __launch_bounds__(kAloneThreads) k_loss_alone(const __grid_constant__ LossArgs a)
-{
-    pdl_enter();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (warp < a.tiles) tile_parts<K, kFewItems>(a, warp, lane);
-    __syncthreads();
-    const int64_t results = K == kPreference ? a.S / 2 : a.S;
-    for (int64_t p = warp; p < results; p += kAloneThreads / 32)
-        finish<K, kFewItems>(a, p, lane, [] {});
 }
 
 // The gradient of each token's loss.
@@ -397,13 +485,9 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad(const __grid_constant__ 
     float v[ITEMS], kk[ITEMS];
     unsigned side = 0;
     if (K == kPolicy) {
+        side = policy_terms<true>(a, x, v, kk);
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            const float change = x.old[j] - x.nll[j];
-            v[j] = expf(change);
-            kk[j] = a.kl_coef != 0.0f ? a.kl_coef * drift(x.nll[j] - x.ref[j]).e : 0.0f;
-            side |= beyond(a, x.old[j], x.nll[j], change) << 2 * j;
-        }
+        for (int j = 0; j < ITEMS; ++j) kk[j] *= a.kl_coef;
     }
     // the advantage, where it is the sequence's, and the upstream gradient of its tokens
     const auto about = [&](int64_t s) {
@@ -436,9 +520,12 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad(const __grid_constant__ 
     });
 }
 
-int items_of(int64_t T) { return T < kFew ? kFewItems : kManyItems; }
-
-int64_t tiles_of(int64_t T) { return (T + 32 * items_of(T) - 1) / (32 * items_of(T)); }
+template <Kind K>
+int64_t tiles_of(int64_t T)
+{
+    const int64_t tile = 32 * (T < kFew ? kFewItems : many_items(K));
+    return (T + tile - 1) / tile;
+}
 
 constexpr int64_t kMaxSequences = 1ll << 30;
 
@@ -459,37 +546,41 @@ unsigned blocks_of(int64_t warps) { return (unsigned)((warps + kThreads / 32 - 1
 template <Kind K, int ITEMS>
 zero_status forward_in(const LossArgs& a, int64_t results, cudaStream_t st)
 {
-    cudaError_t e = launch(k_loss_parts<K, ITEMS>, dim3(blocks_of(a.tiles)), kThreads, 0, st, a);
-    if (e == cudaSuccess)
-        e = launch(k_loss_join<K, ITEMS>, dim3(blocks_of(results)), kThreads, 0, st, a);
-    return status_of(e);
+    // (one block at least: what the second launch reads early is there once the first one runs)
+    cudaError_t e = launch(k_loss_parts<K, ITEMS>, dim3(std::max(1u, blocks_of(a.tiles))), kThreads,
+                           0, st, a);
+    if (e != cudaSuccess) return status_of(e);
+    // a warp takes a result unless it would have to fetch many parts (one sequence of 10^6
+    // tokens: 41 us by a warp, 17 by a block)
+    return status_of(a.tiles >= kWideTiles * results
+                         ? launch(k_loss_join<K, ITEMS, true>, dim3((unsigned)results),
+                                  kWideThreads, 0, st, a)
+                         : launch(k_loss_join<K, ITEMS, false>, dim3(blocks_of(results)), kThreads,
+                                  0, st, a));
 }
 
 template <Kind K>
 zero_status forward(LossArgs& a, int64_t results, cudaStream_t st)
 {
-    a.tiles = tiles_of(a.T);
-    // (without tokens there is no first launch that waits for the offsets)
-    if (a.tiles == 0 || (a.tiles <= kAloneThreads / 32 && results <= kAloneResults))
-        return status_of(launch(k_loss_alone<K>, dim3(1), kAloneThreads, 0, st, a));
-    return items_of(a.T) == kFewItems ? forward_in<K, kFewItems>(a, results, st)
-                                      : forward_in<K, kManyItems>(a, results, st);
+    a.tiles = tiles_of<K>(a.T);
+    return a.T < kFew ? forward_in<K, kFewItems>(a, results, st)
+                      : forward_in<K, many_items(K)>(a, results, st);
 }
 
 template <Kind K>
 zero_status backward(LossArgs& a, cudaStream_t st)
 {
-    a.tiles = tiles_of(a.T);
-    return status_of(launch(items_of(a.T) == kFewItems ? k_loss_grad<K, kFewItems>
-                                                       : k_loss_grad<K, kManyItems>,
+    a.tiles = tiles_of<K>(a.T);
+    return status_of(launch(a.T < kFew ? k_loss_grad<K, kFewItems> : k_loss_grad<K, many_items(K)>,
                             dim3(blocks_of(a.tiles)), kThreads, 0, st, a));
 }
 
+template <Kind K>
 int64_t scratch_for(int64_t T, int64_t S)
 {
     if (check_packed(T, S) != ZERO_OK) return -1;
     // (the longest of few tokens have more tiles than somewhat more tokens)
-    const int64_t tiles = std::max(tiles_of(T), tiles_of(std::min(T, kFew - 1)));
+    const int64_t tiles = std::max(tiles_of<K>(T), tiles_of<K>(std::min(T, kFew - 1)));
     return up((int64_t)sizeof(Part) * (tiles + S), 256);
 }
 
@@ -514,7 +605,7 @@ zero_status policy_bounds(LossArgs& a, double clip_low, double clip_high, double
 
 extern "C" int64_t zero_preference_scratch_bytes(int64_t T, int64_t P)
 {
-    return P < 0 || P > kMaxSequences / 2 ? -1 : scratch_for(T, 2 * P);
+    return P < 0 || P > kMaxSequences / 2 ? -1 : scratch_for<kPreference>(T, 2 * P);
 }
 
 extern "C" zero_status zero_preference(const float* nll, const float* ref_nll, const void* targets,
@@ -630,7 +721,7 @@ extern "C" zero_status zero_preference_grad(const void* targets, int32_t target_
     return backward<kPreference>(a, static_cast<cudaStream_t>(stream));
 }
 
-extern "C" int64_t zero_policy_scratch_bytes(int64_t T, int64_t S) { return scratch_for(T, S); }
+extern "C" int64_t zero_policy_scratch_bytes(int64_t T, int64_t S) { return scratch_for<kPolicy>(T, S); }
 
 // What the two calls of the policy loss have in common; nothing of a call that has
 // nothing to write is looked at but its numbers.
