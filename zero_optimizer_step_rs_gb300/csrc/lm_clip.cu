@@ -298,7 +298,6 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_norm(const __grid_constant
                            : type == ZERO_TYPE_FP16
                                ? sum_squares<ZERO_TYPE_FP16>(p, numel, head, lo, hi)
                                : sum_squares<ZERO_TYPE_FP32>(p, numel, head, lo, hi);
-        if (stop == end) pdl_let_in();
         if (threadIdx.x == 0) {
             for (; slot < (int)blockIdx.x + i; ++slot) a.parts[slot] = 0.0;
             a.parts[slot++] = sum;

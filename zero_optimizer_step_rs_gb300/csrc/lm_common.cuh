@@ -77,13 +77,6 @@ __device__ __forceinline__ void pdl_enter()
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Lets the next launch in once every block has come here (or ended).  Only for a first
-// launch of a call whose second one is small and waits in pdl_enter() for the first's results.
-__device__ __forceinline__ void pdl_let_in()
-{
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
 __device__ __forceinline__ float warp_sum(float x)
 {
 #pragma unroll

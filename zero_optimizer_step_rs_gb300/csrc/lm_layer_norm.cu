@@ -245,9 +245,12 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 1
         if (p_s) p_s += s_step;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    for (int i = threadIdx.x; i < S * STAGE / 16; i += THREADS)
-        reinterpret_cast<uint4*>(ring)[i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+        if (lane + k * TPR >= nv)
+#pragma unroll
+            for (int i = 0; i < 3 * S; ++i)
+                st16(ring + i * N + (k * THREADS + threadIdx.x) * 16, make_uint4(0, 0, 0, 0));
 
     uint4 w4[NV];
 #pragma unroll
@@ -316,7 +319,6 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 1
         stage = stage == (S - 1) * STAGE ? 0 : stage + STAGE;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    pdl_let_in();
     if (!a.parts) return;
     float* part = a.parts + (int64_t)blockIdx.x * 2 * a.D;
     if constexpr (GROUPS == 1) {
@@ -554,7 +556,11 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
     a.D = D;
     auto run = [&](void (*kernel)(LayerNormGradArgs), int tpr, int smem, std::atomic<int>* per_sm) {
         const int threads = tpr > 128 ? tpr : 128, groups = threads / tpr;
-        // as many blocks as are resident at once: a second wave would be a short one
+        // as many blocks as are resident at once: a second wave would be a short one.  With
+        // few rows fewer, one an SM at least, so that there are fewer parts to join: at 16 rows
+        // a group 2000 x 2048 takes 13.6 us and 1000 x 768 7.0, in as many blocks as fit 19.6
+        // and 12.3; a row that is one warp's is short, and 10000 x 256 takes 10.1 us at 16, 8.0 at 4
+        const int64_t few = std::max<int64_t>(device_sms(), T / (groups * (tpr == 32 ? 4 : 16)));
         int dev = 0;
         cudaGetDevice(&dev);
         int fit = per_sm[dev & 63].load(std::memory_order_relaxed);
@@ -566,7 +572,7 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
             if (e == cudaSuccess && fit > 0)
                 per_sm[dev & 63].store(fit, std::memory_order_relaxed);
         }
-        a.blocks = (int)std::min<int64_t>({(T + groups - 1) / groups, (int64_t)grad_blocks(T),
+        a.blocks = (int)std::min<int64_t>({(T + groups - 1) / groups, few, (int64_t)grad_blocks(T),
                                            (int64_t)std::max(1, fit) * device_sms()});
         if (e == cudaSuccess) e = launch(kernel, dim3((unsigned)a.blocks), threads, smem, st, a);
         if (e == cudaSuccess && wanted)

@@ -27,6 +27,7 @@ constexpr int kFewItems = 1;
 constexpr int many_items(int kind) { return kind == 0 ? 8 : 4; }
 constexpr int64_t kFew = 1 << 16;                    // tokens from which on a lane takes several
 constexpr int kThreads = 128;
+constexpr int kAloneTiles = 32, kAloneResults = 16;  // the most that one block takes alone
 constexpr int kWideThreads = 512;                    // of a block that joins one result's parts
 constexpr int64_t kWideTiles = 128;                  // parts a result from which on it does
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -61,7 +62,7 @@ struct LossArgs {
     const float* slope_in;
     const float* dloss;
     float* dnll;
-    int64_t T, S, tiles;
+    int32_t T, S, tiles;                             // (tiles + S slots: below 2^31 as well)
     int32_t target_bytes, offset_bytes, per_token, average, kind;
     float kl_coef;
     float bound_lo, bound_hi;                        // 1 - clip_low, 1 + clip_high
@@ -71,18 +72,17 @@ struct LossArgs {
     float smoothing;
 };
 
-__device__ __forceinline__ int64_t raw_offset(const LossArgs& a, int64_t i)
+__device__ __forceinline__ int64_t raw_offset(const LossArgs& a, int i)
 {
     return token_at(a.offsets, a.offset_bytes, i);
 }
 
 // The number of offsets (of S + 1) that are at most t, by a search in 32 parts.
-__device__ __forceinline__ int64_t offsets_up_to(const LossArgs& a, int64_t t, int lane)
+__device__ __forceinline__ int offsets_up_to(const LossArgs& a, int t, int lane)
 {
-    int64_t lo = 0, hi = a.S + 1;
+    int lo = 0, hi = a.S + 1;
     while (lo < hi) {
-        const int64_t step = (hi - lo + 31) >> 5;
-        const int64_t i = lo + lane * step;
+        const int step = (hi - lo + 31) >> 5, i = lo + lane * step;
         const bool below = i < hi && raw_offset(a, i) <= t;
         const int n = __popc(__ballot_sync(kAll, below));
         if (n == 0) break;
@@ -126,16 +126,15 @@ struct Tokens {
 
 // FULL: the whole tile lies below T.
 template <Kind K, bool GRAD, int ITEMS, bool FULL>
-__device__ __forceinline__ void load_some(const LossArgs& a, int64_t base, int lane,
+__device__ __forceinline__ void load_some(const LossArgs& a, int base, int lane,
                                           Tokens<ITEMS>& x)
 {
-    const int64_t at = base + lane;
-    const int n = FULL ? kTile<ITEMS> : (int)(a.T - base) - lane;    // tokens from `at` on
-    int64_t id[ITEMS];
+    const int at = base + lane, n = a.T - at;        // the lane's first token, tokens from there on
+    int id[ITEMS];                                   // (only the sign is looked at)
     if (a.target_bytes == 8) {
         const auto* p = static_cast<const long long*>(a.targets) + at;
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) id[j] = FULL || j * 32 < n ? p[j * 32] : -1;
+        for (int j = 0; j < ITEMS; ++j) id[j] = FULL || j * 32 < n ? (int)(p[j * 32] >> 32) : -1;
     } else {
         const auto* p = static_cast<const int*>(a.targets) + at;
 #pragma unroll
@@ -143,7 +142,7 @@ __device__ __forceinline__ void load_some(const LossArgs& a, int64_t base, int l
     }
     const auto values = [&](float (&v)[ITEMS], const float* p) {
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) v[j] = p && (FULL || j * 32 < n) ? p[at + j * 32] : 0.0f;
+        for (int j = 0; j < ITEMS; ++j) v[j] = p && (FULL || j * 32 < n) ? (p + at)[j * 32] : 0.0f;
     };
     if (K == kPolicy || !GRAD) {
         values(x.nll, a.nll);
@@ -155,42 +154,49 @@ __device__ __forceinline__ void load_some(const LossArgs& a, int64_t base, int l
     }
     x.live = 0;
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) x.live |= (id[j] >= 0 ? 1u : 0u) << j;
+    for (int j = 0; j < ITEMS; ++j) x.live |= (~(unsigned)id[j] >> 31) << j;
 }
 
 template <Kind K, bool GRAD, int ITEMS>
-__device__ __forceinline__ void load_tokens(const LossArgs& a, int64_t base, int lane,
+__device__ __forceinline__ void load_tokens(const LossArgs& a, int base, int lane,
                                             Tokens<ITEMS>& x)
 {
-    if (base + kTile<ITEMS> <= a.T) load_some<K, GRAD, ITEMS, true>(a, base, lane, x);
+    if (kTile<ITEMS> <= a.T - base) load_some<K, GRAD, ITEMS, true>(a, base, lane, x);
     else load_some<K, GRAD, ITEMS, false>(a, base, lane, x);
 }
 
-// The policy's tokens by themselves: the ratios r, exp(d) - d - 1 or (GRAD) exp(d) - 1 of
-// d = nll - ref, and for each token two bits: r above the upper bound, r below the lower one.
+// The policy's tokens by themselves, whatever their advantage is: the ratios r, exp(d) - d -
+// 1 or (GRAD) exp(d) - 1 of d = nll - ref, and which tokens have r above the upper and below
+// the lower bound (bit j: token j).
 //
 // The bounds are compared as logarithms, old - nll with log(bound), and as exact numbers:
 // rounding keeps the order, so only a difference that rounds to the same fp32 value as the logarithm
 // needs what both roundings lost.  Such tokens, and those with |d| > 1, are few: the warp
 // looks for them once and takes them by themselves.  (Made for every token these took a third of
 // the time; the comparison in 64 bits, half.)
+template <int ITEMS>
+struct Ratios {
+    float r[ITEMS], k[ITEMS];
+    unsigned high, low;
+};
 template <bool GRAD, int ITEMS>
-__device__ __forceinline__ unsigned policy_terms(const LossArgs& a, const Tokens<ITEMS>& x,
-                                                 float (&r)[ITEMS], float (&kk)[ITEMS])
+__device__ __forceinline__ Ratios<ITEMS> ratios_of(const LossArgs& a, const Tokens<ITEMS>& x)
 {
-    unsigned side = 0;
+    Ratios<ITEMS> v;
+    v.high = v.low = 0;
     bool tie = false, far = false;
     const bool drifts = GRAD ? a.kl_coef != 0.0f : a.ref != nullptr;
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
         const float change = a.old ? x.old[j] - x.nll[j] : 0.0f;
-        r[j] = expf(change);
-        side |= (unsigned)(change > a.edge_hi) << 2 * j | (unsigned)(change < a.edge_lo) << (2 * j + 1);
+        v.r[j] = expf(change);
+        v.high |= (change > a.edge_hi ? 1u : 0u) << j;
+        v.low |= (change < a.edge_lo ? 1u : 0u) << j;
         tie |= change == a.edge_hi || change == a.edge_lo;
-        kk[j] = 0.0f;
+        v.k[j] = 0.0f;
         if (drifts) {
             const float d = x.nll[j] - x.ref[j], k = drift_series(d);
-            kk[j] = GRAD ? d + k : k;
+            v.k[j] = GRAD ? d + k : k;
             far |= !(fabsf(d) <= 1.0f);
         }
     }
@@ -198,8 +204,8 @@ __device__ __forceinline__ unsigned policy_terms(const LossArgs& a, const Tokens
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
             const float change = x.old[j] - x.nll[j], rest = lost(x.old[j], x.nll[j], change);
-            if (change == a.edge_hi && rest > a.rest_hi) side |= 1u << 2 * j;
-            if (change == a.edge_lo && rest < a.rest_lo) side |= 2u << 2 * j;
+            if (change == a.edge_hi && rest > a.rest_hi) v.high |= 1u << j;
+            if (change == a.edge_lo && rest < a.rest_lo) v.low |= 1u << j;
         }
     }
     if (__any_sync(kAll, far)) {
@@ -213,22 +219,43 @@ __device__ __forceinline__ unsigned policy_terms(const LossArgs& a, const Tokens
             const float e = expf(d) - 1.0f, k = GRAD ? e : e - d;
 #pragma unroll
             for (int i = 0; i < ITEMS; ++i)
-                if (i == j && !(fabsf(d) <= 1.0f)) kk[i] = k;
+                if (i == j && !(fabsf(d) <= 1.0f)) v.k[i] = k;
         }
     }
-    return side;
+    return v;
+}
+
+// A lane's tokens of [lo, hi) of a tile, as bits.
+template <int ITEMS>
+__device__ __forceinline__ unsigned tokens_in(int lo, int hi, int lane)
+{
+    const int from = (max(lo - lane, 0) + 31) >> 5, to = (max(hi - lane, 0) + 31) >> 5;
+    return (1u << to) - (1u << from);
+}
+
+// The advantages above and below 0 of a lane's tokens, as bits.
+template <int ITEMS>
+__device__ __forceinline__ void signs_of(const float (&A)[ITEMS], unsigned& pos, unsigned& neg)
+{
+    pos = neg = 0;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+        pos |= (A[j] > 0.0f ? 1u : 0u) << j;
+        neg |= (A[j] < 0.0f ? 1u : 0u) << j;
+    }
 }
 
 // Calls f(s, lo, hi, of(s)) for every sequence from s0 on that the tile at base meets, with the
 // part [base + lo, base + hi) of it that lies inside.  The bounds and of(s) of 32 sequences are
 // fetched at once, one a lane.
 template <int ITEMS, typename Of, typename F>
-__device__ __forceinline__ void for_sequences(const LossArgs& a, int64_t base, int64_t s0,
-                                              int lane, Of&& of, F&& f)
+__device__ __forceinline__ void for_sequences(const LossArgs& a, int base, int s0, int lane,
+                                              Of&& of, F&& f)
 {
-    const int64_t n = min((int64_t)kTile<ITEMS>, a.T - base);
-    for (int64_t s = max(s0, (int64_t)0); s < a.S; s += 31) {
-        const int lo = (int)min(max(raw_offset(a, min(s + lane, a.S)) - base, (int64_t)0), n);
+    const int n = min(kTile<ITEMS>, a.T - base);
+    for (int s = max(s0, 0); s < a.S; s += 31) {
+        const int64_t bound = raw_offset(a, min(s + lane, a.S));
+        const int lo = bound <= base ? 0 : (int)min(bound - base, (int64_t)n);
         const float2 about = of(min(s + lane, a.S - 1));
         const int hi = __shfl_down_sync(kAll, lo, 1);
         // (the last lane's sequence is the next round's first; past the last one none begins)
@@ -245,49 +272,53 @@ __device__ __forceinline__ void for_sequences(const LossArgs& a, int64_t base, i
 
 // The terms of a tile, summed for each sequence that it meets.
 template <Kind K, int ITEMS>
-__device__ __forceinline__ void tile_parts(const LossArgs& a, int64_t tile, int lane)
+__device__ __forceinline__ void tile_parts(const LossArgs& a, Part* parts, int tile, int lane)
 {
-    const int64_t base = tile * kTile<ITEMS>;
+    const int base = tile * kTile<ITEMS>;
     Tokens<ITEMS> x;
     load_tokens<K, false, ITEMS>(a, base, lane, x);
-    const int64_t s0 = offsets_up_to(a, base, lane) - 1;     // while the tokens are on their way
-    float v[ITEMS], kk[ITEMS];
-    unsigned side = 0;
+    const int s0 = offsets_up_to(a, base, lane) - 1;     // while the tokens are on their way
+    Ratios<ITEMS> v;
     if (K == kPolicy) {
-        side = policy_terms<false>(a, x, v, kk);
+        v = ratios_of<false>(a, x);
     } else {
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) v[j] = x.ref[j] - x.nll[j];
+        for (int j = 0; j < ITEMS; ++j) v.r[j] = x.ref[j] - x.nll[j];
     }
-    const auto about = [&](int64_t s) {
+    const auto about = [&](int s) {
         return make_float2(K == kPolicy && !a.per_token ? a.adv[s] : 0.0f, 0.0f);
     };
-    for_sequences<ITEMS>(a, base, s0, lane, about, [&](int64_t s, int lo, int hi, float2 of_s) {
-        const float shared = of_s.x;
+    for_sequences<ITEMS>(a, base, s0, lane, about, [&](int s, int lo, int hi, float2 of_s) {
+        const unsigned mine = tokens_in<ITEMS>(lo, hi, lane) & x.live;
         float sum = 0.0f, ksum = 0.0f;
-        int both = 0;                                // clipped tokens above bit 16, all below
+        int both = __popc(mine);                     // clipped tokens above bit 16, all below
+        if (K == kPreference) {
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) {
-            const int t = j * 32 + lane;
-            if (t < lo || t >= hi || !(x.live >> j & 1)) continue;
-            ++both;
-            if (K == kPreference) {
-                sum += v[j];
-            } else {
-                const float A = a.per_token ? x.adv[j] : shared;
-                const bool over = A > 0.0f ? side >> 2 * j & 1 : A < 0.0f && (side >> 2 * j & 2);
-                const float r = over ? (A > 0.0f ? a.bound_hi : a.bound_lo) : v[j];
+            for (int j = 0; j < ITEMS; ++j) sum += mine >> j & 1 ? v.r[j] : 0.0f;
+        } else {
+            if (!a.per_token)
+#pragma unroll
+                for (int j = 0; j < ITEMS; ++j) x.adv[j] = of_s.x;
+            unsigned pos, neg;
+            signs_of(x.adv, pos, neg);
+            both += __popc(mine & (v.high & pos | v.low & neg)) << 16;
+#pragma unroll
+            for (int j = 0; j < ITEMS; ++j) {
+                // -min(r A, bounded r A); where A is 0 no r, Inf among them, counts
+                const float A = x.adv[j];
+                // (comparisons that a NaN fails, so that it stays)
+                const float r = A > 0.0f ? (v.r[j] > a.bound_hi ? a.bound_hi : v.r[j])
+                                         : (v.r[j] < a.bound_lo ? a.bound_lo : v.r[j]);
                 float term = A == 0.0f ? 0.0f : -(r * A);
-                if (a.kl_coef != 0.0f) term = fmaf(a.kl_coef, kk[j], term);
-                sum += term;
-                ksum += kk[j];
-                both += over ? 1 << 16 : 0;
+                if (a.kl_coef != 0.0f) term = fmaf(a.kl_coef, v.k[j], term);
+                sum += mine >> j & 1 ? term : 0.0f;
+                ksum += mine >> j & 1 ? v.k[j] : 0.0f;
             }
         }
         sum = warp_sum(sum);
         if (K == kPolicy) ksum = warp_sum(ksum);
         both = __reduce_add_sync(kAll, both);
-        if (lane == 0) a.parts[tile + s] = Part{sum, ksum, both & 0xFFFF, both >> 16};
+        if (lane == 0) parts[tile + s] = Part{sum, ksum, both & 0xFFFF, both >> 16};
     });
 }
 
@@ -333,8 +364,8 @@ struct Sums {
 // The parts of sequence s = [from, to), each of n threads taking every n-th; joined over the
 // warp's lanes.
 template <Kind K, int ITEMS>
-__device__ __forceinline__ Sums join_parts(const LossArgs& a, int64_t s, int64_t from, int64_t to,
-                                           int thread, int n)
+__device__ __forceinline__ Sums join_parts(const LossArgs& a, const Part* parts, int s, int64_t from,
+                                           int64_t to, int thread, int n)
 {
     Sums r{{0.0f, 0.0f}, {0.0f, 0.0f}, 0, 0};
     if (from < 0 || to < from || to > a.T) {
@@ -342,10 +373,10 @@ __device__ __forceinline__ Sums join_parts(const LossArgs& a, int64_t s, int64_t
         return r;
     }
     if (from == to) return r;
-    const int64_t first = from / kTile<ITEMS>, last = (to - 1) / kTile<ITEMS>;
+    const int first = (int)from / kTile<ITEMS> + s, last = ((int)to - 1) / kTile<ITEMS> + s;
 #pragma unroll 8
-    for (int64_t i = first + thread; i <= last; i += n) {
-        const Part p = a.parts[i + s];
+    for (int i = first + thread; i <= last; i += n) {
+        const Part p = parts[i];
         r.a = plus(r.a, p.a);
         if (K == kPolicy) r.k = plus(r.k, p.k);
         r.count += p.count;
@@ -381,16 +412,14 @@ __device__ __forceinline__ float softplus(float x)
     return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x)));
 }
 
-// Pair p's loss from its two sequences, or sequence p's, by a warp or (WIDE) a block.  Waits
-// for the parts once the offsets are there.
+// Pair p's loss from its two sequences, or sequence p's, by a warp or (WIDE) a block.
 template <Kind K, int ITEMS, bool WIDE>
-__device__ __forceinline__ void finish(const LossArgs& a, int64_t p)
+__device__ __forceinline__ void finish(const LossArgs& a, const Part* parts, int p)
 {
     const int thread = WIDE ? threadIdx.x : threadIdx.x & 31, n = WIDE ? kWideThreads : 32;
     if (K == kPolicy) {
         const int64_t from = raw_offset(a, p), to = raw_offset(a, p + 1);
-        pdl_enter();
-        Sums r = join_parts<K, ITEMS>(a, p, from, to, thread, n);
+        Sums r = join_parts<K, ITEMS>(a, parts, p, from, to, thread, n);
         if (WIDE) r = join_warps(r);
         if (thread) return;
         if (a.average) {
@@ -405,9 +434,8 @@ __device__ __forceinline__ void finish(const LossArgs& a, int64_t p)
     }
     const int64_t from = raw_offset(a, 2 * p), mid = raw_offset(a, 2 * p + 1),
                   to = raw_offset(a, 2 * p + 2);
-    pdl_enter();
-    Sums c = join_parts<K, ITEMS>(a, 2 * p, from, mid, thread, n);
-    Sums r = join_parts<K, ITEMS>(a, 2 * p + 1, mid, to, thread, n);
+    Sums c = join_parts<K, ITEMS>(a, parts, 2 * p, from, mid, thread, n);
+    Sums r = join_parts<K, ITEMS>(a, parts, 2 * p + 1, mid, to, thread, n);
     if (WIDE) {
         c = join_warps(c);
         r = join_warps(r);
@@ -451,23 +479,33 @@ template <Kind K, int ITEMS>
 __global__ void __launch_bounds__(kThreads) k_loss_parts(const __grid_constant__ LossArgs a)
 {
     pdl_enter();
-    pdl_let_in();
-    const int64_t tile = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (tile < a.tiles) tile_parts<K, ITEMS>(a, tile, threadIdx.x & 31);
+    const int tile = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (tile < a.tiles) tile_parts<K, ITEMS>(a, a.parts, tile, threadIdx.x & 31);
 }
 
-// Its blocks come in beside those of k_loss_parts, which have waited for what was before them:
-// the offsets may be read before the parts are there.
 template <Kind K, int ITEMS, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kWideThreads : kThreads)
     k_loss_join(const __grid_constant__ LossArgs a)
 {
-    const int64_t p =
-        WIDE ? blockIdx.x : (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    if (p < (K == kPreference ? a.S / 2 : a.S))
-        finish<K, ITEMS, WIDE>(a, p);
-    else
-        pdl_enter();
+    pdl_enter();
+    const int p = WIDE ? blockIdx.x : blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    if (p < (K == kPreference ? a.S / 2 : a.S)) finish<K, ITEMS, WIDE>(a, a.parts, p);
+}
+
+// Few tokens: one block does both, and the parts stay in its shared memory.  999 tokens of 4 pairs
+// with their gradient 5.1 us (in two launches 5.6), 200 of 4 sequences of the policy 4.6 (5.3);
+// with 60 sequences 8.9 (6.8), 2000 tokens 7.2 (5.7).
+template <Kind K>
+__global__ void __launch_bounds__(1024) k_loss_alone(const __grid_constant__ LossArgs a)
+{
+    pdl_enter();
+    __shared__ Part parts[kAloneTiles + 2 * kAloneResults];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
+    for (int tile = warp; tile < a.tiles; tile += warps)
+        tile_parts<K, kFewItems>(a, parts, tile, threadIdx.x & 31);
+    __syncthreads();
+    for (int p = warp; p < (K == kPreference ? a.S / 2 : a.S); p += warps)
+        finish<K, kFewItems, false>(a, parts, p);
 }
 
 // The gradient of each token's loss.
@@ -476,21 +514,20 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad(const __grid_constant__ 
 {
     pdl_enter();
     const int lane = threadIdx.x & 31;
-    const int64_t tile = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int tile = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
     if (tile >= a.tiles) return;
-    const int64_t base = tile * kTile<ITEMS>;
+    const int base = tile * kTile<ITEMS>;
     Tokens<ITEMS> x;
     load_tokens<K, true, ITEMS>(a, base, lane, x);
-    const int64_t s0 = offsets_up_to(a, base, lane) - 1;
-    float v[ITEMS], kk[ITEMS];
-    unsigned side = 0;
+    const int s0 = offsets_up_to(a, base, lane) - 1;
+    Ratios<ITEMS> v;
     if (K == kPolicy) {
-        side = policy_terms<true>(a, x, v, kk);
+        v = ratios_of<true>(a, x);
 #pragma unroll
-        for (int j = 0; j < ITEMS; ++j) kk[j] *= a.kl_coef;
+        for (int j = 0; j < ITEMS; ++j) v.k[j] *= a.kl_coef;
     }
     // the advantage, where it is the sequence's, and the upstream gradient of its tokens
-    const auto about = [&](int64_t s) {
+    const auto about = [&](int s) {
         float back = a.dloss[K == kPolicy ? s : s >> 1];
         if (K == kPreference) {
             back *= a.slope_in[s >> 1];
@@ -499,23 +536,25 @@ __global__ void __launch_bounds__(kThreads) k_loss_grad(const __grid_constant__ 
         if (a.average) back /= (float)max(a.counts_in[s], 1);
         return make_float2(K == kPolicy && !a.per_token ? a.adv[s] : 0.0f, back);
     };
-    for_sequences<ITEMS>(a, base, s0, lane, about, [&](int64_t s, int lo, int hi, float2 of_s) {
-        const float shared = of_s.x, back = of_s.y;
+    for_sequences<ITEMS>(a, base, s0, lane, about, [&](int s, int lo, int hi, float2 of_s) {
+        const unsigned in = tokens_in<ITEMS>(lo, hi, lane);
+        const float back = of_s.y;
+        float* out = a.dnll + base + lane;
+        unsigned over = 0;
+        if (K == kPolicy) {
+            if (!a.per_token)
+#pragma unroll
+                for (int j = 0; j < ITEMS; ++j) x.adv[j] = of_s.x;
+            unsigned pos, neg;
+            signs_of(x.adv, pos, neg);
+            // clipped, or an advantage of 0, which makes no ratio count, Inf among them
+            over = v.high & pos | v.low & neg | ~(pos | neg);
+        }
 #pragma unroll
         for (int j = 0; j < ITEMS; ++j) {
-            const int t = j * 32 + lane;
-            if (t < lo || t >= hi) continue;
-            float g = 0.0f;
-            if (x.live >> j & 1) {
-                if (K == kPreference) {
-                    g = back;
-                } else {
-                    const float A = a.per_token ? x.adv[j] : shared;
-                    const bool over = A > 0.0f ? side >> 2 * j & 1 : A < 0.0f && (side >> 2 * j & 2);
-                    g = fmaf(over || A == 0.0f ? 0.0f : v[j], A, kk[j]) * back;
-                }
-            }
-            a.dnll[base + t] = g;
+            float g = back;
+            if (K == kPolicy) g = fmaf(over >> j & 1 ? 0.0f : v.r[j], x.adv[j], v.k[j]) * back;
+            if (in >> j & 1) out[j * 32] = x.live >> j & 1 ? g : 0.0f;
         }
     });
 }
@@ -546,9 +585,7 @@ unsigned blocks_of(int64_t warps) { return (unsigned)((warps + kThreads / 32 - 1
 template <Kind K, int ITEMS>
 zero_status forward_in(const LossArgs& a, int64_t results, cudaStream_t st)
 {
-    // (one block at least: what the second launch reads early is there once the first one runs)
-    cudaError_t e = launch(k_loss_parts<K, ITEMS>, dim3(std::max(1u, blocks_of(a.tiles))), kThreads,
-                           0, st, a);
+    cudaError_t e = launch(k_loss_parts<K, ITEMS>, dim3(blocks_of(a.tiles)), kThreads, 0, st, a);
     if (e != cudaSuccess) return status_of(e);
     // a warp takes a result unless it would have to fetch many parts (one sequence of 10^6
     // tokens: 41 us by a warp, 17 by a block)
@@ -562,7 +599,11 @@ zero_status forward_in(const LossArgs& a, int64_t results, cudaStream_t st)
 template <Kind K>
 zero_status forward(LossArgs& a, int64_t results, cudaStream_t st)
 {
-    a.tiles = tiles_of<K>(a.T);
+    a.tiles = (int32_t)tiles_of<K>(a.T);
+    if (a.tiles == 0 || (a.tiles <= kAloneTiles && results <= kAloneResults)) {
+        const int warps = (int)std::min<int64_t>(32, std::max<int64_t>(a.tiles, results));
+        return status_of(launch(k_loss_alone<K>, dim3(1), 32 * warps, 0, st, a));
+    }
     return a.T < kFew ? forward_in<K, kFewItems>(a, results, st)
                       : forward_in<K, many_items(K)>(a, results, st);
 }
@@ -570,7 +611,7 @@ zero_status forward(LossArgs& a, int64_t results, cudaStream_t st)
 template <Kind K>
 zero_status backward(LossArgs& a, cudaStream_t st)
 {
-    a.tiles = tiles_of<K>(a.T);
+    a.tiles = (int32_t)tiles_of<K>(a.T);
     return status_of(launch(a.T < kFew ? k_loss_grad<K, kFewItems> : k_loss_grad<K, many_items(K)>,
                             dim3(blocks_of(a.tiles)), kThreads, 0, st, a));
 }
@@ -666,8 +707,8 @@ extern "C" zero_status zero_preference(const float* nll, const float* ref_nll, c
     a.slope = slope;
     a.ratios = ratios;
     a.counts = counts;
-    a.T = T;
-    a.S = 2 * P;
+    a.T = (int32_t)T;
+    a.S = (int32_t)(2 * P);
     a.target_bytes = target_bytes;
     a.offset_bytes = offset_bytes;
     a.average = average;
@@ -713,8 +754,8 @@ extern "C" zero_status zero_preference_grad(const void* targets, int32_t target_
     a.counts_in = counts;
     a.dloss = dloss;
     a.dnll = dnll;
-    a.T = T;
-    a.S = 2 * P;
+    a.T = (int32_t)T;
+    a.S = (int32_t)(2 * P);
     a.target_bytes = target_bytes;
     a.offset_bytes = offset_bytes;
     a.average = average;
@@ -763,8 +804,8 @@ static zero_status policy_args(LossArgs& a, Spans& sp, bool grad, const float* n
     a.targets = targets;
     a.offsets = offsets;
     a.status = dev_status;
-    a.T = T;
-    a.S = S;
+    a.T = (int32_t)T;
+    a.S = (int32_t)S;
     a.target_bytes = target_bytes;
     a.offset_bytes = offset_bytes;
     a.per_token = per_token;
