@@ -31,24 +31,45 @@ struct LayerNormArgs {
 
 constexpr uint32_t kOnes = 0x3F803F80u;              // two bf16 ones
 
-// TPR threads take a row, each NV vectors of 8 elements; blocks of at least
-// 128 threads, so a block holds several rows where a row is one warp's.
-//
-// The row stays in registers.  Each warp takes the mean of its own elements and
+// How a row's vectors of 8 elements are spread over threads, NV to each.  SUB = 8, 16 or
+// 32: over so many lanes of a warp, and a block of 128 threads has 128 / SUB rows.  SUB = 0:
+// over the whole block, whose size is the row's number of vectors / NV in whole warps, so that
+// few threads have nothing: with sizes in powers of two rows of 2056 columns ran at 4.0 TB/s and
+// rows of 64 at 2.0.
+template <int SUB>
+struct Spread {
+    static constexpr int kRows = SUB ? 128 / SUB : 1;            // of a block
+    static __device__ __forceinline__ int threads() { return SUB ? SUB : (int)blockDim.x; }
+    static __device__ __forceinline__ int row() { return SUB ? (int)threadIdx.x / SUB : 0; }
+    static __device__ __forceinline__ int lane()
+    {
+        return SUB ? (int)threadIdx.x % SUB : (int)threadIdx.x;
+    }
+};
+
+// The sum over the lanes of a row that lie in one warp.
+template <int SUB>
+__device__ __forceinline__ float lane_sum(float x)
+{
+#pragma unroll
+    for (int o = (SUB ? SUB : 32) / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+    return x;
+}
+
+// The row stays in registers.  The lanes of a warp take the mean of their own elements and
 // their squared distances from it, and the warps' pairs are joined by
 //   mean = sum of sums / D,  M2 = sum of (M2_w + n_w (mean_w - mean)^2),
 // which cancels nothing and needs one barrier where two passes over the row would
 // need two.
-template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, 1)
+template <int SUB, int NV>
+__global__ void __launch_bounds__(SUB ? 128 : 512)
     k_layer_norm(const __grid_constant__ LayerNormArgs a)
 {
-    constexpr int THREADS = TPR > 128 ? TPR : 128;
+    using S = Spread<SUB>;
     pdl_enter();
-    const int64_t t = (int64_t)blockIdx.x * (THREADS / TPR) + threadIdx.x / TPR;
-    if (t >= a.T) return;                                  // whole warps; whole blocks if TPR > 32
-    const int lane = threadIdx.x % TPR;
-    const int nv = a.D >> 3;
+    const int64_t t = (int64_t)blockIdx.x * S::kRows + S::row();
+    const int lane = S::lane(), step = S::threads();
+    const int nv = t < a.T ? a.D >> 3 : 0;                 // a row past the last has no vectors
     const uint16_t* x = a.x + t * a.x_ld;
     const uint16_t* r = a.res ? a.res + t * a.res_ld : nullptr;
 
@@ -57,7 +78,7 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, 1)
         uint4 v[NV], u[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR;
+            const int c = lane + k * step;
             v[k] = u[k] = make_uint4(0, 0, 0, 0);
             if (c < nv) {
                 v[k] = ld16_stream(x + c * 8);
@@ -73,52 +94,51 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, 1)
             for (int q = 0; q < 8; ++q) f[k][q] += g[q];
         }
     }
-    // elements of the row that this warp holds
+    // elements of the row that these lanes hold
     int held = 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-        held += min(max(nv - ((lane & ~31) + k * TPR), 0), 32) * 8;
+        held += min(max(nv - (SUB ? 0 : lane & ~31) - k * step, 0), SUB ? SUB : 32) * 8;
     float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int q = 0; q < 8; ++q) s += f[k][q];
-    s = warp_sum(s);
+    s = lane_sum<SUB>(s);
     float mean = held ? s / (float)held : 0.0f, m2 = 0.0f;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-        if (lane + k * TPR < nv)
+        if (lane + k * step < nv)
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float d = f[k][q] - mean;
                 m2 = fmaf(d, d, m2);
             }
-    m2 = warp_sum(m2);
-    if constexpr (TPR > 32) {
-        __shared__ float4 parts[TPR / 32];
+    m2 = lane_sum<SUB>(m2);
+    if constexpr (SUB == 0) {
+        __shared__ float4 parts[16];
+        const int warps = step >> 5;
         if ((threadIdx.x & 31) == 0)
             parts[threadIdx.x >> 5] = make_float4(s, mean, m2, (float)held);
         __syncthreads();
         float total = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < TPR / 32; ++k) total += parts[k].x;
+        for (int k = 0; k < warps; ++k) total += parts[k].x;
         mean = total / (float)a.D;
         m2 = 0.0f;
-#pragma unroll 8
-        for (int k = 0; k < TPR / 32; ++k) {
+        for (int k = 0; k < warps; ++k) {
             const float4 p = parts[k];
             const float d = p.y - mean;
             m2 += fmaf(p.w * d, d, p.z);
         }
     }
     const float rstd = 1.0f / sqrtf(m2 / (float)a.D + a.eps);
-    if (lane == 0) {
+    if (lane == 0 && nv) {
         a.mean[t] = mean;
         a.rstd[t] = rstd;
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int c = lane + k * TPR;
+        const int c = lane + k * step;
         if (c < nv) {
             if (a.sum) st16_stream(a.sum + t * a.sum_ld + c * 8, bf_pack8(f[k]));
             float w[8], b[8];
@@ -148,26 +168,24 @@ struct LayerNormGradArgs {
     int32_t D, blocks;
 };
 
-// The sums of two values over the TPR threads of a row.  `slot` alternates from
-// row to row, so that one barrier a row is enough.
-template <int TPR>
+// The sums of two values over the threads of a row.  `slot` alternates from row to row, so that
+// one barrier a row is enough.
+template <int SUB>
 __device__ __forceinline__ float2 row_sums(float x, float y, float2 (*slots)[32], int slot)
 {
-    x = warp_sum(x);
-    y = warp_sum(y);
-    if constexpr (TPR > 32) {
-        const int warp = threadIdx.x >> 5;
-        if ((threadIdx.x & 31) == 0) slots[slot][warp] = make_float2(x, y);
+    x = lane_sum<SUB>(x);
+    y = lane_sum<SUB>(y);
+    if constexpr (SUB == 0) {
+        const int lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
+        if (lane == 0) slots[slot][threadIdx.x >> 5] = make_float2(x, y);
         __syncthreads();
-        if constexpr (TPR > 256) {
-            const int lane = threadIdx.x & 31;
-            const float2 p = lane < TPR / 32 ? slots[slot][lane] : make_float2(0.0f, 0.0f);
+        if (warps > 8) {
+            const float2 p = lane < warps ? slots[slot][lane] : make_float2(0.0f, 0.0f);
             x = warp_sum(p.x);
             y = warp_sum(p.y);
         } else {
             x = y = 0.0f;
-#pragma unroll
-            for (int k = 0; k < TPR / 32; ++k) {
+            for (int k = 0; k < warps; ++k) {
                 const float2 p = slots[slot][k];
                 x += p.x;
                 y += p.y;
@@ -192,34 +210,81 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at)
     return v;
 }
 
-// Rows that a thread has asked for ahead of the one it works on, plus that one.
-template <int TPR, int NV>
-__host__ __device__ constexpr int grad_stages() { return TPR * NV <= 512 ? 3 : 2; }
-template <int TPR, int NV>
-__host__ __device__ constexpr int grad_smem()
+// Two fp32 values in one register pair, which add, multiply and fma take in one instruction
+// (each value rounded by itself): the gradient's rows fill half of the issue slots with them where
+// they filled 55 to 60 %, and rows that leave lanes without a vector are bound by those.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float lo, float hi)
 {
-    return grad_stages<TPR, NV>() * NV * (TPR > 128 ? TPR : 128) * 48;
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ Two both(float x) { return two(x, x); }
+__device__ __forceinline__ float2 apart2(Two x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ Two add2(Two x, Two y)
+{
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ Two mul2(Two x, Two y)
+{
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two x, Two y, Two z)
+{
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return r;
+}
+__device__ __forceinline__ void bf_unpack_twos(const uint4& x, Two (&f)[4])
+{
+    f[0] = two(bf_lo(x.x), bf_hi(x.x));
+    f[1] = two(bf_lo(x.y), bf_hi(x.y));
+    f[2] = two(bf_lo(x.z), bf_hi(x.z));
+    f[3] = two(bf_lo(x.w), bf_hi(x.w));
+}
+
+// Rows that a thread has asked for ahead of the one it works on, plus that one.
+__host__ __device__ constexpr int grad_stages(int most) { return most <= 512 ? 3 : 2; }
+constexpr int kMostSmem = 225 * 1024;                // of a block, beside its static part
+
+// Blocks that an SM is to hold: they set the registers.  One vector a thread runs best with
+// many warps, 2 in 128 registers and 3 or 4 in 168.
+constexpr int grad_blocks_min(int sub, int nv, int most)
+{
+    if (sub) return nv == 1 ? 7 : nv == 2 ? 4 : 3;
+    return most <= 192 ? 2 : 1;
 }
 
 // A row's threads walk over many rows and keep the sums of dw and db in
 // registers; a block's row groups are added in order at its end.  The rows ahead wait in
 // shared memory, where a thread finds its own vectors: with a barrier in the middle of each
 // row a block would otherwise have nothing in flight for half of the time.
-template <int TPR, int NV>
-__global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 128 ? 512 / TPR : 4)
+template <int SUB, int NV, int MOST>
+__global__ void __launch_bounds__(SUB ? 128 : MOST, grad_blocks_min(SUB, NV, MOST))
     k_layer_norm_grad(const __grid_constant__ LayerNormGradArgs a)
 {
-    constexpr int THREADS = TPR > 128 ? TPR : 128;
-    constexpr int GROUPS = THREADS / TPR;
-    constexpr int S = grad_stages<TPR, NV>();
-    constexpr int N = NV * THREADS * 16, STAGE = 3 * N;      // a stage: dy, x, dsum
+    using W = Spread<SUB>;
+    constexpr int S = grad_stages(MOST);
+    constexpr bool KEEP = (NV == 2 || NV == 3) && MOST <= 512;
+    const int threads = SUB ? 128 : (int)blockDim.x;
+    const int N = NV * threads * 16, STAGE = 3 * N;          // a stage: dy, x, dsum
     pdl_enter();
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 slots[2][32];
-    const int group = threadIdx.x / TPR, lane = threadIdx.x % TPR;
+    const int lane = W::lane(), apart = W::threads();        // between a thread's vectors
     const int nv = a.D >> 3;
-    const int64_t step = (int64_t)gridDim.x * GROUPS;
-    const int64_t first = (int64_t)blockIdx.x * GROUPS + group;
+    const int64_t step = (int64_t)gridDim.x * W::kRows;
+    const int64_t first = (int64_t)blockIdx.x * W::kRows + W::row();
     const float inv = 1.0f / (float)a.D;
 
     // where the row to ask for next lies; a thread past the row's end asks for
@@ -233,11 +298,11 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 1
         if (in) {
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                if (lane + k * TPR >= nv) break;
-                const uint32_t at = mine + stage + k * THREADS * 16;
-                copy_async(at, p_d + k * TPR * 8);
-                copy_async(at + N, p_x + k * TPR * 8);
-                if (p_s) copy_async(at + 2 * N, p_s + k * TPR * 8);
+                if (lane + k * apart >= nv) break;
+                const uint32_t at = mine + stage + k * threads * 16;
+                copy_async(at, p_d + k * apart * 8);
+                copy_async(at + N, p_x + k * apart * 8);
+                if (p_s) copy_async(at + 2 * N, p_s + k * apart * 8);
             }
         }
         p_d += d_step;
@@ -247,18 +312,18 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 1
     };
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-        if (lane + k * TPR >= nv)
+        if (lane + k * apart >= nv)
 #pragma unroll
             for (int i = 0; i < 3 * S; ++i)
-                st16(ring + i * N + (k * THREADS + threadIdx.x) * 16, make_uint4(0, 0, 0, 0));
+                st16(ring + i * N + (k * threads + threadIdx.x) * 16, make_uint4(0, 0, 0, 0));
 
     uint4 w4[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         w4[k] = make_uint4(kOnes, kOnes, kOnes, kOnes);
-        if (a.w && lane + k * TPR < nv) w4[k] = ld16(a.w + (lane + k * TPR) * 8);
+        if (a.w && lane + k * apart < nv) w4[k] = ld16(a.w + (lane + k * apart) * 8);
     }
-    float dw[NV][8] = {}, db[NV][8] = {};
+    Two dw[NV][4] = {}, db[NV][4] = {};
     uint32_t stage = 0;                                   // offset of the row at hand
     int slot = 0;
 #pragma unroll
@@ -269,8 +334,12 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 1
         rstd_next = a.rstd[first];
     }
     uint16_t* p_o = a.dx + first * a.dx_ld + lane * 8;
-    // (barriers: where a row has more than a warp, the block has one row at a time)
-    for (int64_t t = first; t < a.T; t += step, p_o += step * a.dx_ld) {
+    // (all of a block's groups of threads go on while one has a row: the sums take whole warps)
+    int64_t t = first;
+    for (int64_t top = (int64_t)blockIdx.x * W::kRows; top < a.T;
+         top += step, t += step, p_o += step * a.dx_ld) {
+        const bool in = SUB == 0 || SUB == 32 || t < a.T;
+        if ((SUB == 32) && t >= a.T) break;                   // a whole warp
         const float mean = mean_next, rstd = rstd_next;
         if (t + step < a.T) {
             mean_next = a.mean[t + step];
@@ -279,76 +348,102 @@ __global__ void __launch_bounds__(TPR > 128 ? TPR : 128, TPR > 512 ? 1 : TPR > 1
         ask(t + (S - 1) * step < a.T,
             stage == 0 ? (S - 1) * STAGE : stage - STAGE);
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-        // xhat and dy * w are made twice, from what shared memory holds: keeping them
-        // would cost 16 registers a vector
+        // xhat and dy * w are kept for the row's second part where the registers allow it, else
+        // made again from what shared memory holds (2056 columns: 84 us kept, 90 made again;
+        // 64 and 1024 columns: 91 and 103 kept, 82 and 76 made again)
         const uint32_t here = mine + stage;
-        float s1 = 0.0f, s2 = 0.0f;
+        const Two less = both(-mean), scale = both(rstd);
+        Two s1 = 0, s2 = 0, kept_u[KEEP ? NV : 1][4], kept_x[KEEP ? NV : 1][4];
+        if (in)
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            float w[8], x[8], d[8];
-            bf_unpack8(w4[k], w);
-            bf_unpack8(ld_shared(here + k * THREADS * 16), d);
-            bf_unpack8(ld_shared(here + k * THREADS * 16 + N), x);
+            for (int k = 0; k < NV; ++k) {
+                Two w[4], x[4], d[4];
+                bf_unpack_twos(w4[k], w);
+                bf_unpack_twos(ld_shared(here + k * threads * 16), d);
+                bf_unpack_twos(ld_shared(here + k * threads * 16 + N), x);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float xh = (x[q] - mean) * rstd, u = d[q] * w[q];
-                db[k][q] += d[q];
-                dw[k][q] = fmaf(d[q], xh, dw[k][q]);
-                s1 += u;
-                s2 = fmaf(u, xh, s2);
+                for (int q = 0; q < 4; ++q) {
+                    const Two xh = mul2(add2(x[q], less), scale), u = mul2(d[q], w[q]);
+                    if constexpr (KEEP) {
+                        kept_u[k][q] = u;
+                        kept_x[k][q] = xh;
+                    }
+                    db[k][q] = add2(db[k][q], d[q]);
+                    dw[k][q] = fma2(d[q], xh, dw[k][q]);
+                    s1 = add2(s1, u);
+                    s2 = fma2(u, xh, s2);
+                }
             }
-        }
-        const float2 all = row_sums<TPR>(s1, s2, slots, slot);
+        const float2 p1 = apart2(s1), p2 = apart2(s2);
+        const float2 all = row_sums<SUB>(p1.x + p1.y, p2.x + p2.y, slots, slot);
         slot ^= 1;
-        const float c1 = all.x * inv, c2 = all.y * inv;
+        const Two c1 = both(-all.x * inv), c2 = both(-all.y * inv);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (lane + k * TPR >= nv) break;
-            float s[8] = {}, w[8], x[8], d[8];
-            bf_unpack8(w4[k], w);
-            bf_unpack8(ld_shared(here + k * THREADS * 16), d);
-            bf_unpack8(ld_shared(here + k * THREADS * 16 + N), x);
-            if (p_s) bf_unpack8(ld_shared(here + k * THREADS * 16 + 2 * N), s);
+            if (!in || lane + k * apart >= nv) break;
+            Two s[4] = {}, xh[4], v[4];                     // v: u - mean(u)
+            if constexpr (KEEP) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const float xh = (x[q] - mean) * rstd;
-                s[q] = fmaf(rstd, fmaf(-xh, c2, fmaf(d[q], w[q], -c1)), s[q]);
+                for (int q = 0; q < 4; ++q) {
+                    xh[q] = kept_x[k][q];
+                    v[q] = add2(kept_u[k][q], c1);
+                }
+            } else {
+                Two w[4], x[4], d[4];
+                bf_unpack_twos(w4[k], w);
+                bf_unpack_twos(ld_shared(here + k * threads * 16), d);
+                bf_unpack_twos(ld_shared(here + k * threads * 16 + N), x);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    xh[q] = mul2(add2(x[q], less), scale);
+                    v[q] = fma2(d[q], w[q], c1);
+                }
             }
-            st16_stream(p_o + k * TPR * 8, bf_pack8(s));
+            if (p_s) bf_unpack_twos(ld_shared(here + k * threads * 16 + 2 * N), s);
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 r = apart2(fma2(scale, fma2(xh[q], c2, v[q]), s[q]));
+                o[q] = bf_pack(r.x, r.y);
+            }
+            st16_stream(p_o + k * apart * 8, make_uint4(o[0], o[1], o[2], o[3]));
         }
         stage = stage == (S - 1) * STAGE ? 0 : stage + STAGE;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.parts) return;
     float* part = a.parts + (int64_t)blockIdx.x * 2 * a.D;
-    if constexpr (GROUPS == 1) {
+    if constexpr (SUB == 0) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * TPR;
+            const int c = lane + k * apart;
             if (c < nv)
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    part[c * 8 + q] = dw[k][q];
-                    part[a.D + c * 8 + q] = db[k][q];
+                for (int q = 0; q < 4; ++q) {
+                    *reinterpret_cast<float2*>(part + c * 8 + 2 * q) = apart2(dw[k][q]);
+                    *reinterpret_cast<float2*>(part + a.D + c * 8 + 2 * q) = apart2(db[k][q]);
                 }
         }
     } else {
-        __shared__ float all[GROUPS][TPR * NV * 8];
+        // (the ring is free once every thread's copies have landed)
+        float* all = reinterpret_cast<float*>(ring);          // [kRows][SUB * NV * 8]
+        constexpr int kWidth = SUB * NV * 8;
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
+            __syncthreads();
 #pragma unroll
             for (int k = 0; k < NV; ++k)
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    all[group][(lane + k * TPR) * 8 + q] = side ? db[k][q] : dw[k][q];
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float2*>(all + W::row() * kWidth + (lane + k * SUB) * 8 + 2 * q) =
+                        apart2(side ? db[k][q] : dw[k][q]);
             __syncthreads();
-            for (int i = threadIdx.x; i < a.D; i += THREADS) {
-                float s = all[0][i];
+            for (int i = threadIdx.x; i < a.D; i += 128) {
+                float s = all[i];
 #pragma unroll
-                for (int g = 1; g < GROUPS; ++g) s += all[g][i];
+                for (int g = 1; g < W::kRows; ++g) s += all[g * kWidth + i];
                 part[side * a.D + i] = s;
             }
-            __syncthreads();
         }
     }
 }
@@ -404,25 +499,18 @@ __global__ void __launch_bounds__(kJoinThreads)
     }
 }
 
-// Blocks of a form of k_layer_norm_grad that fit on an SM, per device (0: not asked yet).
-template <int TPR, int NV>
-std::atomic<int> grad_per_sm[64];
+// Blocks of a form of k_layer_norm_grad that fit on an SM, by their number of warps and per
+// device (0: not asked yet).
+template <int SUB, int NV, int MOST>
+std::atomic<int> grad_per_sm[64][33];
 
 // The most blocks that k_layer_norm_grad takes.
 int grad_blocks(int64_t T) { return (int)std::min<int64_t>(T, 1216); }
 
 }  // namespace
 
-// The widths each form takes: a row of up to 512 columns is one warp's, wider
-// ones are shared by 128 to 1024 threads with one or two vectors each.
-#define LAYER_NORM_FORMS(F)            \
-    if (D <= 256) return F(32, 1);     \
-    if (D <= 512) return F(32, 2);     \
-    if (D <= 1024) return F(128, 1);   \
-    if (D <= 2048) return F(128, 2);   \
-    if (D <= 4096) return F(256, 2);   \
-    if (D <= 8192) return F(512, 2);   \
-    return F(1024, 2)
+// The warps that a row of D columns needs with NV vectors a thread.
+static int warps_of(int32_t D, int nv) { return (D / 8 + 32 * nv - 1) / (32 * nv); }
 
 extern "C" zero_status zero_layer_norm(const uint16_t* x, int64_t x_ld, const uint16_t* residual,
                                        int64_t residual_ld, const uint16_t* weight,
@@ -473,12 +561,23 @@ extern "C" zero_status zero_layer_norm(const uint16_t* x, int64_t x_ld, const ui
     a.D = D;
     a.eps = eps;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-#define LAYER_NORM_GO(tpr, nv)                                                                 \
-    status_of(launch(k_layer_norm<tpr, nv>,                                                    \
-                     dim3((unsigned)((T + (tpr > 128 ? 1 : 128 / tpr) - 1) /                   \
-                                     (tpr > 128 ? 1 : 128 / tpr))),                            \
-                     tpr > 128 ? tpr : 128, 0, st, a))
-    LAYER_NORM_FORMS(LAYER_NORM_GO);
+    // up to 1024 columns a row is one warp's or less; wider ones get as many warps as their
+    // vectors fill, of the two numbers of vectors a thread that which leaves fewer without one
+#define LAYER_NORM_GO(sub, nv)                                                                  \
+    status_of(launch(k_layer_norm<sub, nv>,                                                     \
+                     dim3((unsigned)((T + Spread<sub>::kRows - 1) / Spread<sub>::kRows)),       \
+                     sub ? 128 : 32 * warps_of(D, nv), 0, st, a))
+    if (T <= 1216 && D > 256 && D <= 4096) return LAYER_NORM_GO(0, 1);
+    if (D <= 64) return LAYER_NORM_GO(8, 1);
+    if (D <= 128) return LAYER_NORM_GO(8, 2);
+    if (D <= 192) return LAYER_NORM_GO(8, 3);
+    if (D <= 256) return LAYER_NORM_GO(16, 2);
+    if (D <= 384) return LAYER_NORM_GO(16, 3);
+    if (D <= 512) return LAYER_NORM_GO(32, 2);
+    if (D <= 768) return LAYER_NORM_GO(32, 3);
+    if (D <= 1024) return LAYER_NORM_GO(32, 4);
+    if (D <= 12288 && 3 * warps_of(D, 3) < 4 * warps_of(D, 4)) return LAYER_NORM_GO(0, 3);
+    return LAYER_NORM_GO(0, 4);
 #undef LAYER_NORM_GO
 }
 
@@ -554,23 +653,26 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
     a.x_ld = x_ld;
     a.dx_ld = dx_ld;
     a.D = D;
-    auto run = [&](void (*kernel)(LayerNormGradArgs), int tpr, int smem, std::atomic<int>* per_sm) {
-        const int threads = tpr > 128 ? tpr : 128, groups = threads / tpr;
+    auto run = [&](void (*kernel)(LayerNormGradArgs), int sub, int nv, int most,
+                   std::atomic<int> (*per_sm)[33]) {
+        const int warps = sub ? 4 : warps_of(D, nv), threads = 32 * warps;
+        const int groups = sub ? 128 / sub : 1;
+        const int smem = grad_stages(most) * nv * threads * 48;
         // as many blocks as are resident at once: a second wave would be a short one.  With
         // few rows fewer, one an SM at least, so that there are fewer parts to join: at 16 rows
         // a group 2000 x 2048 takes 13.6 us and 1000 x 768 7.0, in as many blocks as fit 19.6
         // and 12.3; a row that is one warp's is short, and 10000 x 256 takes 10.1 us at 16, 8.0 at 4
-        const int64_t few = std::max<int64_t>(device_sms(), T / (groups * (tpr == 32 ? 4 : 16)));
+        const int64_t few = std::max<int64_t>(device_sms(), T / (groups * (sub ? 4 : 16)));
         int dev = 0;
         cudaGetDevice(&dev);
-        int fit = per_sm[dev & 63].load(std::memory_order_relaxed);
+        int fit = per_sm[dev & 63][warps].load(std::memory_order_relaxed);
         cudaError_t e = cudaSuccess;
         if (fit == 0) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
             if (e == cudaSuccess)
                 e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&fit, kernel, threads, smem);
             if (e == cudaSuccess && fit > 0)
-                per_sm[dev & 63].store(fit, std::memory_order_relaxed);
+                per_sm[dev & 63][warps].store(fit, std::memory_order_relaxed);
         }
         a.blocks = (int)std::min<int64_t>({(T + groups - 1) / groups, few, (int64_t)grad_blocks(T),
                                            (int64_t)std::max(1, fit) * device_sms()});
@@ -580,8 +682,21 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
                        kJoinThreads, 0, st, a);
         return status_of(e);
     };
-#define GRAD_GO(tpr, nv) \
-    run(k_layer_norm_grad<tpr, nv>, tpr, grad_smem<tpr, nv>(), grad_per_sm<tpr, nv>)
-    LAYER_NORM_FORMS(GRAD_GO);
+#define GRAD_GO(sub, nv, most) \
+    run(k_layer_norm_grad<sub, nv, most>, sub, nv, most, grad_per_sm<sub, nv, most>)
+    if (D <= 64) return GRAD_GO(8, 1, 128);
+    if (D <= 128) return GRAD_GO(8, 2, 128);
+    if (D <= 192) return GRAD_GO(8, 3, 128);
+    if (D <= 256) return GRAD_GO(16, 2, 128);
+    if (D <= 384) return GRAD_GO(16, 3, 128);
+    if (D <= 512) return GRAD_GO(32, 2, 128);
+    if (D <= 768) return GRAD_GO(32, 3, 128);
+    if (D <= 1024) return GRAD_GO(32, 4, 128);
+    // wider rows: 2 vectors a thread, 16 warps an SM; where that leaves one row an SM and 3
+    // vectors in 12 warps two, those (4104 columns: 86 us with 2, 75 with 3; with more vectors
+    // elsewhere, 2048 columns 83 with 2 and 91 with 4, 2056 columns 84 with 2 and 92 with 3)
+    if (D <= 8192 && 16 / warps_of(D, 2) == 1 && 12 / warps_of(D, 3) > 1) return GRAD_GO(0, 3, 192);
+    if (D <= 8192) return GRAD_GO(0, 2, 512);
+    return GRAD_GO(0, 2, 1024);
 #undef GRAD_GO
 }
