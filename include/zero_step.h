@@ -816,7 +816,7 @@ int64_t zero_policy_scratch_bytes(int64_t T, int64_t S);
  *   r = exp(old_nll - nll)  (old_nll NULL: r = 1, the tokens being this model's own),
  *   k = exp(nll - ref_nll) - (nll - ref_nll) - 1,
  *   term = -min(r A, min(max(r, 1 - clip_low), 1 + clip_high) A) + kl_coef k
- * (-0 where A is 0).  loss[s] is the sum of the terms of its tokens, kl[s] that of
+ * (without its first part where A is 0).  loss[s] is the sum of the terms of its tokens, kl[s] that of
  * k, or with average the means; clipped[s] counts the tokens whose bounded r is the
  * smaller one (decided on the exact difference of the two losses), counts[s] those that
  * count.  ref_nll may be NULL where kl_coef is 0; kl is then 0.

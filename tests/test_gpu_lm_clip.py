@@ -43,6 +43,7 @@ SETS = {
     "one": [1], "few": [7, 1, 8, 9], "tile": [8192], "around": [8191, 8192, 8193, 16385],
     "odd": [100_003, 1, 77, 0, 8_000, 0, 0, 40_961, 5, 0], "empty": [0, 0],
     "many": [3] * 200 + [1000] * 300 + [0] * 100 + [8193] * 200,
+    "some": [(k * 613) % 2999 for k in range(150)],
     "more than one launch": [k % 37 for k in range(2100)],
     "big": [30_000_001, 11, 5_000_000],
 }
@@ -141,7 +142,7 @@ def coefficient(norm, most):
 PAIRS = [(d, d) for d in TYPES] + [(torch.float16, torch.bfloat16), (torch.float32, torch.bfloat16)]
 
 
-@pytest.mark.parametrize("name", ["one", "around", "odd", "many", "more than one launch"])
+@pytest.mark.parametrize("name", ["one", "around", "odd", "some", "many", "more than one launch"])
 @pytest.mark.parametrize("dtype,to", PAIRS)
 @pytest.mark.parametrize("shifts", [(0, 0), (3, 3), (1, 2), (0, 7)])
 def test_clip(name, dtype, to, shifts):

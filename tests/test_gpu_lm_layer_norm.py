@@ -201,6 +201,25 @@ def test_rows_of_one_value(value, D):
     R.within(y[rows], want, off + R.U16 * (want.abs() + off) * 1.01)
 
 
+@pytest.mark.parametrize("D", [8, 72, 200, 264, 776, 1032, 2056, 4104, 8200])
+def test_gradient_where_the_mean_over_the_deviation_overflows(D):
+    """A row of one large value: xhat is 0, mean * rstd is past fp32's range, and the threads
+    past the row's end must not make anything of that."""
+    g = R.gen(D)
+    T = 3
+    x = torch.zeros((T, D), dtype=torch.bfloat16, device="cuda")
+    x[1] = 2.0 ** 125
+    dy, w = R.bf16(g, (T, D)), R.bf16(g, (D,))
+    mean, rstd = x[:, 0].float().contiguous(), torch.full((T,), 300.0, device="cuda")
+    dx, dw, db = backward(dy, x, mean, rstd, w)
+    u = dy.to(R.F) * w.to(R.F)
+    want = 300 * (u - u.mean(1, keepdim=True))
+    off = (DEEP + 16 * R.U32) * 300 * (u.abs() + u.abs().mean(1, keepdim=True))
+    R.within(dx, want, off + R.U16 * (want.abs() + off))
+    assert not dw.any()
+    R.within(db, dy.to(R.F).sum(0), (R.U16 + 8 * R.U32) * dy.to(R.F).abs().sum(0))
+
+
 def test_no_tokens():
     e = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, dtype=torch.bfloat16, device="cuda")

@@ -45,7 +45,7 @@ struct Entry {
     uint8_t pad;
 };
 
-constexpr int kFew = 64, kMany = 960;                // entries of a launch: 2 KB, 30 KB of arguments
+constexpr int kFew = 64, kSome = 256, kMany = 960;   // entries of a launch: 2, 8, 30 KB of arguments
 
 template <int N>
 struct ClipArgs {
@@ -627,6 +627,8 @@ extern "C" zero_status zero_grad_norm(const zero_tensor* tensors, int32_t count,
     double* s = static_cast<double*>(scratch);
     return status_of(count <= kFew
                          ? norm_launches<kFew>(tensors, count, norm, norms, s, dev_status, st)
+                     : count <= kSome
+                         ? norm_launches<kSome>(tensors, count, norm, norms, s, dev_status, st)
                          : norm_launches<kMany>(tensors, count, norm, norms, s, dev_status, st));
 }
 
@@ -650,5 +652,7 @@ extern "C" zero_status zero_grad_clip(const zero_tensor* tensors, const zero_ten
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return status_of(count <= kFew
                          ? clip_launches<kFew>(tensors, outs, count, norm, max_norm, st)
+                     : count <= kSome
+                         ? clip_launches<kSome>(tensors, outs, count, norm, max_norm, st)
                          : clip_launches<kMany>(tensors, outs, count, norm, max_norm, st));
 }
