@@ -120,7 +120,9 @@ def test_gradient(T, D):
 
 @pytest.mark.parametrize("T,D", [(12001, 256), (12001, 264), (12001, 512), (4001, 768),
                                  (4001, 1024), (4001, 2048), (2001, 4096), (1001, 8192),
-                                 (601, 16384)])
+                                 (601, 16384), (20001, 64), (9001, 120), (6001, 192), (3001, 328),
+                                 (7001, 1304), (4001, 2056), (3001, 2800), (3003, 4104), (1501, 5608),
+                                 (153, 1032), (305, 2048), (461, 1304)])
 def test_gradient_with_more_rows_than_fit_at_once(T, D):
     check_gradient(T, D)
 

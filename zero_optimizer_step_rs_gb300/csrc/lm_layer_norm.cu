@@ -9,8 +9,8 @@
 //
 // Bound by HBM traffic: forward 2+2 bytes an element read and 2+2 written, gradient
 // 2+2+2 read and 2 written.  Measured, one GB300, 32768 x 2048: forward 79 us (6.8 TB/s, the
-// rate of a copy), gradient 84 us (6.4 TB/s, 4 of them the join of dw and db).  333 x 768: 2.4 us
-// and 4.4 us, one launch and two.
+// rate of a copy), gradient 80 us (6.7 TB/s, 3 of them the join of dw and db).  333 x 768: 2.4 us
+// and 4.2 us, one launch and two.
 #include "lm_common.cuh"
 
 namespace {
@@ -168,27 +168,31 @@ struct LayerNormGradArgs {
     float* parts;                    // [blocks][2][D]; null: neither is wanted
     int64_t T, dy_ld, dsum_ld, x_ld, dx_ld;
     int32_t D, blocks;
+    int32_t apart, groups;           // SUB = 0: threads of a row, rows of a block at a time,
+    int32_t near;                    // and whether these lie one behind the other
 };
 
-// The sums of two values over the threads of a row.  `slot` alternates from row to row, so that
-// one barrier a row is enough.
+// The sums of two values over the threads of a row: a warp's lanes or less, or the `warps` warps
+// of a group, whose first is warp `base` of the block and which has a barrier of its own.  `slot`
+// alternates from row to row, so that one barrier a row is enough.
 template <int SUB>
-__device__ __forceinline__ float2 row_sums(float x, float y, float2 (*slots)[32], int slot)
+__device__ __forceinline__ float2 row_sums(float x, float y, float2 (*slots)[32], int slot, int group,
+                                           int base, int warps)
 {
     x = lane_sum<SUB>(x);
     y = lane_sum<SUB>(y);
     if constexpr (SUB == 0) {
-        const int lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
+        const int lane = threadIdx.x & 31;
         if (lane == 0) slots[slot][threadIdx.x >> 5] = make_float2(x, y);
-        __syncthreads();
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
         if (warps > 8) {
-            const float2 p = lane < warps ? slots[slot][lane] : make_float2(0.0f, 0.0f);
+            const float2 p = lane < warps ? slots[slot][base + lane] : make_float2(0.0f, 0.0f);
             x = warp_sum(p.x);
             y = warp_sum(p.y);
         } else {
             x = y = 0.0f;
             for (int k = 0; k < warps; ++k) {
-                const float2 p = slots[slot][k];
+                const float2 p = slots[slot][base + k];
                 x += p.x;
                 y += p.y;
             }
@@ -214,8 +218,8 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t at)
 
 // Two fp32 values in one register pair, which add, multiply and fma take in one instruction
 // (each value rounded by itself).  The gradient's rows filled 56 % of the issue slots without, and
-// rows that leave lanes without a vector more: 32768 x 2048 takes 84 us with pairs and 89
-// without, 30000 x 2056 90 and 97.
+// rows that leave lanes without a vector more: in blocks of one row 32768 x 2048 took 84 us with
+// pairs and 89 without, 30000 x 2056 90 and 97.
 using Two = unsigned long long;
 __device__ __forceinline__ Two two(float lo, float hi)
 {
@@ -265,7 +269,7 @@ constexpr int kMostSmem = 225 * 1024;                // of a block, beside its s
 constexpr int grad_blocks_min(int sub, int nv, int most)
 {
     if (sub) return nv == 1 ? 7 : nv == 2 ? 4 : 3;
-    return most <= 192 ? 2 : 1;
+    return 1;
 }
 
 // A row's threads walk over many rows and keep the sums of dw and db in
@@ -284,10 +288,13 @@ __global__ void __launch_bounds__(SUB ? 128 : MOST, grad_blocks_min(SUB, NV, MOS
     pdl_enter();
     extern __shared__ __align__(16) uint8_t ring[];
     __shared__ float2 slots[2][32];
-    const int lane = W::lane(), apart = W::threads();        // between a thread's vectors
+    // `apart`: between a thread's vectors
+    const int apart = SUB ? SUB : a.apart, groups = SUB ? W::kRows : a.groups;
+    const int group = threadIdx.x / apart, lane = threadIdx.x % apart;
     const int nv = a.D >> 3;
-    const int64_t step = (int64_t)gridDim.x * W::kRows;
-    const int64_t first = (int64_t)blockIdx.x * W::kRows + W::row();
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t first = SUB || a.near ? (int64_t)blockIdx.x * groups + group
+                                        : blockIdx.x + (int64_t)group * gridDim.x;
     const float inv = 1.0f / (float)a.D;
 
     // where the row to ask for next lies; a thread past the row's end asks for
@@ -337,12 +344,12 @@ __global__ void __launch_bounds__(SUB ? 128 : MOST, grad_blocks_min(SUB, NV, MOS
         rstd_next = a.rstd[first];
     }
     uint16_t* p_o = a.dx + first * a.dx_ld + lane * 8;
-    // (all of a block's groups of threads go on while one has a row: the sums take whole warps)
+    // (the groups that share a warp go on while one of the block's has a row: the sums take whole
+    // warps)
     int64_t t = first;
-    for (int64_t top = (int64_t)blockIdx.x * W::kRows; top < a.T;
+    for (int64_t top = SUB && SUB < 32 ? (int64_t)blockIdx.x * groups : first; top < a.T;
          top += step, t += step, p_o += step * a.dx_ld) {
-        const bool in = SUB == 0 || SUB == 32 || t < a.T;
-        if ((SUB == 32) && t >= a.T) break;                   // a whole warp
+        const bool in = !(SUB && SUB < 32) || t < a.T;
         const float mean = mean_next, rstd = rstd_next;
         if (t + step < a.T) {
             mean_next = a.mean[t + step];
@@ -352,8 +359,8 @@ __global__ void __launch_bounds__(SUB ? 128 : MOST, grad_blocks_min(SUB, NV, MOS
             stage == 0 ? (S - 1) * STAGE : stage - STAGE);
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
         // xhat and dy * w are kept for the row's second part where the registers allow it, else
-        // made again from what shared memory holds (2056 columns: 84 us kept, 90 made again;
-        // 64 and 1024 columns: 91 and 103 kept, 82 and 76 made again)
+        // made again from what shared memory holds (30000 x 2056: 84 us kept, 90 made again; 64 and
+        // 1024 columns: 91 and 103 kept, 82 and 76 made again)
         const uint32_t here = mine + stage;
         const Two less = both(-mean), scale = both(rstd);
         Two s1 = 0, s2 = 0, kept_u[KEEP ? NV : 1][4], kept_x[KEEP ? NV : 1][4];
@@ -380,7 +387,8 @@ __global__ void __launch_bounds__(SUB ? 128 : MOST, grad_blocks_min(SUB, NV, MOS
                 }
             }
         const float2 p1 = apart2(s1), p2 = apart2(s2);
-        const float2 all = row_sums<SUB>(p1.x + p1.y, p2.x + p2.y, slots, slot);
+        const float2 all = row_sums<SUB>(p1.x + p1.y, p2.x + p2.y, slots, slot, group,
+                                        group * (apart >> 5), apart >> 5);
         slot ^= 1;
         const Two c1 = both(-all.x * inv), c2 = both(-all.y * inv);
 #pragma unroll
@@ -418,37 +426,26 @@ __global__ void __launch_bounds__(SUB ? 128 : MOST, grad_blocks_min(SUB, NV, MOS
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.parts) return;
     float* part = a.parts + (int64_t)blockIdx.x * 2 * a.D;
-    if constexpr (SUB == 0) {
+    // the groups' sums, in order (the ring is free once every thread's copies have landed)
+    float* all = reinterpret_cast<float*>(ring);              // [groups][width]
+    const int width = apart * NV * 8;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = lane + k * apart;
-            if (c < nv)
+    for (int side = 0; side < 2; ++side) {
+        __syncthreads();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    *reinterpret_cast<float2*>(part + c * 8 + 2 * q) = apart2(dw[k][q]);
-                    *reinterpret_cast<float2*>(part + a.D + c * 8 + 2 * q) = apart2(db[k][q]);
-                }
-        }
-    } else {
-        // (the ring is free once every thread's copies have landed)
-        float* all = reinterpret_cast<float*>(ring);          // [kRows][SUB * NV * 8]
-        constexpr int kWidth = SUB * NV * 8;
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < NV; ++k)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *reinterpret_cast<float2*>(all + W::row() * kWidth + (lane + k * SUB) * 8 + 2 * q) =
-                        apart2(side ? db[k][q] : dw[k][q]);
-            __syncthreads();
-            for (int i = threadIdx.x; i < a.D; i += 128) {
-                float s = all[i];
-#pragma unroll
-                for (int g = 1; g < W::kRows; ++g) s += all[g * kWidth + i];
-                part[side * a.D + i] = s;
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<float2*>(all + group * width + (lane + k * apart) * 8 + 2 * q) =
+                    apart2(side ? db[k][q] : dw[k][q]);
+        __syncthreads();
+        for (int i = threadIdx.x * 4; i < a.D; i += threads * 4) {
+            float4 sum = *reinterpret_cast<const float4*>(all + i);
+            for (int g = 1; g < groups; ++g) {
+                const float4 y = *reinterpret_cast<const float4*>(all + g * width + i);
+                sum.x += y.x; sum.y += y.y; sum.z += y.z; sum.w += y.w;
             }
+            *reinterpret_cast<float4*>(part + side * a.D + i) = sum;
         }
     }
 }
@@ -660,14 +657,17 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
     a.D = D;
     auto run = [&](void (*kernel)(LayerNormGradArgs), int sub, int nv, int most,
                    std::atomic<int> (*per_sm)[33]) {
-        const int warps = sub ? 4 : warps_of(D, nv), threads = 32 * warps;
-        const int groups = sub ? 128 / sub : 1;
+        // up to 1024 columns blocks of 128 threads, several on an SM; else one block an SM, with as
+        // many rows at a time as its registers allow: fewer parts to join than with a block for
+        // each (2000 x 2048 in blocks of a row 13.2 us)
+        a.apart = sub ? sub : 32 * warps_of(D, nv);
+        a.groups = sub ? 128 / sub : std::max(1, most / a.apart);
+        const int warps = a.apart * a.groups / 32, threads = 32 * warps;
         const int smem = grad_stages(most) * nv * threads * 48;
-        // as many blocks as are resident at once: a second wave would be a short one.  With
-        // few rows fewer, one an SM at least, so that there are fewer parts to join: at 16 rows
-        // a group 2000 x 2048 takes 13.6 us and 1000 x 768 7.0, in as many blocks as fit 19.6
-        // and 12.3; a row that is one warp's is short, and 10000 x 256 takes 10.1 us at 16, 8.0 at 4
-        const int64_t few = std::max<int64_t>(device_sms(), T / (groups * (sub ? 4 : 16)));
+        // as many blocks as are resident at once: a second wave would be a short one.  Where a row
+        // is a warp's or less at 4 rows a group at least, but one block an SM: 10000 x 256 takes
+        // 8.0 us so and 10.1 with 16 rows, 333 x 768 4.3 us, in as many blocks as fit 5.5
+        const int64_t few = std::max<int64_t>(device_sms(), T / (a.groups * 4));
         int dev = 0;
         cudaGetDevice(&dev);
         int fit = per_sm[dev & 63][warps].load(std::memory_order_relaxed);
@@ -679,8 +679,13 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
             if (e == cudaSuccess && fit > 0)
                 per_sm[dev & 63][warps].store(fit, std::memory_order_relaxed);
         }
-        a.blocks = (int)std::min<int64_t>({(T + groups - 1) / groups, few, (int64_t)grad_blocks(T),
+        a.blocks = (int)std::min<int64_t>({sub ? (T + a.groups - 1) / a.groups : T, few,
+                                           (int64_t)grad_blocks(T),
                                            (int64_t)std::max(1, fit) * device_sms()});
+        // Rows of a block at a time: few are spread over all blocks; of many those that share the
+        // cache line between them go to one block (30000 x 2056 90 us spread, 85 near;
+        // 32768 x 2048 80 and 82)
+        a.near = T > 4 * (int64_t)a.blocks * a.groups && (dy_ld | x_ld | dx_ld) % 64 != 0;
         if (e == cudaSuccess) e = launch(kernel, dim3((unsigned)a.blocks), threads, smem, st, a);
         if (e == cudaSuccess && wanted)
             e = launch(k_layer_norm_join, dim3((unsigned)((2 * D + kJoinCols - 1) / kJoinCols)),
@@ -698,9 +703,9 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
     if (D <= 768) return GRAD_GO(32, 3, 128);
     if (D <= 1024) return GRAD_GO(32, 4, 128);
     // wider rows: 2 vectors a thread, 16 warps an SM; where that leaves one row an SM and 3
-    // vectors in 12 warps two, those (4104 columns: 86 us with 2, 75 with 3; with more vectors
+    // vectors in 12 warps two, those (12000 x 4104: 86 us with 2, 75 with 3; with more vectors
     // elsewhere, 2048 columns 83 with 2 and 91 with 4, 2056 columns 84 with 2 and 92 with 3)
-    if (D <= 8192 && 16 / warps_of(D, 2) == 1 && 12 / warps_of(D, 3) > 1) return GRAD_GO(0, 3, 192);
+    if (D <= 8192 && 16 / warps_of(D, 2) == 1 && 12 / warps_of(D, 3) > 1) return GRAD_GO(0, 3, 384);
     if (D <= 8192) return GRAD_GO(0, 2, 512);
     return GRAD_GO(0, 2, 1024);
 #undef GRAD_GO
