@@ -1,9 +1,9 @@
-// lm_common.cuh - what the language-model operators (lm_embed.cu, lm_norm.cu,
-// lm_xent.cu) share: bf16 vectors, launches, argument checks.
+// lm_common.cuh - what the language-model operators (lm_*.cu) share: bf16 vectors,
+// launches, argument checks.
 //
-// Conventions of these three files: matrices are row-major with the columns
+// Conventions: matrices are row-major with the columns
 // contiguous and a row stride ("ld") in elements; widths and strides are
-// multiples of 8 and pointers are 16-byte aligned, so that every row starts on
+// multiples of 8 and pointers to matrices are 16-byte aligned, so that every row starts on
 // a 16-byte vector of 8 bf16 values.  Row offsets are 64-bit.
 #ifndef ZERO_LM_COMMON_CUH
 #define ZERO_LM_COMMON_CUH

@@ -14,7 +14,8 @@ views of a replica or a gradient buffer at the tensor's offset:
 
     grad_table = grads[0][off:off + V * D].view(V, D)
 
-Token ids are int32 or int64; negative ones take part in nothing.
+Token ids are int32 or int64; negative ones take part in nothing.  Losses of tokens and
+sequences are fp32 vectors, gradients given as a list may be bf16, fp16 or fp32.
 """
 from __future__ import annotations
 
