@@ -865,8 +865,8 @@ typedef struct {
 int64_t zero_grad_norm_scratch_bytes(int32_t count);
 
 /*
- * norms[i] = the 2-norm of tensor i (may be NULL), norm[0] = that of all of them.  A
- * thread's squares are added in fp32, the threads' and blocks' sums in 64 bits, in an order
+ * norms[i] = the 2-norm of tensor i (may be NULL), norm[0] = that of all of them.  The
+ * squares are added in fp32 within a block, the blocks' sums in 64 bits, in an order
  * that the sizes alone decide; a part whose sum of squares overflows or vanishes in
  * fp32 is taken again relative to its largest value, so that every finite
  * input has the norm that fp32 can hold.  A norm that is not finite sets

@@ -1,8 +1,8 @@
 """The norm of many tensors and their clipping on the GPU against 64-bit forms.
 
-A thread adds up to 32 squares of a tile and then the tiles of its block's run (at most a
-few in these sizes), all positive, so a sum of squares is off by at most DEEP of itself
-and its root by half of that and one rounding."""
+A thread adds up to 32 squares of a tile, the tiles without loss, and then come 5 halvings and 8
+warps: all positive, so a sum of squares is off by under 64 U32 of itself (DEEP) and its root
+by half of that and one rounding."""
 import math
 
 import pytest
@@ -179,6 +179,44 @@ def test_clip_big():
     # each element was rounded once more
     after = want_norms(t)[0].item()
     assert abs(after - 0.5) <= 0.5 * 2 * (DEEP + 1e-6)
+
+
+def test_more_elements_than_32_bits_count():
+    n = (1 << 31) + 8_195
+    flat = torch.ones(n + 3, dtype=torch.bfloat16, device="cuda")
+    flat[-1] = 3.0
+    t = [flat[:3], flat[3:]]
+    norm, norms = norms_of(t)
+    want = (n + 3 + 8) ** 0.5
+    assert abs(norm.item() - want) <= DEEP * want and norms[0].item() == pytest.approx(3 ** 0.5)
+    z.zero_grad_clip(t, norm, 0.5 * norm.item())
+    assert flat[0].item() == 0.5 and flat[-2].item() == 0.5 and flat[-1].item() == 1.5
+    assert flat[1 << 31].item() == 0.5
+    again = norms_of(t)[0].item()
+    assert abs(again - 0.5 * want) <= DEEP * want
+
+
+def test_the_same_tensor_twice():
+    x = torch.full((1000,), 3.0, device="cuda")
+    norm, norms = norms_of([x, x])
+    assert norm.item() == pytest.approx((2000 * 9) ** 0.5, rel=1e-6)
+    assert norms[0].item() == norms[1].item()
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its own scratch and outputs."""
+    sets = [views(R.gen(k), [200_003, 77, 1_000_001], torch.float32) for k in range(2)]
+    want = [norms_of(t) for t in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    rooms = [torch.empty(z.zero_grad_norm_scratch_bytes(3), dtype=torch.uint8, device="cuda") for _ in sets]
+    got = [(torch.zeros(1, device="cuda"), torch.zeros(3, device="cuda")) for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for t, s, room, (norm, norms) in zip(sets, streams, rooms, got):
+            z.zero_grad_norm(t, norm, room, norms=norms, stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_overlapping_outputs_are_refused():

@@ -437,6 +437,58 @@ def test_no_sequences_and_no_tokens():
     assert not (l6.any() or kl.any() or clipped.any() or n6.any())
 
 
+def test_tokens_up_to_the_last_that_32_bits_count():
+    """2^31 - 1024 tokens: addresses past 32 bits, counts that fp32 does not hold."""
+    T = (1 << 31) - 1024
+    cut = [1, 1 << 30, T - 301, T - 300]
+    off = torch.tensor([0, *cut[:3], T], dtype=torch.int32, device="cuda")
+    targets = torch.zeros(T, dtype=torch.int32, device="cuda")
+    nll = torch.zeros(T, device="cuda")
+    nll[-200:] = 2.0
+    targets[-100:] = -1
+    nll[-50:] = NAN
+    nll[(1 << 30) + 5] = 1e6
+    dnll = torch.full((T,), 9.0, device="cuda")
+    f = lambda n: torch.zeros(n, device="cuda")  # noqa: E731
+    loss, slope, ratios, counts = f(2), f(2), f(4), torch.zeros(4, dtype=torch.int32, device="cuda")
+    lengths = [1, (1 << 30) - 1, T - 301 - (1 << 30), 301 - 100]
+    for average in (False, True):
+        room = scratch_of(z.zero_preference_scratch_bytes, T, 2)
+        z.zero_preference(nll, None, targets, off, loss, slope, ratios, counts, room, average=average)
+        assert counts.tolist() == lengths
+        n = [lengths[2], lengths[3]] if average else [1, 1]
+        assert ratios.tolist() == pytest.approx([0.0, 0.0, -1e6 / n[0], -200.0 / n[1]], rel=1e-6)
+        z.zero_preference_grad(targets, off, slope, counts, torch.ones(2, device="cuda"), dnll, average=average)
+        n = lengths[1] if average else 1
+        assert dnll[1].item() == dnll[(1 << 30) - 1].item() == pytest.approx(-0.05 / n, rel=1e-6)
+        assert not dnll[-100:].any() and dnll[-101].item() < 0
+    loss, kl, cut_n, n4 = f(4), f(4), *(torch.zeros(4, dtype=torch.int32, device="cuda") for _ in range(2))
+    room = scratch_of(z.zero_policy_scratch_bytes, T, 4)
+    adv = torch.tensor([1.0, 2.0, 3.0, -4.0], device="cuda")
+    z.zero_policy(nll, None, None, adv, targets, off, loss, kl, cut_n, n4, room)
+    assert n4.tolist() == lengths and loss.tolist() == [-1.0, -2.0, -3.0, 4.0]
+    z.zero_policy_grad(nll, None, None, adv, targets, off, n4, torch.ones(4, device="cuda"), dnll)
+    assert dnll[-101].item() == pytest.approx(-4 / lengths[3], rel=1e-6) and not dnll[-100:].any()
+    assert dnll[0].item() == 1.0 and dnll[5].item() == pytest.approx(2 / lengths[1], rel=1e-6)
+
+
+def test_two_calls_at_once():
+    """On two streams, each with its own scratch and outputs."""
+    cases = [Case("ragged", seed=k) for k in range(2)]
+    dloss = [torch.ones(c.S, device="cuda") for c in cases]
+    want = [policy(c, dloss=d) for c, d in zip(cases, dloss)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for c, d, s in zip(cases, dloss, streams):
+            with torch.cuda.stream(s):
+                got.append(policy(c, dloss=d))
+    torch.cuda.synchronize()
+    for k, result in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(result, want[k % 2]))
+
+
 @pytest.mark.parametrize("name", ["gaps", "two long"])
 def test_another_stream_and_a_graph(name):
     c = Case(name)

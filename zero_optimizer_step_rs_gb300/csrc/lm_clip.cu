@@ -220,8 +220,30 @@ __device__ __forceinline__ uint32_t block_max(uint32_t x)
     return m;
 }
 
-// The sum of squares over tiles [lo, hi) of a tensor where fp32 squares overflow or
-// vanish: relative to the largest value's power of two.
+// A thread's sum of squares over tiles [lo, hi) of a tensor, each value times s1 and s2 first
+// (SCALED).  A tile's squares are added by themselves, and what the tiles' addition rounds away
+// is kept beside it: a block may have thousands of tiles.
+template <int TYPE, bool SCALED>
+__device__ __forceinline__ float thread_squares(const void* p, int64_t numel, int head, int64_t lo,
+                                                int64_t hi, float s1, float s2)
+{
+    float sum = 0.0f, rest = 0.0f;
+#pragma unroll 1
+    for (int64_t t = lo; t < hi; ++t) {
+        float part = 0.0f;
+        for_elements<TYPE>(p, numel, head, t, [&](float x) {
+            if (SCALED) x = x * s1 * s2;
+            part = fmaf(x, x, part);
+        });
+        const float next = sum + part, back = next - sum;
+        rest += (sum - (next - back)) + (part - back);
+        sum = next;
+    }
+    return sum + rest;
+}
+
+// The block's sum of squares where fp32 squares overflow or vanish: relative to the largest
+// value's power of two.
 template <int TYPE>
 __device__ __noinline__ double scaled_sum(const void* p, int64_t numel, int head, int64_t lo,
                                           int64_t hi)
@@ -239,32 +261,16 @@ __device__ __noinline__ double scaled_sum(const void* p, int64_t numel, int head
     frexp(top, &power);
     // in two steps: 2^-power alone may be past fp32
     const float s1 = ldexpf(1.0f, -power / 2), s2 = ldexpf(1.0f, -power - -power / 2);
-    float s = 0.0f;
-#pragma unroll 1
-    for (int64_t t = lo; t < hi; ++t) {
-        float part = 0.0f;
-        for_elements<TYPE>(p, numel, head, t, [&](float x) {
-            x = x * s1 * s2;
-            part = fmaf(x, x, part);
-        });
-        s += part;
-    }
-    return ldexp((double)block_sum(s), 2 * power);
+    return ldexp((double)block_sum(thread_squares<TYPE, true>(p, numel, head, lo, hi, s1, s2)),
+                 2 * power);
 }
 
 template <int TYPE>
 __device__ __forceinline__ double sum_squares(const void* p, int64_t numel, int head, int64_t lo,
                                               int64_t hi)
 {
-    float s = 0.0f;
-#pragma unroll 1
-    for (int64_t t = lo; t < hi; ++t) {
-        // a tile's squares by themselves, so that the long sum has few terms
-        float part = 0.0f;
-        for_elements<TYPE>(p, numel, head, t, [&](float x) { part = fmaf(x, x, part); });
-        s += part;
-    }
-    s = block_sum(s);
+    const float s =
+        block_sum(thread_squares<TYPE, false>(p, numel, head, lo, hi, 1.0f, 1.0f));
     // (each of the sum's terms was off by at most 2^-150: under 2^-24 of it from here up)
     if (s >= 0x1p-80f && s <= 0x1p120f) return (double)s;
     return scaled_sum<TYPE>(p, numel, head, lo, hi);
