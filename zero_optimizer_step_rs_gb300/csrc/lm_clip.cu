@@ -12,9 +12,10 @@
 // device, and a captured graph holds it.
 //
 // Bound by HBM: the norm reads every element once, the clipping once more and writes it, since
-// the first output depends on the last input.  Measured, one GB300, 146 tensors of 1.24 G elements:
-// the norm of bf16 ones 351 us (7.05 TB/s), norm and clipping of fp32 ones into bf16 1776 us
-// (6.96 TB/s of the 10 bytes).  37 tensors of 10^6 elements: 4.4 and 7.7 us, two and three launches.
+// the first output depends on the last input.  Measured, one GB300, 146 tensors of 1.24 G
+// elements: the norm of bf16 ones 344 to 350 us (7.1 TB/s), norm and clipping of fp32 ones into
+// bf16 1763 to 1778 us (7.0 TB/s of the 10 bytes).  37 tensors of 10^6 elements: 4.4 and 7.7 us,
+// two and three launches.
 #include "lm_common.cuh"
 
 #include <cuda_fp16.h>
@@ -28,9 +29,12 @@ using namespace lm;
 
 constexpr int kThreads = 256;
 // Elements of a tile, 4 vectors of a thread: with 2 vectors the norm of 1.24 G bf16 elements takes
-// 443 us, with 1 573 (351 with 4), since a block waits for a tile before it asks for the next.
+// 443 us, with 1 573 (350 with 4), since a block waits for a tile before it asks for the next.
 constexpr int kTile = 8192;
-constexpr int kMaxBlocks = 1216;                     // 8 for each of 152 SMs
+// The most blocks of a launch, for each of 152 SMs 4, which are resident at once, and 8.  The norm
+// of 30 M bf16 elements takes 14.5 us in 4 and 16.3 in 8, norm and clipping of 1.24 G fp32 ones 1763
+// us with 8 for the clipping and 1787 with 4.
+constexpr int kNormBlocks = 608, kClipBlocks = 1216;
 constexpr int kJoinThreads = 128;
 constexpr int kNoVectors = 255;                      // a head: input and output never have one together
 constexpr int64_t kMaxNumel = 1ll << 40, kMaxTotal = 1ll << 43;
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_grad_clip(const __grid_constant
     if (coef == 1.0f && a.in_place) return;
     const int64_t begin = (int64_t)blockIdx.x * a.per_block;
     int64_t tile = min(begin + a.per_block, a.tiles) - 1;
-    // backwards: the end of a block's run is what the norm's pass has read last
+    // backwards: the ends of the norm's blocks' runs are what it has read last
     int i = tensor_of(a, tile);
 #pragma unroll 1
     for (; tile >= begin; --tile) {
@@ -531,12 +535,14 @@ uint8_t head_of(const zero_tensor& t, const zero_tensor* out)
 
 int64_t slots(int64_t count)
 {
-    return count + ((count + kMany - 1) / kMany) * kMaxBlocks;
+    return count + ((count + kMany - 1) / kMany) * kNormBlocks;
 }
 
-// The launches of a call, each with at most N tensors: f(args, blocks, first tensor).
+// The launches of a call, each with at most N tensors in `most` blocks: f(args, blocks, first
+// tensor).
 template <int N, typename F>
-cudaError_t for_launches(const zero_tensor* t, const zero_tensor* outs, int32_t count, F&& f)
+cudaError_t for_launches(const zero_tensor* t, const zero_tensor* outs, int32_t count, int most,
+                         F&& f)
 {
     ClipArgs<N> a;
     for (int32_t at = 0; at < count; at += N) {
@@ -558,7 +564,7 @@ cudaError_t for_launches(const zero_tensor* t, const zero_tensor* outs, int32_t 
             if (x.numel) a.last_full = i;
             if (x.numel) a.tiles += std::max<int64_t>(1, (x.numel - before + kTile - 1) / kTile);
         }
-        a.per_block = (int32_t)std::max<int64_t>(1, (a.tiles + kMaxBlocks - 1) / kMaxBlocks);
+        a.per_block = (int32_t)std::max<int64_t>(1, (a.tiles + most - 1) / most);
         const unsigned blocks = (unsigned)((a.tiles + a.per_block - 1) / a.per_block);
         if (cudaError_t e = f(a, blocks, at)) return e;
     }
@@ -569,11 +575,11 @@ template <int N>
 cudaError_t norm_launches(const zero_tensor* t, int32_t count, float* norm, float* norms,
                           double* scratch, int32_t* status, cudaStream_t st)
 {
-    return for_launches<N>(t, nullptr, count, [&](ClipArgs<N>& a, unsigned blocks, int32_t at) {
+    return for_launches<N>(t, nullptr, count, kNormBlocks, [&](ClipArgs<N>& a, unsigned blocks, int32_t at) {
         a.norm = norm;
         a.norms = norms ? norms + at : nullptr;
         a.total = scratch;
-        a.parts = scratch + 2 + at + (int64_t)(at / N) * kMaxBlocks;
+        a.parts = scratch + 2 + at + (int64_t)(at / N) * kNormBlocks;
         a.status = status;
         a.first = at == 0;
         a.last = at + N >= count;
@@ -592,7 +598,7 @@ template <int N>
 cudaError_t clip_launches(const zero_tensor* t, const zero_tensor* outs, int32_t count,
                           const float* norm, float max_norm, cudaStream_t st)
 {
-    return for_launches<N>(t, outs, count, [&](ClipArgs<N>& a, unsigned blocks, int32_t) {
+    return for_launches<N>(t, outs, count, kClipBlocks, [&](ClipArgs<N>& a, unsigned blocks, int32_t) {
         a.norm_in = norm;
         a.max_norm = max_norm;
         a.in_place = outs == nullptr;
