@@ -49,7 +49,10 @@ struct Entry {
     uint8_t pad;
 };
 
-constexpr int kFew = 64, kSome = 256, kMany = 960;   // entries of a launch: 2, 8, 30 KB of arguments
+// Entries of a launch: 2, 8, 30 KB of arguments.  A few hundred launches of 30 KB fill the queue, and
+// the host waits for the GPU (146 tensors: 6.5 us a call of the norm in 8 KB, 200 in 30, behind a long
+// kernel).
+constexpr int kFew = 64, kSome = 256, kMany = 960;
 
 template <int N>
 struct ClipArgs {

@@ -563,8 +563,12 @@ extern "C" zero_status zero_layer_norm(const uint16_t* x, int64_t x_ld, const ui
     a.D = D;
     a.eps = eps;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    // up to 1024 columns a row is one warp's or less; wider ones get as many warps as their
-    // vectors fill, of the two numbers of vectors a thread that which leaves fewer without one
+    // Up to 1024 columns a row is one warp's or less, with lanes that hold as many vectors as leave
+    // few without one: 500000 x 128 takes 75 us in 8 lanes and 81 in 16, 200000 x 256 60 in 16 and 65
+    // in 32, 80000 x 768 72 in a warp and 98 in four.  Wider rows get as many warps as their vectors
+    // fill, with 3 or 4 vectors a thread: 8000 x 8192 77 us with 4, 83 with 3 and 98 with 2; 30000 x
+    // 2056 74 with 3, 80 with 4 and 85 with 2.  Rows that do not fill the SMs take more threads each:
+    // 333 x 768 2.4 us with a vector a thread, 2.7 in a warp.
 #define LAYER_NORM_GO(sub, nv)                                                                  \
     status_of(launch(k_layer_norm<sub, nv>,                                                     \
                      dim3((unsigned)((T + Spread<sub>::kRows - 1) / Spread<sub>::kRows)),       \
@@ -694,6 +698,9 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
     };
 #define GRAD_GO(sub, nv, most) \
     run(k_layer_norm_grad<sub, nv, most>, sub, nv, most, grad_per_sm<sub, nv, most>)
+    // Up to 1024 columns as in the forward pass: 500000 x 128 takes 77 us in 8 lanes and 82 in 16,
+    // 200000 x 256 63 in 16 and 69 in 32, 80000 x 768 74 in a warp and 93 in four, 60000 x 1024 76
+    // and 90.
     if (D <= 64) return GRAD_GO(8, 1, 128);
     if (D <= 128) return GRAD_GO(8, 2, 128);
     if (D <= 192) return GRAD_GO(8, 3, 128);
