@@ -766,14 +766,15 @@ zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld, const uint16
  * tokens offsets[s] <= t < offsets[s + 1], offsets being S + 1 integers of
  * offset_bytes (4 or 8) that do not fall, from 0 or more to T or less; a sequence may
  * be empty.  Offsets that fall or lie outside set ZERO_DEV_BAD_OFFSETS in the forward call's
- * dev_status (optional) and leave the outputs unspecified (nothing outside of them is touched).  Tokens before the
- * first sequence and behind the last one are not read for a result and their dnll
- * is not written.  A token with a negative target takes part in nothing, whatever
- * its losses hold (NaN and Inf included), and its dnll is 0.
- * S and P below 2^30, T below 2^31 - 1024.  Arrays of 4-byte elements need 4-byte
- * alignment only, ids and offsets their own size.  Sums over a sequence have fp32 terms
- * and partial sums of at most 256 tokens, which are joined without loss (as two fp32 numbers).  S = 0 is allowed.
- * average = 1 divides a sequence's sum by the number of its tokens that count
+ * dev_status (optional) and leave the outputs unspecified; nothing outside of them is touched.
+ * Tokens before the first sequence and behind the last one are not read for a result and their
+ * dnll is not written.  A token with a negative target takes part in nothing, whatever
+ * its losses hold (NaN and Inf included), and its dnll is 0.  (A target past the table, which
+ * zero_xent reports, is a token like others here.)
+ * S at most 2^30, P at most 2^29, T at most 2^31 - 1024.  Arrays of 4-byte elements need 4-byte
+ * alignment only, ids and offsets their own size.  Sums over a sequence have fp32 terms and
+ * partial sums of at most 256 tokens, which are joined without loss (as two fp32 numbers).
+ * S = 0 is allowed.  average = 1 divides a sequence's sum by the number of its tokens that count
  * (0 where none does).
  * ---------------------------------------------------------------------- */
 

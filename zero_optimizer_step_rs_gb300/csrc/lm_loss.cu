@@ -11,12 +11,12 @@
 // the other, and no slot needs clearing.  The sequence's slots are then joined, with what
 // the additions round away kept beside the sum: no atomics, the same bits in every call.
 //
-// A token is 16 to 24 bytes read and 4 written in the gradient, which reads them once more
-// from L2.  Measured, one GB300, with the gradient: 2^20 tokens of 256 pairs 9.5 us, of 512
-// sequences of the policy 15.0 us (2.2 and 2.0 TB/s of what they cannot do without).  That is three
-// launches of 2 us with the time between, and in each the first loads' way; the instructions
-// fill a quarter of the issue slots (half as many of them left the policy's time as it was).  999
-// tokens of 4 pairs take 5.2 us, 1501 of 16 sequences of the policy 6.6: two launches.
+// A token is 16 to 24 bytes read and 4 written in the gradient, which reads them once more.
+// Measured, one GB300, with the gradient: 2^20 tokens of 256 pairs 9.5 us, of 512 sequences of the
+// policy 15.0 us (2.2 and 2.0 TB/s of what they cannot do without).  About 5 us of each are three
+// launches and their first loads' way; each half million tokens of the policy more takes 4.9 us,
+// 5.4 TB/s of what both passes read, with half of the issue slots full.  999 tokens of 4 pairs take
+// 5.2 us, 1501 of 16 sequences of the policy 6.6: two launches.
 #include "lm_common.cuh"
 
 #include <math.h>
