@@ -594,7 +594,8 @@ unsigned blocks_of(int64_t warps) { return (unsigned)((warps + kThreads / 32 - 1
 template <Kind K, int ITEMS>
 zero_status forward_in(const LossArgs& a, int64_t results, cudaStream_t st)
 {
-    cudaError_t e = launch(k_loss_parts<K, ITEMS>, dim3(blocks_of(a.tiles)), kThreads, 0, st, a);
+    cudaError_t e = cudaSuccess;                     // (no tokens: no parts)
+    if (a.tiles) e = launch(k_loss_parts<K, ITEMS>, dim3(blocks_of(a.tiles)), kThreads, 0, st, a);
     if (e != cudaSuccess) return status_of(e);
     // a warp takes a result unless it would have to fetch many parts (one sequence of 10^6
     // tokens: 41 us by a warp, 17 by a block)
@@ -609,7 +610,8 @@ template <Kind K>
 zero_status forward(LossArgs& a, int64_t results, cudaStream_t st)
 {
     a.tiles = (int32_t)tiles_of<K>(a.T);
-    if (a.tiles == 0 || (a.tiles <= kAloneTiles && results <= kAloneResults)) {
+    // (nor without tokens more: 2^30 results would take one block's warps ten seconds and more)
+    if (a.tiles <= kAloneTiles && results <= kAloneResults) {
         const int warps = (int)std::min<int64_t>(32, std::max<int64_t>(a.tiles, results));
         return status_of(launch(k_loss_alone<K>, dim3(1), 32 * warps, 0, st, a));
     }
