@@ -255,13 +255,16 @@ __device__ __forceinline__ void signs_of(const float (&A)[ITEMS], unsigned& pos,
 
 // Calls f(s, lo, hi, of(s)) for every sequence from s0 on that the tile at base meets, with the
 // part [base + lo, base + hi) of it that lies inside.  The bounds and of(s) of 32 sequences are
-// fetched at once, one a lane.
+// fetched at once, one a lane.  Where none of these has a token in the tile, the lanes look 2^lane
+// sequences further on and the warp goes where still none had one: what a buffer of a fixed size has
+// left over ends in one tile, and 31 at a time 2^20 empty sequences would take 34000 rounds (2^30,
+// ten seconds and more).  Offsets that fall end it.
 template <int ITEMS, typename Of, typename F>
 __device__ __forceinline__ void for_sequences(const LossArgs& a, int base, int s0, int lane,
                                               Of&& of, F&& f)
 {
     const int n = min(kTile<ITEMS>, a.T - base);
-    for (int s = max(s0, 0); s < a.S; s += 31) {
+    for (int s = max(s0, 0); s < a.S;) {
         const int64_t bound = raw_offset(a, min(s + lane, a.S));
         const int lo = bound <= base ? 0 : (int)min(bound - base, (int64_t)n);
         const float2 about = of(min(s + lane, a.S - 1));
@@ -274,7 +277,15 @@ __device__ __forceinline__ void for_sequences(const LossArgs& a, int base, int s
             f(s + k, __shfl_sync(kAll, lo, k), __shfl_sync(kAll, hi, k),
               make_float2(__shfl_sync(kAll, about.x, k), __shfl_sync(kAll, about.y, k)));
         }
-        if (__shfl_sync(kAll, lo, 31) >= n) return;
+        const int end = __shfl_sync(kAll, lo, 31);
+        if (end >= n || __any_sync(kAll, lane < 31 && lo > hi)) return;
+        s += 31;
+        if (__shfl_sync(kAll, lo, 0) == end) {
+            const unsigned far = (unsigned)s + (1u << lane);
+            const bool none = far <= (unsigned)a.S && raw_offset(a, (int)far) <= base + end;
+            const int lanes = __popc(__ballot_sync(kAll, none));
+            if (lanes) s += 1 << (lanes - 1);
+        }
     }
 }
 
@@ -517,9 +528,10 @@ __global__ void __launch_bounds__(1024) k_loss_alone(const __grid_constant__ Los
         finish<K, kFewItems, false>(a, parts, p);
 }
 
-// The gradient of each token's loss.
+// The gradient of each token's loss.  (12 blocks an SM: without the bound 4 tokens a lane take 42
+// registers, and 10 blocks fit.)
 template <Kind K, int ITEMS>
-__global__ void __launch_bounds__(kThreads) k_loss_grad(const __grid_constant__ LossArgs a)
+__global__ void __launch_bounds__(kThreads, 12) k_loss_grad(const __grid_constant__ LossArgs a)
 {
     pdl_enter();
     const int lane = threadIdx.x & 31;
