@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import zero_optimizer_step_rs_gb300 as z
+from tests import test_gpu_lm_loss as losses
 from tests.test_gpu_lm_loss import fresh, scratch_of
 
 pytestmark = pytest.mark.gpu
@@ -138,3 +139,30 @@ def test_many_offsets_that_fall(pattern, T):
     assert seconds(lambda: z.zero_policy(*args, loss, kl, clipped, counts, room, dev_status=status)) < 0.05
     assert seconds(lambda: z.zero_policy_grad(*args, counts, ones[:S], dnll)) < 0.05
     assert status.item() == z.ZERO_DEV_BAD_OFFSETS
+
+
+# Around where one block takes a call alone: 48 tiles of 32 tokens, 16 sequences.  With a token a lane
+# a tile's sum is 5 halvings deep; the parts are joined as two fp32 numbers each, whose rest is
+# off by U32 of itself: both far inside what the checks allow.
+ALONE = {
+    "32 tiles": (0, [64] * 16, 0),
+    "a second tile for one warp": (0, [64] * 15 + [65], 0),
+    "48 tiles of one sequence": (0, [1536, 0], 0),
+    "48 tiles of 16 sequences": (0, [96] * 16, 0),
+    "48 tiles cut anywhere": (5, [1, 0, 333, 31, 64, 33, 127, 0, 700, 2, 95, 1, 40, 77, 0, 20], 7),
+    "49 tiles": (0, [96] * 15 + [97], 0),
+    "18 sequences": (3, [80] * 17 + [60], 4),
+    "two halves": (0, [768, 768], 0),
+    "49 tiles of two sequences": (1, [1500, 31], 5),
+}
+
+
+@pytest.mark.parametrize("name", ALONE)
+@pytest.mark.parametrize("average", [False, True])
+def test_around_what_one_block_takes(name, average, monkeypatch):
+    monkeypatch.setitem(losses.CASES, name, ALONE[name])
+    for kind, smoothing, margin in losses.KINDS:
+        losses.test_preference(name, kind, smoothing, margin, average, True, average)
+    for per_token in (False, True):
+        losses.test_policy(name, True, True, per_token, average, average, 0.05)
+    losses.test_policy(name, False, False, False, average, True, 0.0)

@@ -35,7 +35,7 @@ constexpr int kFewItems = 1;
 constexpr int many_items(int kind) { return kind == 0 ? 8 : 4; }
 constexpr int64_t kFew = 1 << 16;                    // tokens from which on a lane takes several
 constexpr int kThreads = 128;
-constexpr int kAloneTiles = 48, kAloneResults = 16;  // the most that one block takes alone
+constexpr int kAloneTiles = 48, kAloneSequences = 16;    // the most that one block takes alone
 constexpr int kWideThreads = 512;                    // of a block that joins one result's parts
 constexpr int64_t kWideTiles = 128;                  // parts a result from which on it does
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -511,15 +511,24 @@ __global__ void __launch_bounds__(WIDE ? kWideThreads : kThreads)
     if (p < (K == kPreference ? a.S / 2 : a.S)) finish<K, ITEMS, WIDE>(a, a.parts, p);
 }
 
-// Few tokens: one block does both, and the parts stay in its shared memory.  With their gradient
-// 999 tokens of 4 pairs take 5.2 us (5.6 in two launches), 200 of 4 sequences of the policy 4.6
-// (5.3), 1501 of 16 sequences 6.6 (5.5, but the launches take the host 7.8, and 6.3 with one
-// less); 2000 tokens 7.4 (5.8), 900 of 60 sequences 9.1 (6.8).
+// Few tokens: one block does both, and the parts stay in its shared memory.  Calls this small keep
+// the host longer than the GPU (about 5.1 us with the gradient, 6.7 with a launch more), so the limits are
+// where a call with its gradient, one behind the other from the host, takes as long in either
+// form.  us in one block / in two launches, in brackets the same in a graph, where the host's time
+// does not count and up to 32 tiles, one a warp, are the limit:
+//   policy, sequences     1000 tokens             1536                    1750           2048
+//      4            5.2 / 6.8 (4.9, 4.9)   6.0 / 6.9 (5.7, 4.9)   6.2 / 6.9        6.4 / 7.0
+//     16            6.0 / 6.8 (5.7, 5.4)   6.9 / 6.9 (6.6, 5.4)   7.0 / 6.7        7.2 / 7.1
+//   preferences, pairs    1000                    1536
+//      4            5.7 / 6.6 (5.4, 5.8)   6.3 / 6.6 (6.0, 5.7)
+//      8            5.8 / 6.2 (5.6, 5.7)   at 1100: 6.2 / 6.2 (6.0, 5.6)
+//     12            6.4 / 6.1 (6.2, 5.7)   at 200:  6.6 / 6.8 (6.4, 6.4)
+//     16            7.4 / 6.7 (7.1, 6.2)   at 200:  7.7 / 7.6 (7.4, 7.2)
 template <Kind K>
 __global__ void __launch_bounds__(1024) k_loss_alone(const __grid_constant__ LossArgs a)
 {
     pdl_enter();
-    __shared__ Part parts[kAloneTiles + 2 * kAloneResults];
+    __shared__ Part parts[kAloneTiles + kAloneSequences];
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5;
     for (int tile = warp; tile < a.tiles; tile += warps)
         tile_parts<K, kFewItems>(a, parts, tile, threadIdx.x & 31);
@@ -623,7 +632,7 @@ zero_status forward(LossArgs& a, int64_t results, cudaStream_t st)
 {
     a.tiles = (int32_t)tiles_of<K>(a.T);
     // (nor without tokens more: 2^30 results would take one block's warps ten seconds and more)
-    if (a.tiles <= kAloneTiles && results <= kAloneResults) {
+    if (a.tiles <= kAloneTiles && a.S <= kAloneSequences) {
         const int warps = (int)std::min<int64_t>(32, std::max<int64_t>(a.tiles, results));
         return status_of(launch(k_loss_alone<K>, dim3(1), 32 * warps, 0, st, a));
     }
