@@ -773,7 +773,8 @@ zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld, const uint16
  * zero_xent reports, is a token like others here.)
  * S at most 2^30, P at most 2^29, T at most 2^31 - 1024.  Arrays of 4-byte elements need 4-byte
  * alignment only, ids and offsets their own size.  Sums over a sequence have fp32 terms and
- * partial sums of at most 256 tokens, which are joined without loss (as two fp32 numbers).
+ * partial sums of at most 256 tokens, which are joined as two fp32 numbers: the second is the
+ * sum, itself rounded, of what the first one's additions round away.
  * S = 0 is allowed.  average = 1 divides a sequence's sum by the number of its tokens that count
  * (0 where none does).
  * ---------------------------------------------------------------------- */
@@ -868,9 +869,11 @@ int64_t zero_grad_norm_scratch_bytes(int32_t count);
 /*
  * norms[i] = the 2-norm of tensor i (may be NULL), norm[0] = that of all of them.  The
  * squares are added in fp32 within a block, the blocks' sums in 64 bits, in an order
- * that the sizes alone decide; a part whose sum of squares overflows or vanishes in
+ * that the tensors' sizes and types and their addresses modulo 16 decide: equal tensors that
+ * lie otherwise to 16 bytes may give a norm with other last bits (replicas that have to clip alike
+ * lie alike, or share one norm).  A part whose sum of squares overflows or vanishes in
  * fp32 is taken again relative to its largest value, so that every finite
- * input has the norm that fp32 can hold.  A norm that is not finite sets
+ * input has the norm that fp32 can hold; a part of zeros alone is read twice for it.  A norm that is not finite sets
  * ZERO_DEV_NONFINITE.  `tensors` is a host array that is read during the call; count at most
  * ZERO_MAX_TENSORS, 0 gives norm 0; at most 2^40 elements a tensor and 2^43 together.
  */

@@ -8,7 +8,8 @@
 // block takes a run of consecutive tiles.  Going along the tiles either the block
 // or the tensor steps on, so block + tensor is a slot of its own for every pair that
 // meets, the slots of a tensor lie one behind the other, and no slot needs
-// clearing.  The table of tensors goes into the launch's arguments: nothing is copied to the
+// clearing.  A tensor's tiles begin at its first 16-byte boundary, so that the order of the
+// additions depends on the addresses modulo 16 too.  The table of tensors goes into the launch's arguments: nothing is copied to the
 // device, and a captured graph holds it.
 //
 // Bound by HBM: the norm reads every element once, the clipping once more and writes it, since
@@ -278,7 +279,9 @@ __device__ __forceinline__ double sum_squares(const void* p, int64_t numel, int 
 {
     const float s =
         block_sum(thread_squares<TYPE, false>(p, numel, head, lo, hi, 1.0f, 1.0f));
-    // (each of the sum's terms was off by at most 2^-150: under 2^-24 of it from here up)
+    // (each of the sum's terms was off by at most 2^-150: under 2^-24 of it from here up; a sum of 0
+    // may be of zeros or of values whose squares vanish, so a run of zeros is read twice: 2^30 bf16
+    // elements 309 us, 605 if all are 0, of fp32 594 and 1180)
     if (s >= 0x1p-80f && s <= 0x1p120f) return (double)s;
     return scaled_sum<TYPE>(p, numel, head, lo, hi);
 }
