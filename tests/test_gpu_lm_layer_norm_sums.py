@@ -47,3 +47,26 @@ def test_every_row_is_in_the_sums(T, D, extra):
             if terms[t].any() and D >= 64:
                 less = (total - terms[t]).float().to(torch.bfloat16)
                 assert not torch.equal(got, less)
+
+
+@pytest.mark.parametrize("T,D", [(3000, 2040), (5000, 1080), (3000, 4024), (3000, 2048), (40_000, 120)])
+def test_the_sums_do_not_depend_on_the_rows_padding(T, D):
+    """The same bits whatever the strides are, multiples of a cache line (64 elements) or not.  Each
+    row comes back with the other sign, so that all that is left of the sums is what their order
+    rounds away."""
+    g = R.gen(D)
+    dy = R.bf16(g, (T // 2, D)) * torch.randn((T // 2, 1), generator=g, device="cuda").mul(3).exp().to(torch.bfloat16)
+    x, w = R.bf16(g, (T // 2, D)), R.bf16(g, (D,))
+    back = torch.randperm(T // 2, generator=g, device="cuda")
+    dy, x = torch.cat([dy, -dy[back]]), torch.cat([x, x[back]])
+    mean, rstd = torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")
+    want = None
+    for extra in (0, 8, 64 - D % 64, 128 - D % 64 + 24):
+        rows = [R.strided(t, extra) if extra else t for t in (dy, x, torch.zeros_like(x))]
+        dw, db = (torch.empty(D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        scratch = torch.empty(z.zero_layer_norm_grad_scratch_bytes(T, D), dtype=torch.uint8, device="cuda")
+        z.zero_layer_norm_grad(rows[0], rows[1], mean, rstd, w, rows[2], dw, db, scratch)
+        got = (rows[2].clone(), dw, db)
+        want = want or got
+        assert dw.any()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), extra

@@ -450,7 +450,8 @@ __global__ void __launch_bounds__(SUB ? 128 : MOST, grad_blocks_min(SUB, NV, MOS
     }
 }
 
-// dw and db = the blocks' parts, added in an order that depends on their number only:
+// dw and db = the blocks' parts, added in an order that depends on their number only (so T, D and
+// the GPU's number of SMs decide the order of all additions):
 // 32 of the 2 D columns a block, 128 shares of the rows; four shares lie in a warp's
 // lanes, the 32 warps' sums are added by the first one.
 constexpr int kJoinThreads = 1024;
@@ -688,8 +689,9 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
                                            (int64_t)std::max(1, fit) * device_sms()});
         // Rows of a block at a time: few are spread over all blocks; of many those that share the
         // cache line between them go to one block (30000 x 2056 90 us spread, 85 near;
-        // 32768 x 2048 80 and 82)
-        a.near = T > 4 * (int64_t)a.blocks * a.groups && (dy_ld | x_ld | dx_ld) % 64 != 0;
+        // 32768 x 2048 80 and 82).  By the width, not by the strides: which rows' sums are added first
+        // would else depend on the rows' padding, and with it the last bits of dw and db.
+        a.near = T > 4 * (int64_t)a.blocks * a.groups && D % 64 != 0;
         if (e == cudaSuccess) e = launch(kernel, dim3((unsigned)a.blocks), threads, smem, st, a);
         if (e == cudaSuccess && wanted)
             e = launch(k_layer_norm_join, dim3((unsigned)((2 * D + kJoinCols - 1) / kJoinCols)),
