@@ -37,7 +37,9 @@ constexpr int kTile = 8192;
 // us with 8 for the clipping and 1787 with 4.
 constexpr int kNormBlocks = 608, kClipBlocks = 1216;
 constexpr int kJoinThreads = 128;
-constexpr int kNoVectors = 255;                      // a head: input and output never have one together
+// A head: input and output have no boundary together, and go an element at a time (2^30 elements, fp32
+// into bf16 3.38 ms instead of 0.95, bf16 3.33 instead of 0.64).
+constexpr int kNoVectors = 255;
 constexpr int64_t kMaxNumel = 1ll << 40, kMaxTotal = 1ll << 43;
 
 struct Entry {
@@ -52,7 +54,8 @@ struct Entry {
 
 // Entries of a launch: 2, 8, 30 KB of arguments.  A few hundred launches of 30 KB fill the queue, and
 // the host waits for the GPU (146 tensors: 6.5 us a call of the norm in 8 KB, 200 in 30, behind a long
-// kernel).
+// kernel).  Without one a call of 256 tensors takes the host 8.2 us and the GPU 5.2, of 290 10.5 and
+// 5.1, of 960 19.9 and 9.2.
 constexpr int kFew = 64, kSome = 256, kMany = 960;
 
 template <int N>

@@ -716,6 +716,9 @@ extern "C" zero_status zero_layer_norm_grad(const uint16_t* dy, int64_t dy_ld,
     // elsewhere, 2048 columns 83 with 2 and 91 with 4, 2056 columns 84 with 2 and 92 with 3)
     if (D <= 8192 && 16 / warps_of(D, 2) == 1 && 12 / warps_of(D, 3) > 1) return GRAD_GO(0, 3, 384);
     if (D <= 8192) return GRAD_GO(0, 2, 512);
+    // Beyond, a row of 2 vectors a thread takes 1024 threads, which leave 64 registers: the sums of dw
+    // and db alone are 32, and the loop spills (364 bytes a thread).  8000 x 8200 takes 225 us (2.3
+    // TB/s; 8000 x 8192 81), 6000 x 12000 207, 4000 x 16384 174 (3.0 TB/s).
     return GRAD_GO(0, 2, 1024);
 #undef GRAD_GO
 }

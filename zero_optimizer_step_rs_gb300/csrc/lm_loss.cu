@@ -29,8 +29,14 @@ using namespace lm;
 // other, several us of a call of few tokens; with 1 it does less work per instruction (the
 // search for its sequences, the sums' halvings), which costs where there are many: 2^20 tokens
 // of the policy 15.8 us with 4 and 16.2 with 8, of preferences 11.0 and 9.7; 30000 of the policy
-// 6.8 us with 1 and 7.5 with 2; 80000 of it 7.1 with 1 and 8.5 with 4, of preferences 8.4 and 7.4
-// (with 8).
+// 6.8 us with 1 and 7.5 with 2.
+//
+// The limit between few and many is the same for both kinds.  Batches of even lengths of the policy
+// would take 1 for longer (of 512 sequences, 1 / 4 a lane: 65535 tokens 7.5 / 10.5 us, 200000 9.0 /
+// 10.3, 300000 10.6 / 10.7), but where one sequence has most of the tokens its join has four times as
+// many parts (the others 4 tokens each: 65535 25 / 33, 100000 35 / 34, 200000 62 / 42).
+// Preferences, 1 / 8 a lane: 65535 tokens of 512 sequences 7.3 / 8.3, of 16 7.1 / 6.6, 200000 9.1 /
+// 8.8 and 9.3 / 9.1; with one long sequence 65535 13 / 24, 200000 24 / 26.
 constexpr int kFewItems = 1;
 constexpr int many_items(int kind) { return kind == 0 ? 8 : 4; }
 constexpr int64_t kFew = 1 << 16;                    // tokens from which on a lane takes several
@@ -624,7 +630,9 @@ zero_status forward_in(const LossArgs& a, int64_t results, cudaStream_t st)
     if (a.tiles) e = launch(k_loss_parts<K, ITEMS>, dim3(blocks_of(a.tiles)), kThreads, 0, st, a);
     if (e != cudaSuccess) return status_of(e);
     // a warp takes a result unless it would have to fetch many parts (one sequence of 10^6
-    // tokens: 41 us by a warp, 17 by a block)
+    // tokens: 41 us by a warp, 17 by a block).  The host knows only their mean: where one of 502
+    // sequences has all but 2000 of 2^20 tokens, a warp joins its 8192 parts, and a call of the policy
+    // with its gradient takes 106 us (even lengths 17), of preferences 37 (11).
     return status_of(a.tiles >= kWideTiles * results
                          ? launch(k_loss_join<K, ITEMS, true>, dim3((unsigned)results),
                                   kWideThreads, 0, st, a)
